@@ -312,6 +312,11 @@ def _exponent(a):
     return torch.where(a > 0, e - 7 + (m > 127 / 128).to(e.dtype), -50).clamp(-50, 50)
 
 
+def _power(e):
+    """2^e in fp32, by its bits: a power function may be a step off."""
+    return ((e.to(torch.int32) + 127) << 23).view(torch.float32)
+
+
 def _summarise(s, pages, held):
     """Summaries of the pages from their first `held` tokens."""
     k = _take(s["k"], pages).float()
@@ -320,7 +325,7 @@ def _summarise(s, pages, held):
     here = (torch.arange(k.shape[2], device="cuda")[None, :] < held[:, None])[:, None, :, None]
     high, low = torch.where(here, k, -math.inf).amax(2), torch.where(here, k, math.inf).amin(2)
     e = _exponent(torch.maximum(high.abs(), low.abs()).amax(2))
-    scale = torch.ldexp(torch.ones_like(high[..., :1]), e[..., None])
+    scale = _power(e)[..., None]
     s["summary"][pages] = torch.stack([(high / scale).ceil(), (low / scale).floor()], 2).clamp(-127, 127).to(torch.int8)
     s["summary_scale"][pages] = scale[..., 0]
 
@@ -363,7 +368,7 @@ def _sparse(s):
     table, n = s["table"].long(), s["lens"].long()
     q = s["q"].reshape(b, hk, -1, d).float()
     e = _exponent(q.abs().amax(-1))
-    scale = torch.ldexp(torch.ones_like(q[..., 0]), e)
+    scale = _power(e)
     x = (q / scale[..., None]).round().clamp(-127, 127)
     x = torch.cat([x.clamp(min=0), x.clamp(max=0)], -1)  # [b, hk, g, 2d]
     summary = s["summary"][table].permute(0, 2, 1, 3, 4).flatten(3).float()  # [b, hk, pages, 2d]
@@ -486,10 +491,11 @@ def _exact_pages(case, s, b, row):
     q = s["q"][b].double().unflatten(0, (hk, -1))
     top = q.abs().amax(-1, keepdim=True)
     f = torch.ceil(torch.log2(top / 127) - 1e-9).clamp(-50, 50)  # bf16 tops lie far from the borders
-    x = torch.round(q / 2 ** f).clamp(-127, 127)
+    f = ((f.long() + 1023) << 52).view(torch.float64)  # 2^f
+    x = torch.round(q / f).clamp(-127, 127)
     high, low = s["summary"][row].double().unbind(2)  # [pages, hk, d]
     score = torch.einsum("hgc,phc->hgp", x.clamp(min=0), high) + torch.einsum("hgc,phc->hgp", x.clamp(max=0), low)
-    score = (score * 2 ** f * s["summary_scale"][row].double().T[:, None]).amax(1)
+    score = (score * f * s["summary_scale"][row].double().T[:, None]).amax(1)
     score[:, :case["first"]] = math.inf
     score[:, many - case["last"]:] = math.inf
     order = torch.argsort(-score, dim=1, stable=True)[:, :case["keep"]]
