@@ -283,6 +283,156 @@ CM_API int cm_attn_bwd_noalloc(const cm_descriptor* desc, const void* q, const v
                                void* dq, void* dk, void* dv, int B, int H, int S, int d,
                                float scale, void* stream);
 
+/* ---- serving: a paged key-value cache (no counterpart in the paper) ------------------------- */
+
+/* Generated tokens, one at a time: their keys and values go into a cache made of pages
+ * (cm_kv_append), and each new token attends to the cache (cm_attn_decode), under the mask of the
+ * prompt's descriptor where one is given, or to pages that a cheap score selects for it
+ * (cm_select_pages).  Beside the conventions above:
+ *   - "lens" is the number of tokens a sequence holds; token p of sequence b is row
+ *     p % page_size of page page_table[b][p / page_size].
+ *   - Index arrays are read on the device, so a captured graph can be replayed with new lengths
+ *     and page tables.  Values that would lead out of bounds (a page number outside
+ *     [0, num_pages), a length beyond the table) are not followed: the kernel records
+ *     CM_ERR_DEVICE_CHECK in the cache's status word and skips what they name, as each entry
+ *     point says.
+ *   - Keys past a sequence's length, and keys that a mask hides, are never used: whatever their
+ *     memory holds (NaN and infinities too) does not reach an output. */
+
+#define CM_KV_BF16 0
+#define CM_KV_E4M3 1
+
+/* The cache.  All pointers are device memory of the caller, 16-byte aligned but the scales, the
+ * summary scales and the status word (4 bytes).
+ *   k, v         [num_pages][H_kv][page_size][d] of the type `dtype` names: bf16, or e4m3 with one
+ *                positive fp32 scale per head (value = stored * scale).  Pages may lie apart:
+ *                page n starts at n * k_page_stride (v_page_stride) elements, a multiple of 16
+ *                bytes and at least H_kv * page_size * d.
+ *   k_scale, v_scale  fp32 [H_kv]; e4m3 only, NULL for bf16.
+ *   summary      int8 [num_pages][H_kv][2][d] and summary_scale fp32 [num_pages][H_kv], both or
+ *                neither (NULL): per page, head and channel the largest key, then the smallest,
+ *                over the tokens the page holds, in units of summary_scale.  With a = the largest
+ *                magnitude of any channel's two, summary_scale is the smallest power of two 2^e
+ *                with a <= 127 * 2^e, e held to [-50, 50]; the largest keys are rounded up, the
+ *                smallest down, and held to [-127, 127].  NaN keys are passed over.
+ *                Maintained by cm_kv_append, read by cm_select_pages.
+ *   status       int32: 0, or the first device error; zeroed by the caller when it makes the
+ *                cache, read and zeroed by cm_kv_status.
+ * page_size is 16, 32, 64 or 128; d 64 or 128; H_kv at most 1024; num_pages * H_kv * page_size
+ * below 2^40. */
+typedef struct cm_kv_cache {
+  int32_t num_pages, page_size, H_kv, d, dtype;
+  int64_t k_page_stride, v_page_stride;
+  void* k;
+  void* v;
+  const float* k_scale;
+  const float* v_scale;
+  int8_t* summary;
+  float* summary_scale;
+  int32_t* status;
+} cm_kv_cache;
+
+/* The sequences of a call: page_table device int32 [B][max_pages], lens device int32 [B].
+ * Entries of the table past a sequence's tokens are never read.  B at most 32767; max_pages *
+ * page_size at most 2^27. */
+typedef struct cm_kv_seqs {
+  int32_t B, max_pages;
+  const int32_t* page_table;
+  const int32_t* lens;
+} cm_kv_seqs;
+
+/* New tokens of cm_kv_append: bf16 tensors whose last axis (d) is contiguous, with strides in
+ * elements for {sequence, head, token}, each a multiple of 8.
+ *   k, v    H_kv heads; q (may be NULL) H_q heads, rotated into q_out; k_out (may be NULL) receives
+ *           the rotated keys.  q_out may be q, and k_out k, with the same strides; otherwise
+ *           outputs overlap nothing else.
+ *   cu_new  packed tokens: device int32 [B + 1], sequence b's are tokens cu_new[b] .. cu_new[b+1]-1
+ *           of n_tokens (the sequence strides are not used).  NULL: padded tokens, sequence b's
+ *           are tokens 0 .. n_new[b]-1 of n_tokens; n_new (device int32 [B]) NULL: all n_tokens.
+ *   max_new the most tokens any sequence appends in this call (host), at most n_tokens.
+ *   rope    fp32 [rope_len][rot_dim / 2][2]: cosine and sine of each position's angles.  The first
+ *           rot_dim channels (a multiple of 16, at most d; 0: no rotation, rope NULL) are rotated
+ *           in pairs (i, i + rot_dim / 2), or (2i, 2i + 1) if interleaved:
+ *           (x, y) -> (x cos - y sin, y cos + x sin), every product and sum rounded to fp32 once.
+ *   new_lens device int32 [B] (may be NULL, not lens): receives lens[b] + the tokens appended. */
+typedef struct cm_kv_new {
+  const void* k;
+  const void* v;
+  const void* q;
+  void* q_out;
+  void* k_out;
+  int64_t k_stride[3], v_stride[3], q_stride[3], q_out_stride[3], k_out_stride[3];
+  const int32_t* cu_new;
+  const int32_t* n_new;
+  int32_t n_tokens, max_new, H_q;
+  int32_t rot_dim, interleaved, rope_len;
+  const float* rope;
+  int32_t* new_lens;
+} cm_kv_new;
+
+/* Append: token i of sequence b gets position p = lens[b] + i; its key and query are rotated to p
+ * and rounded to bf16, its key and value stored in the cache (e4m3: the bf16 value divided by the
+ * head's scale, rounded to nearest, held to +-448), and the summaries of the pages it touches
+ * are made anew from all the tokens these then hold.  lens is read only.
+ * A sequence whose length or token count is out of range (lens[b] < 0, more than max_new tokens,
+ * tokens outside n_tokens, positions past the table or rope_len) appends nothing (new_lens[b] =
+ * lens[b]), and tokens of a page outside the pool are left out (their q_out and k_out are written);
+ * both record CM_ERR_DEVICE_CHECK.  Tokens of no sequence, and their outputs, are left alone.
+ * Sequences must not append to a page they share. */
+CM_API int cm_kv_append(const cm_kv_cache* cache, const cm_kv_seqs* seqs, const cm_kv_new* tok,
+                        void* stream);
+
+/* Workspace bytes of cm_attn_decode (device, 16-byte aligned, contents irrelevant before and
+ * after the call; calls whose work may overlap need one each). */
+CM_API int cm_attn_decode_workspace_size(int B, int H_q, int H_kv, int d, size_t* bytes);
+
+/* Attention of one new token per sequence, the last of its lens[b] tokens:
+ * o[b][h] = softmax_j(scale * q[b][h] . k[j]) v[j] over the visible j < lens[b], of key-value head
+ * h / (H_q / H_kv).  q, o: bf16 [B][H_q][d] with strides in elements for {sequence, head}, multiples
+ * of 8; lse: fp32 [B][H_q] in natural log, or NULL.  H_q is a multiple of H_kv.
+ *   desc  NULL: every token is visible.  Else a descriptor of B samples with S >= lens[b] in the
+ *         CM_FORM_VISIBLE form: the token sees what row lens[b] - 1 of the forward half says, cut
+ *         at lens[b].  One built for the prompt's MaskSpec with room for the tokens to come (the
+ *         last segment ending at S) serves the prompt and every token after it.
+ *   sel   NULL, or device int32 [B][H_kv][sel_max] with nsel device int32 [B][H_kv]: only the pages
+ *         sel[b][g][0 .. nsel[b][g]-1] (places in the sequence's table, ascending) are attended to.
+ *         Not together with desc.
+ * A row with no visible key gets o = 0 and lse = -inf.  So does a sequence whose length is below 0,
+ * beyond the table or beyond desc->S (with CM_ERR_DEVICE_CHECK); a page outside the pool, or a
+ * selected page that is out of order or past the sequence, is skipped (same).
+ * The sums of a row are split over the keys in a way that depends on all the batch's lengths; the
+ * same call gives the same bits every time. */
+CM_API int cm_attn_decode(const cm_kv_cache* cache, const cm_kv_seqs* seqs,
+                          const cm_descriptor* desc, const int32_t* sel, const int32_t* nsel,
+                          int sel_max, const void* q, const int64_t q_stride[2], void* o,
+                          const int64_t o_stride[2], float* lse, int H_q, float scale,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of cm_select_pages (rules as for cm_attn_decode's). */
+CM_API int cm_select_pages_workspace_size(int B, int H_kv, int max_pages, size_t* bytes);
+
+/* For every sequence and key-value head, the sel_max pages whose summaries promise the largest
+ * scores for the new token's queries.  With f from the largest |q| of a query head as e is from a
+ * page's keys, x = rint(q / 2^f) (halves to even, held to [-127, 127]) and
+ *   score(page) = max over the group's query heads of
+ *                 2^(e + f) * sum_c (x_c > 0 ? x_c * largest_c : x_c * smallest_c),
+ * which is exact: whole numbers, scaled by powers of two.  The first keep_first and the last
+ * keep_last pages of the sequence come before all others (keep_first + keep_last <= sel_max); the
+ * rest by score, the lowest page first among equals.  sel [B][H_kv][sel_max] receives them in
+ * ascending order, -1 behind the last, nsel [B][H_kv] their number: all pages of a sequence that
+ * holds no more than sel_max.  q as in cm_attn_decode; a summary of a page outside the pool
+ * counts as the lowest score, a length out of range selects nothing (both with
+ * CM_ERR_DEVICE_CHECK).  sel_max at most 8192; max_pages at most 32768. */
+CM_API int cm_select_pages(const cm_kv_cache* cache, const cm_kv_seqs* seqs, const void* q,
+                           const int64_t q_stride[2], int H_q, int keep_first, int keep_last,
+                           int32_t* sel, int32_t* nsel, int sel_max, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* Wait for `stream`, then read the cache's status word and zero it: CM_OK or the first error
+ * recorded since it was last zeroed (CM_ERR_DEVICE_CHECK, CM_ERR_TIMEOUT; CM_ERR_CUDA if the wait
+ * or a copy itself failed). */
+CM_API int cm_kv_status(const cm_kv_cache* cache, void* stream);
+
 /* ---- status --------------------------------------------------------------------------------- */
 
 /* Wait for `stream`, then read desc->status: CM_OK, CM_ERR_TIMEOUT, CM_ERR_DEVICE_CHECK or

@@ -47,6 +47,37 @@ class cm_descriptor(ctypes.Structure):
                 ("status", ctypes.c_void_p)]
 
 
+class cm_kv_cache(ctypes.Structure):
+    _fields_ = [("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("H_kv", ctypes.c_int32), ("d", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("k_page_stride", ctypes.c_int64), ("v_page_stride", ctypes.c_int64),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("summary", ctypes.c_void_p), ("summary_scale", ctypes.c_void_p),
+                ("status", ctypes.c_void_p)]
+
+
+class cm_kv_seqs(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("page_table", ctypes.c_void_p), ("lens", ctypes.c_void_p)]
+
+
+_Strides2 = ctypes.c_int64 * 2
+_Strides3 = ctypes.c_int64 * 3
+
+
+class cm_kv_new(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("q", ctypes.c_void_p),
+                ("q_out", ctypes.c_void_p), ("k_out", ctypes.c_void_p),
+                ("k_stride", _Strides3), ("v_stride", _Strides3), ("q_stride", _Strides3),
+                ("q_out_stride", _Strides3), ("k_out_stride", _Strides3),
+                ("cu_new", ctypes.c_void_p), ("n_new", ctypes.c_void_p),
+                ("n_tokens", ctypes.c_int32), ("max_new", ctypes.c_int32),
+                ("H_q", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("rope_len", ctypes.c_int32),
+                ("rope", ctypes.c_void_p), ("new_lens", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -87,6 +118,16 @@ def lib() -> ctypes.CDLL:
         L.cm_attn_bwd_noalloc.argtypes = [ctypes.POINTER(cm_descriptor), vp, vp, vp, vp, vp, vp,
                                           vp, vp, vp, i32, i32, i32, i32, ctypes.c_float, vp]
         L.cm_get_status.argtypes = [ctypes.POINTER(cm_descriptor), vp]
+        cache_p, seqs_p = ctypes.POINTER(cm_kv_cache), ctypes.POINTER(cm_kv_seqs)
+        i64_p, size_p = ctypes.POINTER(ctypes.c_int64), ctypes.POINTER(sz)
+        L.cm_kv_append.argtypes = [cache_p, seqs_p, ctypes.POINTER(cm_kv_new), vp]
+        L.cm_attn_decode_workspace_size.argtypes = [i32, i32, i32, i32, size_p]
+        L.cm_attn_decode.argtypes = [cache_p, seqs_p, ctypes.POINTER(cm_descriptor), vp, vp, i32,
+                                     vp, i64_p, vp, i64_p, vp, i32, ctypes.c_float, vp, sz, vp]
+        L.cm_select_pages_workspace_size.argtypes = [i32, i32, i32, size_p]
+        L.cm_select_pages.argtypes = [cache_p, seqs_p, vp, i64_p, i32, i32, i32, vp, vp, i32,
+                                      vp, sz, vp]
+        L.cm_kv_status.argtypes = [cache_p, vp]
         L.cm_error_string.argtypes = [i32]
         L.cm_error_string.restype = ctypes.c_char_p
         _lib = L
@@ -416,3 +457,280 @@ def attention_backward(desc: Descriptor, q, k, v, o, lse, d_o, scale=None, strea
                                 device=q.device)
     cm_attn_bwd(desc, q, k, v, o, lse, d_o, dq, dk, dv, workspace, scale, stream)
     return dq, dk, dv
+
+
+# ------------------------------------------------------------------------------------------------
+# serving: a paged key-value cache
+# ------------------------------------------------------------------------------------------------
+CM_KV_BF16 = 0
+CM_KV_E4M3 = 1
+
+
+def _pool(t: torch.Tensor, name: str):
+    if not (t.is_cuda and t.dim() == 4 and t.dtype in (torch.bfloat16, torch.float8_e4m3fn)):
+        raise ValueError(f"{name} must be a bf16 or float8_e4m3fn CUDA tensor "
+                         "[num_pages, H_kv, page_size, d]")
+    n, H, P, d = t.shape
+    if t[:1].is_contiguous() and (n == 1 or t.stride(0) >= H * P * d):
+        return t.shape, (t.stride(0) if n > 1 else H * P * d)
+    raise ValueError(f"{name}: every page must be contiguous, and pages must not overlap")
+
+
+class KVCache:
+    """A paged key-value cache over the caller's tensors (cm_kv_cache): k, v
+    [num_pages, H_kv, page_size, d], bf16 or float8_e4m3fn; e4m3 takes k_scale and v_scale, fp32
+    [H_kv].  Pages may lie apart (a view such as kv[:, 0] of a [num_pages, 2, H_kv, page_size, d]
+    tensor).  summary (int8 [num_pages, H_kv, 2, d]) with summary_scale (fp32 [num_pages, H_kv])
+    holds the page summaries that cm_select_pages reads."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale=None, v_scale=None, summary=None,
+                 summary_scale=None):
+        shape, k_stride = _pool(k, "k")
+        v_shape, v_stride = _pool(v, "v")
+        if v_shape != shape or v.dtype != k.dtype or v.device != k.device:
+            raise ValueError("v must have the shape, type and device of k")
+        n, H, P, d = shape
+        e4m3 = k.dtype == torch.float8_e4m3fn
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if (t is not None) != e4m3:
+                raise ValueError("an e4m3 cache takes k_scale and v_scale, a bf16 cache neither")
+            if e4m3:
+                _kv_tensor(t, name, torch.float32, (H,), k.device)
+        if (summary is None) != (summary_scale is None):
+            raise ValueError("summary and summary_scale come together")
+        if summary is not None:
+            _kv_tensor(summary, "summary", torch.int8, (n, H, 2, d), k.device)
+            _kv_tensor(summary_scale, "summary_scale", torch.float32, (n, H), k.device)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.summary, self.summary_scale = summary, summary_scale
+        self.num_pages, self.H_kv, self.page_size, self.d = n, H, P, d
+        self.device = k.device
+        self.status = torch.zeros(1, dtype=torch.int32, device=k.device)
+        self.c = cm_kv_cache(n, P, H, d, CM_KV_E4M3 if e4m3 else CM_KV_BF16, k_stride, v_stride,
+                             k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale),
+                             _ptr(summary), _ptr(summary_scale), self.status.data_ptr())
+        self._ref = ctypes.byref(self.c)
+
+    @classmethod
+    def alloc(cls, num_pages: int, H_kv: int, page_size: int, d: int, dtype=torch.bfloat16,
+              device="cuda", k_scale=None, v_scale=None, summaries: bool = False) -> "KVCache":
+        """A cache in new memory (not initialised: what no token was written to is never used)."""
+        k, v = (torch.empty(num_pages, H_kv, page_size, d, dtype=dtype, device=device)
+                for _ in range(2))
+        more = {}
+        if summaries:
+            more = {"summary": torch.empty(num_pages, H_kv, 2, d, dtype=torch.int8, device=device),
+                    "summary_scale": torch.empty(num_pages, H_kv, device=device)}
+        return cls(k, v, k_scale, v_scale, **more)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _kv_tensor(t, name, dtype, shape, device):
+    if not (t.dtype == dtype and t.shape == shape and t.device == device and t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on {device}")
+
+
+def _kv_seqs(cache: KVCache, page_table, lens) -> cm_kv_seqs:
+    dev = cache.device
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"the cache is on {dev}, which is not the current device")
+    if not (page_table.dim() == 2 and page_table.dtype == torch.int32
+            and page_table.device == dev and page_table.is_contiguous()):
+        raise ValueError(f"page_table must be a contiguous int32 tensor [B, max_pages] on {dev}")
+    B, n = page_table.shape
+    _kv_tensor(lens, "lens", torch.int32, (B,), dev)
+    return cm_kv_seqs(B, n, page_table.data_ptr(), lens.data_ptr())
+
+
+def _tokens(t, name, cache: KVCache, packed: bool):
+    """Strides {sequence, head, token} of new tokens: packed [n, H, d] or padded [B, H, T, d]."""
+    if not (t.dtype == torch.bfloat16 and t.device == cache.device
+            and t.dim() == (3 if packed else 4) and t.shape[-1] == cache.d
+            and t.stride(-1) == 1):
+        raise ValueError(f"{name} must be a bf16 tensor " +
+                         ("[n, H, d]" if packed else "[B, H, T, d]") +
+                         f" on {cache.device} with d = {cache.d} contiguous")
+    s = [x if n > 1 else 0 for x, n in zip(t.stride(), t.shape)]  # one row: any stride will do
+    return (0, s[1], s[0]) if packed else s[:3]
+
+
+def cm_kv_append(cache: KVCache, page_table, lens, k, v, q=None, q_out=None, k_out=None, rope=None,
+                 interleaved: bool = False, cu_new=None, n_new=None, max_new: int | None = None,
+                 new_lens=None, stream=None) -> None:
+    """Store the new tokens' keys and values behind the lens[b] tokens that each sequence holds,
+    rotating keys (and queries, into q_out) to their positions.  With cu_new (int32 [B + 1]) the
+    tokens are packed, k, v [n, H_kv, d] and q [n, H_q, d]; without it they are padded, [B, H, T, d],
+    and n_new (int32 [B]) says how many of T each sequence has (all of them where it is not given).
+    max_new: the most tokens of any sequence (default: as many as the tensors hold).  rope: fp32
+    [positions, rot_dim / 2, 2] of cosines and sines.  new_lens (int32 [B]) receives the new
+    lengths."""
+    seqs = _kv_seqs(cache, page_table, lens)
+    dev, packed = cache.device, cu_new is not None
+    t = cm_kv_new()
+    t.k_stride[:] = _tokens(k, "k", cache, packed)
+    t.v_stride[:] = _tokens(v, "v", cache, packed)
+    shape = k.shape
+    if shape[1] != cache.H_kv or v.shape != shape or not (packed or shape[0] == seqs.B):
+        raise ValueError("k and v must have the cache's heads, one shape and one row a sequence")
+    n = shape[0] if packed else shape[2]
+    t.k, t.v = k.data_ptr(), v.data_ptr()
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out come together")
+    if q is not None:
+        t.q_stride[:] = _tokens(q, "q", cache, packed)
+        t.q_out_stride[:] = _tokens(q_out, "q_out", cache, packed)
+        if q.shape != q_out.shape or q.shape[0] != shape[0] or q.shape[2:] != shape[2:]:
+            raise ValueError("q and q_out must have one shape, with the tokens of k")
+        t.q, t.q_out, t.H_q = q.data_ptr(), q_out.data_ptr(), q.shape[1]
+    if k_out is not None:
+        t.k_out_stride[:] = _tokens(k_out, "k_out", cache, packed)
+        if k_out.shape != shape:
+            raise ValueError("k_out must have the shape of k")
+        t.k_out = k_out.data_ptr()
+    if packed:
+        if n_new is not None:
+            raise ValueError("n_new is for padded tokens, cu_new for packed ones")
+        _kv_tensor(cu_new, "cu_new", torch.int32, (seqs.B + 1,), dev)
+        t.cu_new = cu_new.data_ptr()
+    elif n_new is not None:
+        _kv_tensor(n_new, "n_new", torch.int32, (seqs.B,), dev)
+        t.n_new = n_new.data_ptr()
+    t.n_tokens, t.max_new = n, n if max_new is None else max_new
+    if rope is not None:
+        if not (rope.dim() == 3 and rope.shape[2] == 2):
+            raise ValueError("rope must be [positions, rot_dim / 2, 2]")
+        _kv_tensor(rope, "rope", torch.float32, rope.shape, dev)
+        t.rope, t.rope_len, t.rot_dim = rope.data_ptr(), rope.shape[0], 2 * rope.shape[1]
+        t.interleaved = interleaved
+    if new_lens is not None:
+        _kv_tensor(new_lens, "new_lens", torch.int32, (seqs.B,), dev)
+        t.new_lens = new_lens.data_ptr()
+    _check(lib().cm_kv_append(cache._ref, ctypes.byref(seqs), ctypes.byref(t), _stream(stream)),
+           "cm_kv_append")
+
+
+def cm_attn_decode_workspace_size(B: int, H_q: int, H_kv: int, d: int) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().cm_attn_decode_workspace_size(B, H_q, H_kv, d, ctypes.byref(n)),
+           "cm_attn_decode_workspace_size")
+    return n.value
+
+
+def _one_token(t, name, cache: KVCache, B: int):
+    if not (t.dtype == torch.bfloat16 and t.dim() == 3 and t.device == cache.device
+            and t.shape[0] == B and t.shape[2] == cache.d and t.stride(2) == 1):
+        raise ValueError(f"{name} must be a bf16 tensor [B, H_q, d] on {cache.device} with d = "
+                         f"{cache.d} contiguous")
+    return _Strides2(*(x if n > 1 else 0 for x, n in zip(t.stride()[:2], t.shape)))
+
+
+def cm_attn_decode(cache: KVCache, page_table, lens, q, o, lse, workspace: torch.Tensor,
+                   desc: Descriptor | None = None, sel=None, nsel=None,
+                   scale: float | None = None, stream=None) -> None:
+    """Attention of the last of each sequence's lens[b] tokens over the cache: q, o bf16
+    [B, H_q, d]; lse fp32 [B, H_q] or None.  desc: the mask, whose row lens[b] - 1 the token sees by;
+    or sel (int32 [B, H_kv, n]) with nsel (int32 [B, H_kv]): the pages to attend to."""
+    seqs = _kv_seqs(cache, page_table, lens)
+    B, H = seqs.B, q.shape[1]
+    qs, os = _one_token(q, "q", cache, B), _one_token(o, "o", cache, B)
+    if o.shape != q.shape:
+        raise ValueError("o shape mismatch")
+    if lse is not None:
+        _kv_tensor(lse, "lse", torch.float32, (B, H), cache.device)
+    sel_max = 0
+    if (sel is None) != (nsel is None):
+        raise ValueError("sel and nsel come together")
+    if sel is not None:
+        sel_max = sel.shape[-1]
+        _kv_tensor(sel, "sel", torch.int32, (B, cache.H_kv, sel_max), cache.device)
+        _kv_tensor(nsel, "nsel", torch.int32, (B, cache.H_kv), cache.device)
+    _workspace(workspace, cache)
+    if desc is not None and desc.itab_f.device != cache.device:
+        raise ValueError(f"desc must be on {cache.device}")
+    scale = 1.0 / math.sqrt(cache.d) if scale is None else scale
+    _check(lib().cm_attn_decode(cache._ref, ctypes.byref(seqs),
+                                ctypes.byref(desc.c) if desc is not None else None, _ptr(sel),
+                                _ptr(nsel), sel_max, q.data_ptr(), qs, o.data_ptr(), os, _ptr(lse),
+                                H, scale, workspace.data_ptr(), workspace.nbytes, _stream(stream)),
+           "cm_attn_decode")
+
+
+def _workspace(w, cache: KVCache):
+    if not (w.device == cache.device and w.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous tensor on {cache.device}")
+
+
+def cm_select_pages_workspace_size(B: int, H_kv: int, max_pages: int) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().cm_select_pages_workspace_size(B, H_kv, max_pages, ctypes.byref(n)),
+           "cm_select_pages_workspace_size")
+    return n.value
+
+
+def cm_select_pages(cache: KVCache, page_table, lens, q, sel, nsel, workspace: torch.Tensor,
+                    keep_first: int = 0, keep_last: int = 0, stream=None) -> None:
+    """The sel.shape[2] pages of each sequence and key-value head whose summaries promise the largest
+    scores for the new token's queries q (bf16 [B, H_q, d]), the first keep_first and last keep_last
+    pages always among them: sel int32 [B, H_kv, n] in ascending order, -1 behind the last, and
+    their number nsel int32 [B, H_kv]."""
+    seqs = _kv_seqs(cache, page_table, lens)
+    B = seqs.B
+    if cache.summary is None:
+        raise ValueError("the cache has no page summaries")
+    if not (sel.dim() == 3 and sel.shape[2] > 0):
+        raise ValueError("sel must be [B, H_kv, n]")
+    _kv_tensor(sel, "sel", torch.int32, (B, cache.H_kv, sel.shape[2]), cache.device)
+    _kv_tensor(nsel, "nsel", torch.int32, (B, cache.H_kv), cache.device)
+    _workspace(workspace, cache)
+    qs = _one_token(q, "q", cache, B)
+    _check(lib().cm_select_pages(cache._ref, ctypes.byref(seqs), q.data_ptr(), qs, q.shape[1],
+                                 keep_first, keep_last, sel.data_ptr(), nsel.data_ptr(),
+                                 sel.shape[2], workspace.data_ptr(), workspace.nbytes,
+                                 _stream(stream)),
+           "cm_select_pages")
+
+
+def cm_kv_status(cache: KVCache, stream=None) -> int:
+    """The first device error since the last call (CM_OK where there was none); zeroes it."""
+    return lib().cm_kv_status(cache._ref, _stream(stream))
+
+
+def _used_on(stream, *tensors):
+    """Tells the allocator of tensors made on the current stream that `stream` uses them."""
+    if stream is not None:
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream))
+        for t in tensors:
+            t.record_stream(stream)
+
+
+def decode_attention(cache: KVCache, page_table, lens, q, desc=None, sel=None, nsel=None,
+                     scale=None, stream=None, workspace=None):
+    """cm_attn_decode into new tensors: (o, lse)."""
+    B, H, d = q.shape
+    o = torch.empty(B, H, d, dtype=q.dtype, device=q.device)
+    lse = torch.empty(B, H, dtype=torch.float32, device=q.device)
+    if workspace is None:
+        workspace = torch.empty(cm_attn_decode_workspace_size(B, H, cache.H_kv, d),
+                                dtype=torch.uint8, device=q.device)
+    cm_attn_decode(cache, page_table, lens, q, o, lse, workspace, desc, sel, nsel, scale, stream)
+    _used_on(stream, o, lse, workspace)
+    return o, lse
+
+
+def select_pages(cache: KVCache, page_table, lens, q, n: int, keep_first: int = 0,
+                 keep_last: int = 0, stream=None, workspace=None):
+    """cm_select_pages of n pages into new tensors: (sel, nsel)."""
+    B = q.shape[0]
+    sel = torch.empty(B, cache.H_kv, n, dtype=torch.int32, device=q.device)
+    nsel = torch.empty(B, cache.H_kv, dtype=torch.int32, device=q.device)
+    if workspace is None:
+        workspace = torch.empty(
+            cm_select_pages_workspace_size(B, cache.H_kv, page_table.shape[1]), dtype=torch.uint8,
+            device=q.device)
+    cm_select_pages(cache, page_table, lens, q, sel, nsel, workspace, keep_first, keep_last, stream)
+    _used_on(stream, sel, nsel, workspace)
+    return sel, nsel

@@ -13,6 +13,7 @@ which holds no masking or attention arithmetic.
 Modules
   masks      dense visibility predicates, canonical Interval Tables, Tile-State Bitmaps
   attention  fp64 softmax attention forward and backward over a dense boolean mask
+  kv_cache   append, single-token attention and page selection over a paged key-value cache
 
 Every function is pinned by a ``-m "not gpu"`` test to something other than itself (closed-form
 counts, library routines, autograd, finite differences, the paper's worked example).
