@@ -84,6 +84,10 @@ int check_workspace(const void* workspace, size_t workspace_bytes, int B, int H,
 
 }  // namespace
 
+namespace cm {
+uint64_t wait_limit_ns() { return g_wait_limit_ns.load(); }
+}  // namespace cm
+
 extern "C" {
 
 CM_API const char* cm_error_string(int code) {

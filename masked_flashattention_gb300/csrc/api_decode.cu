@@ -4,6 +4,7 @@
 #include <cstdint>
 
 #include "../../include/cm.h"
+#include "kernels.h"
 #include "kv_cache.h"
 #include "ptx.cuh"
 
@@ -203,7 +204,9 @@ CM_API int cm_attn_decode(const cm_kv_cache* cache, const cm_kv_seqs* seqs,
   p.H_q = H_q;
   p.scale = scale;
   p.workspace = workspace;
-  return cm::launch_attn_decode(p, static_cast<cudaStream_t>(stream)) == 0 ? CM_OK : CM_ERR_CUDA;
+  return cm::launch_attn_decode(p, cm::wait_limit_ns(), static_cast<cudaStream_t>(stream)) == 0
+             ? CM_OK
+             : CM_ERR_CUDA;
 }
 
 CM_API int cm_select_pages_workspace_size(int B, int H_kv, int max_pages, size_t* bytes) {

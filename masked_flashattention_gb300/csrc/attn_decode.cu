@@ -1,137 +1,1099 @@
 // Attention of one new token per sequence over a paged key-value cache (cm_attn_decode).
 //
-// First form: one CTA per (sequence, query head).  Each of its 4 warps takes every fourth key, with
-// the row's channels spread over its lanes and a running maximum and sum (one pass over the keys);
-// the warps are joined through shared memory.
-#include <cuda_fp8.h>
+// What bounds it: every visible key and value is read once for 4 * (query heads a key-value head)
+// flops an element pair, so up to 16 heads a group (128 flops every 4 bytes of a bf16 cache, every 2
+// of an e4m3 one) the bytes bound it, far below the tensor cores' rate.
+//
+// Work.  A row is one key-value head of one sequence with up to 8 * NB of its query heads; its keys
+// are cut into tiles of 32.  All rows' tiles, one after another, are dealt out in equal runs: one
+// run a CTA (one CTA an SM), and within it one run a warp, so a batch of any lengths keeps every SM
+// equally busy and a single long sequence is split over all of them.  Where a run ends inside a row, the row's
+// parts are joined: within a CTA through shared memory, between CTAs by a second small kernel that
+// is already resident when the first ends.  The dealing goes by the lengths on the device, which
+// every CTA adds up for itself (a scan over the batch).
+//
+// A warp pair works alone: one warp fetches tiles by TMA into a ring of its own (page numbers are
+// read 32 tiles ahead), the other computes; no barrier of the CTA until the run's end.  The
+// tensor-core shape is turned around so that few query heads waste little of it:
+//   S^T [32 keys x 8 heads] = K Q^T          A = K rows as they lie in shared memory (ldmatrix)
+//   O^T [d x 8 heads]      += V^T P^T        A = V transposed on the way (ldmatrix.trans)
+// with a running maximum and sum per head (one pass).  The maximum is only renewed when a score
+// passes it by 2^8 (all in log2 units), which bounds p by 256 and spares the cross-lane maximum on
+// most tiles.  P is rounded to the values' 16-bit type for the second product; sums, maxima and O are fp32.
+// An e4m3 cache is widened to fp16 (exactly) between shared memory and the product; queries become
+// fp16 scaled by a power of two per head so that none overflows.
+#include <cuda_fp16.h>
 
 #include "kv_cache.h"
 #include "ptx.cuh"
+#include "tma_host.h"
 
 namespace cm {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kPairs = 4;           // warp pairs of a CTA
+constexpr int kThreads = 64 * kPairs;
+constexpr int kTileKeys = 32;
+constexpr int kMaxCtas = 320;
 constexpr int kMaxIntervals = 8;
+constexpr float kRenew = 8.f;       // log2 units a score may pass the running maximum by
+constexpr size_t kSmemMax = 232448;
 
-template <int D, bool E4M3>
-__global__ void __launch_bounds__(32 * kWarps) decode_kernel(const DecodeParams p) {
-  constexpr int N = D / 32;  // channels of a lane
-  __shared__ float part[kWarps][D + 2];
-  const int b = blockIdx.y, h = blockIdx.x, P = 1 << p.c.log2_page;
-  const int g = h / (p.H_q / p.c.H_kv);
-  const int warp = threadIdx.x / 32, lane = lane_id();
-  int len = p.c.lens[b];
-  bool good = len >= 0 && static_cast<int64_t>(len) <= (static_cast<int64_t>(p.c.max_pages) << p.c.log2_page);
-  if (p.itab && len > p.S) good = false;
-  if (!good) {
-    if (threadIdx.x == 0) set_status(p.c.status, kDevBadMeta, b);
-    len = 0;
-  }
-  int ni = 1, st[kMaxIntervals], en[kMaxIntervals];
-  st[0] = 0;
-  en[0] = len;
-  if (p.itab && len > 0) {
-    ni = p.NI;
+// flags of a tile
+constexpr int kFirst = 1;   // first tile of the warp's part of the row
+constexpr int kLast = 2;    // last tile of that part
+constexpr int kStarts = 4;  // the part begins where the row begins
+constexpr int kEnds = 8;    // the part ends where the row ends
+
+template <int D, bool E4M3, int NB>
+struct Cfg {
+  static constexpr int kItem = E4M3 ? 1 : 2;
+  static constexpr int kRowBytes = D * kItem;
+  static constexpr int kBoxBytes = kRowBytes < 128 ? kRowBytes : 128;  // inner width of a TMA box
+  static constexpr int kBoxes = kRowBytes / kBoxBytes;
+  static constexpr int kMatrix = kTileKeys * kRowBytes;
+  static constexpr int kStage = 2 * kMatrix;  // K, then V
+  static constexpr int kStages = 49152 / kStage < 8 ? 49152 / kStage : 8;
+  static constexpr int kHeads = 8 * NB;
+  static constexpr int kHeadPitch = D + 4;  // floats; keeps a warp's fragment stores free of conflicts
+  static constexpr int kPiece = kHeads * kHeadPitch * 4 + 2 * kHeads * 4;  // O, m, l
+  static constexpr int kRing = kPairs * kStages * kStage;
+  static constexpr int kOffPiece = kRing;
+  static constexpr int kOffMeta = kOffPiece + kPairs * kPiece;
+  static constexpr int kOffBars = kOffMeta + kPairs * kStages * 16;
+  static constexpr int kOffHead = kOffBars + kPairs * kStages * 16;   // int4 per piece
+  static constexpr int kOffMisc = kOffHead + 2 * kPairs * 16;         // starts, counts, abort flag
+  static constexpr int kSmem = kOffMisc + 128;
+  static_assert(kSmem <= static_cast<int>(kSmemMax), "shared memory");
+  static_assert(kPairs * kPiece >= kThreads * 8, "the scan borrows the pieces' memory");
+  static_assert(kStages * kStage >= kPiece, "the last piece of a warp borrows its ring");
+};
+
+// Workspace: per CTA a header (int4, .x = parts of the row whose start its second part holds, .y = that
+// row) and two parts, the first of a row begun earlier, the second of a row carried on.
+struct Part {
+  float* o;  // [heads][D]
+  float* m;  // [heads], log2 units
+  float* l;
+};
+template <int D>
+__device__ __forceinline__ Part part_at(void* workspace, int heads, int cta, int slot) {
+  float* f = reinterpret_cast<float*>(static_cast<char*>(workspace) + kMaxCtas * 16) +
+             static_cast<size_t>(cta * 2 + slot) * heads * (D + 2);
+  return {f, f + heads * D, f + heads * (D + 1)};
+}
+
+struct DecodeArgs {
+  DecodeParams p;
+  int chunks;   // rows of one key-value head: ceil(group / heads of a row)
+  int group;
+  int units;    // B, or B * H_kv where pages are selected
+  int rows;     // of a unit
+  int ctas;
+  int64_t min_run;  // fewest tiles a CTA's run is given
+  uint64_t wait_ns;
+};
+
+// ---- instructions -----------------------------------------------------------------------------
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t movm_trans(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+template <bool F16>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  if constexpr (F16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// two e4m3 (the low or the high half of x) as fp16x2, exact
+__device__ __forceinline__ uint32_t widen_lo(uint32_t x) {
+  uint32_t y;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t widen_hi(uint32_t x) {
+  uint32_t y;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int32_t x, int32_t y,
+                                            int32_t z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+// ---- the plan of a unit: which tiles it has ------------------------------------------------------
+// A unit is a sequence (all its key-value heads see the same keys), or with selected pages one
+// key-value head of a sequence.  Intervals [st, en) of keys become tile ranges; a tile that several touch
+// belongs to the first in the order of the ranges' starts, so with `before` that order, interval i
+// owns the tiles [max(a_i, max of b_j before i), b_i).
+__device__ __forceinline__ int unit_length(const DecodeArgs& a, int b, bool report) {
+  const DecodeParams& p = a.p;
+  const int len = p.c.lens[b];
+  const bool good = len >= 0 &&
+                    static_cast<int64_t>(len) <= (static_cast<int64_t>(p.c.max_pages) << p.c.log2_page) &&
+                    (p.itab == nullptr || len <= p.S);
+  if (!good && report) set_status(p.c.status, kDevBadMeta, b);
+  return good ? len : 0;
+}
+__device__ __forceinline__ int2 unit_interval(const DecodeArgs& a, int b, int n, int len) {
+  if (a.p.itab == nullptr) return make_int2(0, n == 0 ? len : 0);
+  if (n >= a.p.NI || len == 0) return make_int2(0, 0);
+  const int2 iv = reinterpret_cast<const int2*>(
+      a.p.itab)[(static_cast<int64_t>(b) * a.p.NI + n) * a.p.S + (len - 1)];
+  const int s = max(iv.x, 0), e = min(iv.y, len);
+  return e > s ? make_int2(s, e) : make_int2(0, 0);
+}
+__device__ __forceinline__ int selected_tiles(const DecodeArgs& a, int u) {
+  const int n = min(max(a.p.nsel[u], 0), a.p.sel_max);
+  return a.p.c.log2_page == 4 ? (n + 1) / 2 : n << (a.p.c.log2_page - 5);
+}
+__device__ __forceinline__ int unit_tiles(const DecodeArgs& a, int u, bool report) {
+  const int b = a.p.sel ? u / a.p.c.H_kv : u;
+  const int len = unit_length(a, b, report);
+  if (a.p.sel) return len ? selected_tiles(a, u) : 0;
+  if (a.p.itab == nullptr) return (len + kTileKeys - 1) / kTileKeys;
+  int lo[kMaxIntervals], hi[kMaxIntervals], total = 0;
 #pragma unroll
-    for (int n = 0; n < kMaxIntervals; ++n)
-      if (n < ni) {
-        const int2 iv = reinterpret_cast<const int2*>(p.itab)[(static_cast<int64_t>(b) * ni + n) * p.S + len - 1];
-        st[n] = iv.x;
-        en[n] = min(iv.y, len);
-      }
+  for (int n = 0; n < kMaxIntervals; ++n) {
+    const int2 iv = unit_interval(a, b, n, len);
+    lo[n] = iv.x / kTileKeys;
+    hi[n] = (iv.y + kTileKeys - 1) / kTileKeys;
   }
-  float q[N], o[N], m = -INFINITY, l = 0.f;
-  const __nv_bfloat16* qr = p.q + b * p.qs.seq + h * p.qs.head;
-  const float ks = E4M3 ? p.c.k_scale[g] : 1.f, vs = E4M3 ? p.c.v_scale[g] : 1.f;
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    q[i] = __bfloat162float(qr[lane + 32 * i]) * (p.scale * ks);
-    o[i] = 0.f;
+  for (int i = 0; i < kMaxIntervals; ++i) {
+    int from = lo[i];
+#pragma unroll
+    for (int j = 0; j < kMaxIntervals; ++j)
+      if (j != i && (lo[j] < lo[i] || (lo[j] == lo[i] && j < i))) from = max(from, hi[j]);
+    total += max(hi[i] - from, 0);
   }
-  const int pages = (len + P - 1) >> p.c.log2_page;
-  const int64_t row = static_cast<int64_t>(b) * p.c.H_kv + g;
-  const int entries = p.sel ? min(max(p.nsel[row], 0), p.sel_max) : pages;
-  int before = -1;
-  for (int e = 0; e < entries; ++e) {
-    int place = e;
-    if (p.sel) {
-      place = p.sel[row * p.sel_max + e];
-      if (place <= before || place >= pages) {
-        if (threadIdx.x == 0) set_status(p.c.status, kDevBadMeta, b);
-        continue;
-      }
-      before = place;
+  return total;
+}
+
+// The same by a warp: lane n < 8 holds interval n.
+struct Plan {
+  int b, len, tiles;
+  int st, en;         // keys of the lane's interval
+  int from, cnt, off; // its own tiles, and their place in the unit's order
+};
+__device__ __forceinline__ Plan make_plan(const DecodeArgs& a, int u, int lane) {
+  Plan w;
+  w.b = a.p.sel ? u / a.p.c.H_kv : u;
+  w.len = unit_length(a, w.b, false);
+  w.st = w.en = w.from = w.cnt = w.off = 0;
+  if (a.p.sel) {
+    w.tiles = w.len ? selected_tiles(a, u) : 0;
+    return w;
+  }
+  const int2 iv = lane < kMaxIntervals ? unit_interval(a, w.b, lane, w.len) : make_int2(0, 0);
+  w.st = iv.x;
+  w.en = iv.y;
+  const int lo = iv.x / kTileKeys, hi = (iv.y + kTileKeys - 1) / kTileKeys;
+  if (a.p.itab == nullptr) {  // one interval
+    w.cnt = lane == 0 ? hi : 0;
+    w.tiles = __shfl_sync(0xFFFFFFFFu, hi, 0);
+    return w;
+  }
+  w.from = lo;
+#pragma unroll
+  for (int j = 0; j < kMaxIntervals; ++j) {
+    const int lj = __shfl_sync(0xFFFFFFFFu, lo, j), hj = __shfl_sync(0xFFFFFFFFu, hi, j);
+    if (j != lane && (lj < lo || (lj == lo && j < lane))) w.from = max(w.from, hj);
+  }
+  w.cnt = lane < kMaxIntervals ? max(hi - w.from, 0) : 0;
+  w.tiles = 0;
+#pragma unroll
+  for (int j = 0; j < kMaxIntervals; ++j) {
+    const int lj = __shfl_sync(0xFFFFFFFFu, lo, j), cj = __shfl_sync(0xFFFFFFFFu, w.cnt, j);
+    if (lj < lo || (lj == lo && j < lane)) w.off += cj;
+    w.tiles += cj;
+  }
+  return w;
+}
+
+// Up to 32 consecutive tiles of a row, one per lane.
+struct Chunk {
+  int row, n, c0;        // row, tiles, place of the first in the row
+  int h;                 // key-value head
+  int page0, page1;      // pages of the tile (page1: second half of a tile of two 16-key pages); -1: none
+  int key0, key1;        // first keys of these
+  bool full;             // every key of the tile is visible
+};
+
+struct Walk {
+  int u, m, c;      // unit, row of the unit, tile of the row: what comes next
+  int64_t pos, end; // of the warp's run
+  Plan plan;
+};
+
+template <int D>
+__device__ __forceinline__ void next_chunk(const DecodeArgs& a, Walk& w, Chunk& k, int lane) {
+  k.n = 0;
+  if (w.pos >= w.end) return;
+  while (w.c >= w.plan.tiles || w.m >= a.rows) {  // next row, next unit (some have no tiles)
+    if (w.plan.tiles > 0 && w.m + 1 < a.rows) {
+      ++w.m;
+      w.c = 0;
+    } else {
+      ++w.u;
+      if (w.u >= a.units) return;  // not reached: the run ends with the last tile
+      w.m = 0;
+      w.c = 0;
+      w.plan = make_plan(a, w.u, lane);
     }
-    const int page = p.c.table[static_cast<int64_t>(b) * p.c.max_pages + place];
-    if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.c.num_pages)) {
-      if (threadIdx.x == 0) set_status(p.c.status, kDevBadMeta, b);
+  }
+  const DecodeParams& p = a.p;
+  const int log2_page = p.c.log2_page, P = 1 << log2_page;
+  k.row = w.u * a.rows + w.m;
+  const int bh = k.row / a.chunks;  // sequence * H_kv + head
+  k.h = bh - bh / p.c.H_kv * p.c.H_kv;
+  k.c0 = w.c;
+  k.n = static_cast<int>(min(min(static_cast<int64_t>(32), static_cast<int64_t>(w.plan.tiles - w.c)), w.end - w.pos));
+  const int c = w.c + lane;
+  const bool in = lane < k.n;
+  const int pages = (w.plan.len + P - 1) >> log2_page;
+  int place0 = -1, place1 = -1;
+  k.key0 = k.key1 = 0;
+  k.full = false;
+  if (p.sel) {
+    const int32_t* sel = p.sel + static_cast<int64_t>(bh) * p.sel_max;
+    const int entries = min(max(p.nsel[bh], 0), p.sel_max);
+    const int e0 = log2_page == 4 ? 2 * c : c >> (log2_page - 5);
+    if (in) {
+      place0 = sel[e0];
+      const int before = e0 > 0 ? sel[e0 - 1] : -1;
+      int place = place0;
+      if (log2_page == 4 && e0 + 1 < entries) {
+        place1 = sel[e0 + 1];
+        if (place1 <= place0 || place1 >= pages) {
+          set_status(p.c.status, kDevBadMeta, w.plan.b);
+          place1 = -1;
+        }
+      }
+      if (place <= before || place >= pages) {
+        set_status(p.c.status, kDevBadMeta, w.plan.b);
+        place0 = -1;
+      }
+      k.key0 = (place0 << log2_page) + (log2_page == 4 ? 0 : (c & ((P >> 5) - 1)) * kTileKeys);
+      k.key1 = place1 << 4;
+    }
+  } else {
+    int tile = c;
+    if (p.itab) {
+#pragma unroll
+      for (int j = 0; j < kMaxIntervals; ++j) {
+        const int from = __shfl_sync(0xFFFFFFFFu, w.plan.from, j);
+        const int off = __shfl_sync(0xFFFFFFFFu, w.plan.off, j);
+        const int cnt = __shfl_sync(0xFFFFFFFFu, w.plan.cnt, j);
+        if (c >= off && c < off + cnt) tile = from + c - off;
+      }
+    }
+    if (in) {
+      k.key0 = tile * kTileKeys;
+      k.key1 = k.key0 + 16;
+      place0 = k.key0 >> log2_page;
+      if (log2_page == 4 && place0 + 1 < pages) place1 = place0 + 1;
+    }
+  }
+  // visible keys are [st, en) of the intervals; without intervals, [0, len)
+  const bool two = log2_page == 4;
+  const int end0 = k.key0 + (two ? 16 : kTileKeys);
+  if (p.itab) {
+#pragma unroll
+    for (int j = 0; j < kMaxIntervals; ++j) {
+      const int st = __shfl_sync(0xFFFFFFFFu, w.plan.st, j), en = __shfl_sync(0xFFFFFFFFu, w.plan.en, j);
+      k.full |= st <= k.key0 && k.key0 + kTileKeys <= en;
+    }
+    k.full = k.full && in;
+  } else {
+    k.full = in && place0 >= 0 && end0 <= w.plan.len && (!two || (place1 >= 0 && k.key1 + 16 <= w.plan.len));
+  }
+  const int32_t* table = p.c.table + static_cast<int64_t>(w.plan.b) * p.c.max_pages;
+  k.page0 = place0 >= 0 ? table[place0] : -1;
+  k.page1 = place1 >= 0 ? table[place1] : -1;
+  if ((place0 >= 0 && static_cast<unsigned>(k.page0) >= static_cast<unsigned>(p.c.num_pages)) ||
+      (place1 >= 0 && static_cast<unsigned>(k.page1) >= static_cast<unsigned>(p.c.num_pages))) {
+    set_status(p.c.status, kDevBadMeta, w.plan.b);
+    if (static_cast<unsigned>(k.page0) >= static_cast<unsigned>(p.c.num_pages)) k.page0 = -1;
+    if (static_cast<unsigned>(k.page1) >= static_cast<unsigned>(p.c.num_pages)) k.page1 = -1;
+    k.full = false;
+  }
+  w.c += k.n;
+  w.pos += k.n;
+}
+
+// A warp's wait: whole or not at all, so that its lanes go on together.
+__device__ __forceinline__ bool warp_wait(const WaitCtl& wait, uint32_t bar, uint32_t parity, int where) {
+  return __all_sync(0xFFFFFFFFu, wait(bar, parity, where));
+}
+
+// ---- fetching warp ------------------------------------------------------------------------------
+// Returns the tiles fetched; `rest` is the first of them whose copy the computing warp need not have
+// waited for, were it to give up.
+template <int D, bool E4M3, int NB>
+__device__ __forceinline__ int fetch(const DecodeArgs& a, const CUtensorMap* kmap,
+                                      const CUtensorMap* vmap, Walk w, uint32_t ring,
+                                      uint32_t meta, uint32_t bars, int64_t run, const WaitCtl& wait,
+                                     int lane, int& rest) {
+  using C = Cfg<D, E4M3, NB>;
+  const DecodeParams& p = a.p;
+  const int log2_page = p.c.log2_page, P = 1 << log2_page;
+  int issued = 0;
+  const int64_t begin = w.pos, end = w.end;
+  Chunk next;
+  next_chunk<D>(a, w, next, lane);
+  bool ok = true;
+  while (next.n > 0 && ok) {
+    const Chunk cur = next;
+    const Plan plan = w.plan;  // of cur's unit
+    const int64_t row_begin = w.pos - cur.n - cur.c0, at = w.pos - cur.n;
+    // parts of the row, one a CTA's run
+    const int parts = static_cast<int>((row_begin + plan.tiles - 1) / run - row_begin / run) + 1;
+    next_chunk<D>(a, w, next, lane);  // its loads are on their way while cur is fetched
+    for (int j = 0; j < cur.n; ++j) {
+      const int stage = issued % C::kStages;
+      const uint32_t full = bars + stage * 16, empty = full + 8;
+      if (issued >= C::kStages && !warp_wait(wait, empty, ((issued / C::kStages) & 1) ^ 1, 1)) {
+        ok = false;
+        break;
+      }
+      const int page0 = __shfl_sync(0xFFFFFFFFu, cur.page0, j), page1 = __shfl_sync(0xFFFFFFFFu, cur.page1, j);
+      const int key0 = __shfl_sync(0xFFFFFFFFu, cur.key0, j), key1 = __shfl_sync(0xFFFFFFFFu, cur.key1, j);
+      uint32_t seen = 0xFFFFFFFFu;
+      if (!__shfl_sync(0xFFFFFFFFu, static_cast<int>(cur.full), j)) {  // one lane a key
+        const bool second = log2_page == 4 && lane >= 16;
+        const int key = second ? key1 + lane - 16 : key0 + lane;
+        bool in = key < plan.len;
+        if (p.itab) {
+          in = false;
+#pragma unroll
+          for (int n = 0; n < kMaxIntervals; ++n) {
+            const int st = __shfl_sync(0xFFFFFFFFu, plan.st, n), en = __shfl_sync(0xFFFFFFFFu, plan.en, n);
+            in |= key >= st && key < en;
+          }
+        }
+        seen = __ballot_sync(0xFFFFFFFFu, in && (second ? page1 : page0) >= 0);
+      }
+      if (lane == 0) {
+        const int c = cur.c0 + j;
+        int flags = 0;
+        if (c == 0) flags |= kFirst | kStarts;
+        if (at + j == begin) flags |= kFirst;
+        if (c == plan.tiles - 1) flags |= kLast | kEnds;
+        if (at + j == end - 1) flags |= kLast;
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(meta + stage * 16), "r"(cur.row),
+                     "r"(seen), "r"(flags), "r"(parts)
+                     : "memory");
+        const uint32_t k_at = ring + stage * C::kStage, v_at = k_at + C::kMatrix;
+        const int half = log2_page == 4 ? 2 : 1;  // boxes of 16 or 32 keys
+        const bool get0 = page0 >= 0, get1 = half == 2 && page1 >= 0;
+        mbar_arrive_expect_tx(full, C::kStage / half * (static_cast<int>(get0) + static_cast<int>(get1)));
+        if (get0) {
+          const int y = (cur.h << log2_page) + (key0 & (P - 1));
+#pragma unroll
+          for (int x = 0; x < C::kBoxes; ++x) {
+            tma_load_3d(k_at + x * kTileKeys * C::kBoxBytes, kmap, x * C::kBoxBytes / C::kItem, y, page0, full);
+            tma_load_3d(v_at + x * kTileKeys * C::kBoxBytes, vmap, x * C::kBoxBytes / C::kItem, y, page0, full);
+          }
+        }
+        if (get1) {
+          const int y = cur.h << log2_page;
+#pragma unroll
+          for (int x = 0; x < C::kBoxes; ++x) {
+            const uint32_t to = (x * kTileKeys + 16) * C::kBoxBytes;
+            tma_load_3d(k_at + to, kmap, x * C::kBoxBytes / C::kItem, y, page1, full);
+            tma_load_3d(v_at + to, vmap, x * C::kBoxBytes / C::kItem, y, page1, full);
+          }
+        }
+      }
+      __syncwarp();
+      ++issued;
+    }
+  }
+  rest = max(issued - C::kStages, 0);
+  if (ok) {  // tell the computing warp that there is no more
+    const int stage = issued % C::kStages;
+    const uint32_t full = bars + stage * 16, empty = full + 8;
+    if (issued < C::kStages || warp_wait(wait, empty, ((issued / C::kStages) & 1) ^ 1, 2)) {
+      rest = max(issued + 1 - C::kStages, 0);
+      if (lane == 0) {
+        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(meta + stage * 16), "r"(-1) : "memory");
+        mbar_arrive(full);
+      }
+    }
+  }
+  return issued;
+}
+
+// ---- computing warp -------------------------------------------------------------------------------
+// Query fragments of a row: B operand [16 channels x 8 heads] of each step, thread (head lane / 4,
+// channels by lane % 4).  bf16 steps take channels 2t, 2t+1 and 2t+8, 2t+9; e4m3 steps take
+// 4t .. 4t+3, the order in which a lane gets the keys' bytes.
+template <int D, bool E4M3, int NB>
+__device__ __forceinline__ void load_q(const DecodeArgs& a, int row, int lane,
+                                       uint32_t (&q)[NB][D / 16][2], float (&scale)[NB][2]) {
+  const DecodeParams& p = a.p;
+  const int bh = row / a.chunks, chunk = row - bh * a.chunks;
+  const int b = bh / p.c.H_kv, h = bh - b * p.c.H_kv;
+  const float base = p.scale * 1.4426950408889634f * (E4M3 ? p.c.k_scale[h] : 1.f);
+#pragma unroll
+  for (int n = 0; n < NB; ++n) {
+    const int i = chunk * 8 * NB + n * 8 + lane / 4;
+    const bool in = i < a.group;
+    const __nv_bfloat16* src = p.q + b * p.qs.seq + static_cast<int64_t>(h * a.group + (in ? i : 0)) * p.qs.head;
+    if constexpr (!E4M3) {
+#pragma unroll
+      for (int s = 0; s < D / 16; ++s)
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          q[n][s][x] = in ? *reinterpret_cast<const uint32_t*>(src + s * 16 + x * 8 + (lane & 3) * 2) : 0u;
+      scale[n][0] = scale[n][1] = base;
+    } else {
+      float top = 0.f;
+#pragma unroll
+      for (int s = 0; s < D / 16; ++s) {
+        const uint2 w = in ? *reinterpret_cast<const uint2*>(src + s * 16 + (lane & 3) * 4) : make_uint2(0, 0);
+        q[n][s][0] = w.x;
+        q[n][s][1] = w.y;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          top = fmaxf(top, fabsf(__uint_as_float(q[n][s][x] << 16)));
+          top = fmaxf(top, fabsf(__uint_as_float(q[n][s][x] & 0xFFFF0000u)));
+        }
+      }
+      top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+      const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -100), 100);
+      const float inv = pow2_bits(-e);
+#pragma unroll
+      for (int s = 0; s < D / 16; ++s)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const __half2 f = __floats2half2_rn(__uint_as_float(q[n][s][x] << 16) * inv,
+                                              __uint_as_float(q[n][s][x] & 0xFFFF0000u) * inv);
+          q[n][s][x] = *reinterpret_cast<const uint32_t*>(&f);
+        }
+      const float mine = base * pow2_bits(e);
+      scale[n][0] = __shfl_sync(0xFFFFFFFFu, mine, (lane & 3) * 8);      // heads of the lane's columns
+      scale[n][1] = __shfl_sync(0xFFFFFFFFu, mine, (lane & 3) * 8 + 4);
+    }
+  }
+}
+
+// Address of the 16-byte piece `c` of key `r` in a matrix of the ring (TMA's swizzle).
+template <int D, bool E4M3>
+__device__ __forceinline__ uint32_t piece_at(uint32_t matrix, int r, int c) {
+  if constexpr (E4M3 && D == 64) {  // 64-byte rows
+    return matrix + r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+  } else {
+    return matrix + (c >> 3) * (kTileKeys * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+  }
+}
+
+template <int D, bool E4M3, int NB>
+struct State {
+  uint32_t q[NB][D / 16][2];
+  float scale[NB][2];
+  float m[NB][2], l[NB][2];
+  float o[NB][D / 16][4];
+};
+
+template <int D, bool E4M3, int NB>
+__device__ __forceinline__ void compute_tile(State<D, E4M3, NB>& t, uint32_t k_at, uint32_t v_at,
+                                             uint32_t seen, int lane) {
+  float s[2][NB][4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) s[i][n][x] = 0.f;
+  // S^T = K Q^T: matrices of ldmatrix are (keys 0-7, 8-15) x (pieces 2j, 2j+1)
+  const int row = lane & 15, col = lane >> 4;
+#pragma unroll
+  for (int j = 0; j < D * (E4M3 ? 1 : 2) / 32; ++j)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t w[4];
+      ldsm4(w, piece_at<D, E4M3>(k_at, i * 16 + row, 2 * j + col));
+      if constexpr (!E4M3) {
+#pragma unroll
+        for (int n = 0; n < NB; ++n) mma16816<false>(s[i][n], w, t.q[n][j][0], t.q[n][j][1]);
+      } else {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const uint32_t f[4] = {widen_lo(w[2 * x]), widen_lo(w[2 * x + 1]), widen_hi(w[2 * x]), widen_hi(w[2 * x + 1])};
+#pragma unroll
+          for (int n = 0; n < NB; ++n) mma16816<true>(s[i][n], f, t.q[n][2 * j + x][0], t.q[n][2 * j + x][1]);
+        }
+      }
+    }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) s[i][n][x] *= t.scale[n][x & 1];
+  const bool whole = seen == 0xFFFFFFFFu;
+  if (!whole) {  // keys of the lane: lane / 4 and 8 further, of both halves
+    const uint32_t bits = seen >> (lane >> 2);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          s[i][n][x] = (bits >> (i * 16 + (x >> 1) * 8)) & 1u ? s[i][n][x] : -INFINITY;
+  }
+  // running maximum in log2 units; renewed when a score passes it by kRenew
+  bool pass = false;
+#pragma unroll
+  for (int n = 0; n < NB; ++n)
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) pass |= s[i][n][x] > t.m[n][x & 1] + kRenew;
+  if (__any_sync(0xFFFFFFFFu, pass)) {
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        float top = fmaxf(fmaxf(s[0][n][x], s[0][n][x + 2]), fmaxf(s[1][n][x], s[1][n][x + 2]));
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+        top = fmaxf(top, t.m[n][x]);
+        const float fade = top == -INFINITY ? 1.f : ex2_approx(t.m[n][x] - top);
+        t.m[n][x] = top;
+        t.l[n][x] *= fade;
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+          t.o[n][j][x] *= fade;
+          t.o[n][j][x + 2] *= fade;
+        }
+      }
+  }
+  // P^T as the B operand [16 keys x 8 heads]
+  uint32_t pb[2][NB][2];
+#pragma unroll
+  for (int n = 0; n < NB; ++n) {
+    const float m0 = t.m[n][0] == -INFINITY ? 0.f : t.m[n][0], m1 = t.m[n][1] == -INFINITY ? 0.f : t.m[n][1];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float e[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        e[x] = ex2_approx(s[i][n][x] - (x & 1 ? m1 : m0));
+        t.l[n][x & 1] += e[x];
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        uint32_t w;
+        if constexpr (E4M3) {
+          const __half2 f = __floats2half2_rn(e[2 * x], e[2 * x + 1]);
+          w = *reinterpret_cast<const uint32_t*>(&f);
+        } else {
+          w = pack_bf16x2(e[2 * x], e[2 * x + 1]);
+        }
+        pb[i][n][x] = movm_trans(w);
+      }
+    }
+  }
+  // O^T += V^T P^T.  Hidden keys' values are cleared: 0 * NaN is no 0.
+  const int key = (lane & 7) + ((lane >> 4) << 3), piece = (lane >> 3) & 1;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t keep[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};  // keys 2t, 2t+1 and 8 further
+    if (!whole) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const uint32_t b = seen >> (i * 16 + x * 8 + (lane & 3) * 2);
+        keep[x] = (b & 1u ? 0xFFFFu : 0u) | (b & 2u ? 0xFFFF0000u : 0u);
+      }
+    }
+    if constexpr (!E4M3) {
+      // matrices (keys 0-7, piece 2j), (keys 0-7, 2j+1), (keys 8-15, 2j), (keys 8-15, 2j+1)
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) {
+        uint32_t w[4];
+        ldsm4t(w, piece_at<D, E4M3>(v_at, i * 16 + key, 2 * j + piece));
+        if (!whole) {
+          w[0] &= keep[0];
+          w[1] &= keep[0];
+          w[2] &= keep[1];
+          w[3] &= keep[1];
+        }
+#pragma unroll
+        for (int n = 0; n < NB; ++n) mma16816<false>(t.o[n][j], w, pb[i][n][0], pb[i][n][1]);
+      }
+    } else {
+      // matrices (keys 0-7, 8-15) x (pieces 2j, 2j+1); a lane gets channels 2c, 2c+1 (c = lane / 4) of
+      // keys 2t, 2t+1: row r of the product's tile is channel 2r, row r + 8 channel 2r + 1
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) {
+        uint32_t w[4];
+        ldsm4t(w, piece_at<D, E4M3>(v_at, i * 16 + row, 2 * j + col));
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const uint32_t u0 = __byte_perm(w[2 * x], 0, 0x3120), u1 = __byte_perm(w[2 * x + 1], 0, 0x3120);
+          uint32_t f[4] = {widen_lo(u0), widen_hi(u0), widen_lo(u1), widen_hi(u1)};
+          if (!whole) {
+            f[0] &= keep[0];
+            f[1] &= keep[0];
+            f[2] &= keep[1];
+            f[3] &= keep[1];
+          }
+#pragma unroll
+          for (int n = 0; n < NB; ++n) mma16816<true>(t.o[n][2 * j + x], f, pb[i][n][0], pb[i][n][1]);
+        }
+      }
+    }
+  }
+}
+
+// Channel of accumulator x (0 or 2: rows lane / 4 and 8 further) of tile j.
+template <bool E4M3>
+__device__ __forceinline__ int channel_of(int j, int x, int lane) {
+  return E4M3 ? j * 16 + (lane >> 2) * 2 + (x >> 1) : j * 16 + (lane >> 2) + (x >> 1) * 8;
+}
+
+struct RowAt {
+  __nv_bfloat16* o;  // first head of the row
+  float* lse;
+  int heads;         // of the row
+  float v_scale;
+};
+template <bool E4M3, int NB>
+__device__ __forceinline__ RowAt row_at(const DecodeArgs& a, int row) {
+  const DecodeParams& p = a.p;
+  const int bh = row / a.chunks, chunk = row - bh * a.chunks;
+  const int b = bh / p.c.H_kv, h = bh - b * p.c.H_kv;
+  const int head = h * a.group + chunk * 8 * NB;
+  return {p.o + b * p.os.seq + head * p.os.head,
+          p.lse ? p.lse + static_cast<int64_t>(b) * p.H_q + head : nullptr,
+          min(8 * NB, a.group - chunk * 8 * NB), E4M3 ? p.c.v_scale[h] : 1.f};
+}
+
+// 1 / l, 0 for a row that saw nothing (l = 0 and O = 0: the output is 0)
+__device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
+__device__ __forceinline__ float natural_lse(float m, float l) {
+  return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+template <int D, bool E4M3, int NB>
+__device__ __forceinline__ void compute(const DecodeArgs& a, char* smem, uint32_t ring, uint32_t meta,
+                                        uint32_t bars, int pair, const WaitCtl& wait, int lane) {
+  using C = Cfg<D, E4M3, NB>;
+  State<D, E4M3, NB> t;
+  int4* heads = reinterpret_cast<int4*>(smem + C::kOffHead) + 2 * pair;
+  bool starts = false;
+  for (int done = 0;; ++done) {
+    const int stage = done % C::kStages;
+    const uint32_t full = bars + stage * 16;
+    if (!warp_wait(wait, full, (done / C::kStages) & 1, 4)) return;
+    const uint4 x = ld_shared_v4(meta + stage * 16);
+    const int row = static_cast<int>(x.x), flags = static_cast<int>(x.z);
+    if (row < 0) return;
+    if (flags & kFirst) {
+      starts = flags & kStarts;
+      load_q<D, E4M3, NB>(a, row, lane, t.q, t.scale);
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        t.m[n][0] = t.m[n][1] = -INFINITY;
+        t.l[n][0] = t.l[n][1] = 0.f;
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) t.o[n][j][i] = 0.f;
+      }
+    }
+    const uint32_t k_at = ring + stage * C::kStage;
+    compute_tile<D, E4M3, NB>(t, k_at, k_at + C::kMatrix, x.y, lane);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(full + 8);
+    if (!(flags & kLast)) continue;
+
+    // the sums so far are per lane: over the 8 lanes of a column
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) t.l[n][i] += __shfl_xor_sync(0xFFFFFFFFu, t.l[n][i], d);
+    if (starts && (flags & kEnds)) {  // the whole row
+      const RowAt r = row_at<E4M3, NB>(a, row);
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        const float i0 = inverse(t.l[n][0]) * r.v_scale, i1 = inverse(t.l[n][1]) * r.v_scale;
+        const int h0 = n * 8 + (lane & 3) * 2;
+        if constexpr (E4M3) {
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) {
+            const int c = channel_of<true>(j, 0, lane);
+            if (h0 < r.heads)
+              *reinterpret_cast<uint32_t*>(r.o + h0 * a.p.os.head + c) = pack_bf16x2(t.o[n][j][0] * i0, t.o[n][j][2] * i0);
+            if (h0 + 1 < r.heads)
+              *reinterpret_cast<uint32_t*>(r.o + (h0 + 1) * a.p.os.head + c) = pack_bf16x2(t.o[n][j][1] * i1, t.o[n][j][3] * i1);
+          }
+        } else {  // [channel][head pair] to [head][channel pair]
+          const int h = n * 8 + (lane >> 2);
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+            for (int x2 = 0; x2 < 2; ++x2) {
+              const uint32_t w = movm_trans(pack_bf16x2(t.o[n][j][2 * x2] * i0, t.o[n][j][2 * x2 + 1] * i1));
+              if (h < r.heads)
+                *reinterpret_cast<uint32_t*>(r.o + h * a.p.os.head + j * 16 + x2 * 8 + (lane & 3) * 2) = w;
+            }
+        }
+        if (r.lse && lane < 4) {
+          if (h0 < r.heads) r.lse[h0] = natural_lse(t.m[n][0], t.l[n][0]);
+          if (h0 + 1 < r.heads) r.lse[h0 + 1] = natural_lse(t.m[n][1], t.l[n][1]);
+        }
+      }
       continue;
     }
-    const int64_t at = (static_cast<int64_t>(g) << p.c.log2_page) * D;
-    for (int r = warp; r < P; r += kWarps) {
-      const int pos = (place << p.c.log2_page) + r;
-      bool seen = false;
+    // a part: of a row begun before this warp's run (slot 0, its first part), or of one carried on
+    // (slot 1, its last part: nothing will come into the ring any more)
+    const int slot = starts ? 1 : 0;
+    float* f = slot ? reinterpret_cast<float*>(smem + pair * C::kStages * C::kStage)
+                    : reinterpret_cast<float*>(smem + C::kOffPiece + pair * C::kPiece);
 #pragma unroll
-      for (int n = 0; n < kMaxIntervals; ++n)
-        if (n < ni) seen |= pos >= st[n] && pos < en[n];
-      if (!seen) continue;
-      float k[N], v[N], s = 0.f;
+    for (int n = 0; n < NB; ++n) {
+      const int h0 = n * 8 + (lane & 3) * 2;
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int64_t x = at + r * D + lane + 32 * i;
-        if (E4M3) {
-          k[i] = static_cast<float>(reinterpret_cast<const __nv_fp8_e4m3*>(p.c.k + page * p.c.k_page_bytes)[x]);
-          v[i] = static_cast<float>(reinterpret_cast<const __nv_fp8_e4m3*>(p.c.v + page * p.c.v_page_bytes)[x]);
-        } else {
-          k[i] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.c.k + page * p.c.k_page_bytes)[x]);
-          v[i] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.c.v + page * p.c.v_page_bytes)[x]);
+      for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          f[(h0 + (i & 1)) * C::kHeadPitch + channel_of<E4M3>(j, i, lane)] = t.o[n][j][i];
+      if (lane < 4) {
+        float* ml = f + C::kHeads * C::kHeadPitch;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          ml[h0 + i] = t.m[n][i];
+          ml[C::kHeads + h0 + i] = t.l[n][i];
         }
-        s += q[i] * k[i];
       }
+    }
+    if (lane == 0)
+      heads[slot] = make_int4(row, (starts ? kStarts : 0) | (flags & kEnds), static_cast<int>(x.w), 1);
+  }
+}
+
+// Joins the CTA's parts, row by row: 16 threads a head, D / 16 channels a thread.
+template <int D, bool E4M3, int NB>
+__device__ __forceinline__ void join_warps(const DecodeArgs& a, char* smem, int tid) {
+  using C = Cfg<D, E4M3, NB>;
+  constexpr int N = D / 16;
+  const int4* heads = reinterpret_cast<const int4*>(smem + C::kOffHead);
+  const int c0 = (tid & 15) * 4;  // channels c0 .. c0+3 of each 64
+  int carried = 0, carried_row = 0;
+  for (int i = 0; i < 2 * kPairs;) {
+    if (!heads[i].w) {
+      ++i;
+      continue;
+    }
+    const int4 first = heads[i];
+    int j = i, ends = 0;
+    while (j < 2 * kPairs && (!heads[j].w || heads[j].x == first.x)) {
+      if (heads[j].w) ends = heads[j].y & kEnds;
+      ++j;
+    }
+    const bool starts = first.y & kStarts;
+    const RowAt r = row_at<E4M3, NB>(a, first.x);
+    const Part out = part_at<D>(a.p.workspace, C::kHeads, blockIdx.x, starts ? 1 : 0);
+    for (int h = tid >> 4; h < r.heads; h += 2 * kPairs) {
+      float m = -INFINITY, l = 0.f, o[N];
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-      const float top = fmaxf(m, s), keep = top == -INFINITY ? 0.f : top;
-      const float a = __expf(m - keep), w = __expf(s - keep);
-      l = l * a + w;
+      for (int c = 0; c < N; ++c) o[c] = 0.f;
+      for (int s = i; s < j; ++s) {
+        if (!heads[s].w) continue;
+        const float* f = s & 1 ? reinterpret_cast<const float*>(smem + (s >> 1) * C::kStages * C::kStage)
+                               : reinterpret_cast<const float*>(smem + C::kOffPiece + (s >> 1) * C::kPiece);
+        const float* ml = f + C::kHeads * C::kHeadPitch;
+        const float ms = ml[h], ls = ml[C::kHeads + h];
+        const float top = fmaxf(m, ms), zero = top == -INFINITY ? 0.f : top;
+        const float fade = ex2_approx(m - zero), w = ex2_approx(ms - zero);
+        m = top;
+        l = l * fade + ls * w;
 #pragma unroll
-      for (int i = 0; i < N; ++i) o[i] = o[i] * a + w * v[i];
-      m = top;
+        for (int g = 0; g < N / 4; ++g) {
+          const float4 x = *reinterpret_cast<const float4*>(f + h * C::kHeadPitch + g * 64 + c0);
+          o[4 * g] = o[4 * g] * fade + x.x * w;
+          o[4 * g + 1] = o[4 * g + 1] * fade + x.y * w;
+          o[4 * g + 2] = o[4 * g + 2] * fade + x.z * w;
+          o[4 * g + 3] = o[4 * g + 3] * fade + x.w * w;
+        }
+      }
+      if (starts && ends) {
+        const float inv = inverse(l) * r.v_scale;
+#pragma unroll
+        for (int g = 0; g < N / 4; ++g)
+          *reinterpret_cast<uint2*>(r.o + h * a.p.os.head + g * 64 + c0) =
+              make_uint2(pack_bf16x2(o[4 * g] * inv, o[4 * g + 1] * inv),
+                         pack_bf16x2(o[4 * g + 2] * inv, o[4 * g + 3] * inv));
+        if (r.lse && (tid & 15) == 0) r.lse[h] = natural_lse(m, l);
+      } else {
+#pragma unroll
+        for (int g = 0; g < N / 4; ++g)
+          *reinterpret_cast<float4*>(out.o + h * D + g * 64 + c0) =
+              make_float4(o[4 * g], o[4 * g + 1], o[4 * g + 2], o[4 * g + 3]);
+        if ((tid & 15) == 0) {
+          out.m[h] = m;
+          out.l[h] = l;
+        }
+      }
+    }
+    if (starts && !ends) {
+      carried = first.z;
+      carried_row = first.x;
+    }
+    i = j;
+  }
+  if (tid == 0) reinterpret_cast<int4*>(a.p.workspace)[blockIdx.x] = make_int4(carried, carried_row, 0, 0);
+}
+
+template <int D, bool E4M3, int NB>
+__global__ void __launch_bounds__(kThreads, 1)
+    decode_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
+                  const __grid_constant__ CUtensorMap vmap) {
+  using C = Cfg<D, E4M3, NB>;
+  extern __shared__ __align__(1024) char smem[];  // the swizzled tiles need the alignment
+  const uint32_t base = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
+  int64_t* starts = reinterpret_cast<int64_t*>(smem + C::kOffMisc);          // [kPairs]: unit
+  int64_t* rests = starts + kPairs;                                          // [kPairs]: tiles into it
+  int64_t* total_at = rests + kPairs;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(total_at + 1);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if ((base & 1023u) != 0) {
+    if (tid == 0) {
+      set_status(a.p.c.status, kDevBadMeta, 0x1ff);
+      reinterpret_cast<int4*>(a.p.workspace)[blockIdx.x] = make_int4(0, 0, 0, 0);
+    }
+    return;
+  }
+  if (tid < kPairs * C::kStages) {
+    mbar_init(base + C::kOffBars + tid * 16, 1);
+    mbar_init(base + C::kOffBars + tid * 16 + 8, 1);
+  }
+  if (tid < 2 * kPairs) reinterpret_cast<int4*>(smem + C::kOffHead)[tid] = make_int4(0, 0, 0, 0);
+  if (tid == 0) {
+    *abort_flag = 0;
+    tma_prefetch_desc(&kmap);
+    tma_prefetch_desc(&vmap);
+  }
+  fence_barrier_init();
+
+  // tiles of all units: each thread adds up a run of them, then a scan over the threads
+  const int per = (a.units + kThreads - 1) / kThreads;
+  const int u0 = min(tid * per, a.units), u1 = min(u0 + per, a.units);
+  int64_t mine = 0;
+  for (int u = u0; u < u1; ++u) {
+    const bool owner = u % a.ctas == static_cast<int>(blockIdx.x);
+    const int n = unit_tiles(a, u, owner);
+    mine += static_cast<int64_t>(n) * a.rows;
+    if (n == 0 && owner) {  // nothing visible: zeros
+      for (int m = 0; m < a.rows; ++m) {
+        const RowAt r = row_at<E4M3, NB>(a, u * a.rows + m);
+        for (int h = 0; h < r.heads; ++h) {
+          for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(r.o + h * a.p.os.head + c) = make_uint4(0, 0, 0, 0);
+          if (r.lse) r.lse[h] = -INFINITY;
+        }
+      }
     }
   }
+  int64_t sum = mine;
 #pragma unroll
-  for (int i = 0; i < N; ++i) part[warp][lane + 32 * i] = o[i];
-  if (lane == 0) {
-    part[warp][D] = m;
-    part[warp][D + 1] = l;
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t x = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+    if (lane >= d) sum += x;
+  }
+  int64_t* warp_sum = reinterpret_cast<int64_t*>(smem + C::kOffPiece);
+  if (lane == 31) warp_sum[warp] = sum;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) sum += warp_sum[w];
+  int64_t total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) total += warp_sum[w];
+  const int64_t run = max((total + a.ctas - 1) / a.ctas, a.min_run);  // of a CTA
+  const int64_t cta0 = min(run * blockIdx.x, total), cta1 = min(cta0 + run, total);
+  const int64_t share = (cta1 - cta0 + kPairs - 1) / kPairs;          // of a warp
+#pragma unroll
+  for (int w = 0; w < kPairs; ++w) {
+    const int64_t at = cta0 + w * share;
+    if (at < cta1 && at >= sum - mine && at < sum) {
+      int64_t from = sum - mine;
+      int u = u0;
+      for (;; ++u) {
+        const int64_t n = static_cast<int64_t>(unit_tiles(a, u, false)) * a.rows;
+        if (at < from + n) break;
+        from += n;
+      }
+      starts[w] = u;
+      rests[w] = at - from;
+    }
   }
   __syncthreads();
-  float top = -INFINITY, sum = 0.f;
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, part[w][D]);
-  const float keep = top == -INFINITY ? 0.f : top;
-  for (int w = 0; w < kWarps; ++w) sum += part[w][D + 1] * __expf(part[w][D] - keep);
-  for (int c = threadIdx.x; c < D; c += 32 * kWarps) {
-    float x = 0.f;
-    for (int w = 0; w < kWarps; ++w) x += part[w][c] * __expf(part[w][D] - keep);
-    p.o[b * p.os.seq + h * p.os.head + c] = __float2bfloat16(sum > 0.f ? x * vs / sum : sum == 0.f ? 0.f : sum);
+
+  const WaitCtl wait{abort_flag, a.p.c.status, a.wait_ns};
+  const int pair = warp & (kPairs - 1);
+  const int64_t at = min(cta0 + pair * share, cta1), until = min(at + share, cta1);
+  const uint32_t ring = base + pair * C::kStages * C::kStage;
+  const uint32_t meta = base + C::kOffMeta + pair * C::kStages * 16;
+  const uint32_t bars = base + C::kOffBars + pair * C::kStages * 16;
+  int fetched = 0, rest = 0;
+  if (at < until) {
+    if (warp >= kPairs) {
+      Walk w;
+      w.u = static_cast<int>(starts[pair]);
+      w.plan = make_plan(a, w.u, lane);
+      w.m = static_cast<int>(rests[pair] / w.plan.tiles);
+      w.c = static_cast<int>(rests[pair] - static_cast<int64_t>(w.m) * w.plan.tiles);
+      w.pos = at;
+      w.end = until;
+      fetched = fetch<D, E4M3, NB>(a, &kmap, &vmap, w, ring, meta, bars, run, wait, lane, rest);
+    } else {
+      compute<D, E4M3, NB>(a, smem, ring, meta, bars, pair, wait, lane);
+    }
   }
-  if (threadIdx.x == 0 && p.lse) p.lse[static_cast<int64_t>(b) * p.H_q + h] = sum == 0.f ? -INFINITY : keep + logf(sum);
+  __syncthreads();
+  if (*abort_flag) {  // the outputs are undefined; the second kernel must not follow what is not there
+    // copies in flight end by themselves, and the CTA must not exit before they have
+    for (int i = rest; i < fetched; ++i)
+      mbar_wait_drain(bars + (i % C::kStages) * 16, (i / C::kStages) & 1, a.p.c.status, 3);
+    if (tid == 0) reinterpret_cast<int4*>(a.p.workspace)[blockIdx.x] = make_int4(0, 0, 0, 0);
+    return;
+  }
+  if (tid < 32 * kPairs) join_warps<D, E4M3, NB>(a, smem, tid);
 }
+
+// Joins the parts of a row that several CTAs hold: CTA x's header says how many there are, its own
+// second part first, then the first parts of the CTAs behind it.  One block a head, one thread a channel.
+template <int D, bool E4M3, int NB>
+__global__ void __launch_bounds__(D) join_kernel(const __grid_constant__ DecodeArgs a) {
+  constexpr int kHeads = 8 * NB;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int4 head = reinterpret_cast<const int4*>(a.p.workspace)[blockIdx.x];
+  const int n = min(head.x, a.ctas - static_cast<int>(blockIdx.x)), h = blockIdx.y;
+  if (n < 2) return;
+  const RowAt r = row_at<E4M3, NB>(a, head.y);
+  if (h >= r.heads) return;
+  float m = -INFINITY;
+  for (int i = 0; i < n; ++i) m = fmaxf(m, part_at<D>(a.p.workspace, kHeads, blockIdx.x + i, i == 0).m[h]);
+  const float zero = m == -INFINITY ? 0.f : m;
+  float l = 0.f, o = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const Part x = part_at<D>(a.p.workspace, kHeads, blockIdx.x + i, i == 0);
+    const float w = ex2_approx(x.m[h] - zero);
+    l += x.l[h] * w;
+    o += x.o[h * D + threadIdx.x] * w;
+  }
+  r.o[h * a.p.os.head + threadIdx.x] = __float2bfloat16(o * inverse(l) * r.v_scale);
+  if (r.lse && threadIdx.x == 0) r.lse[h] = natural_lse(m, l);
+}
+
+// 3-D map of a pool: [pages][heads * page size][d], boxes of `rows` keys x 128 bytes (64 where a row
+// is no longer), swizzled by that width.
+bool make_pool_map(CUtensorMap* map, const void* base, const KvView& c, int64_t page_bytes) {
+  EncodeTiledFn enc = encode_tiled_fn();
+  if (!enc) return false;
+  const int item = c.e4m3 ? 1 : 2, P = 1 << c.log2_page, row = c.d * item;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(c.d), static_cast<cuuint64_t>(c.H_kv) * P,
+                              static_cast<cuuint64_t>(c.num_pages)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(row), static_cast<cuuint64_t>(page_bytes)};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>((row < 128 ? row : 128) / item),
+                             static_cast<cuuint32_t>(P < kTileKeys ? P : kTileKeys), 1};
+  const cuuint32_t steps[3] = {1, 1, 1};
+  return enc(map, c.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+             const_cast<void*>(base), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             row < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
+    return -1;
+  return n < kMaxCtas ? n : kMaxCtas;
+}
+
+template <int D, bool E4M3, int NB>
+int launch(DecodeArgs& a, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream) {
+  using C = Cfg<D, E4M3, NB>;
+  if (cudaFuncSetAttribute(decode_kernel<D, E4M3, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           C::kSmem) != cudaSuccess)
+    return -1;
+  decode_kernel<D, E4M3, NB><<<a.ctas, kThreads, C::kSmem, stream>>>(a, k, v);
+  if (cudaGetLastError() != cudaSuccess) return -1;
+  cudaLaunchAttribute overlap;
+  overlap.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  overlap.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.ctas, a.group < C::kHeads ? a.group : C::kHeads);
+  cfg.blockDim = dim3(D);
+  cfg.stream = stream;
+  cfg.attrs = &overlap;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel<D, E4M3, NB>, static_cast<const DecodeArgs&>(a)) == cudaSuccess ? 0 : -1;
+}
+
+// Heads of a row: 8 where a group has no more, else 16 (a larger group takes several rows, whose
+// second reading of the keys comes from L2).
+int heads_of(int group) { return group <= 8 ? 8 : 16; }
 
 }  // namespace
 
-size_t decode_workspace_bytes(int, int, int, int) { return 16; }
+size_t decode_workspace_bytes(int, int H_q, int H_kv, int d) {
+  return kMaxCtas * 16 + static_cast<size_t>(kMaxCtas) * 2 * heads_of(H_q / H_kv) * (d + 2) * 4;
+}
 
-int launch_attn_decode(const DecodeParams& p, cudaStream_t stream) {
-  const dim3 grid(p.H_q, p.c.B);
-  if (p.c.d == 128) {
-    if (p.c.e4m3) decode_kernel<128, true><<<grid, 32 * kWarps, 0, stream>>>(p);
-    else decode_kernel<128, false><<<grid, 32 * kWarps, 0, stream>>>(p);
-  } else {
-    if (p.c.e4m3) decode_kernel<64, true><<<grid, 32 * kWarps, 0, stream>>>(p);
-    else decode_kernel<64, false><<<grid, 32 * kWarps, 0, stream>>>(p);
+int launch_attn_decode(const DecodeParams& p, uint64_t wait_ns, cudaStream_t stream) {
+  DecodeArgs a;
+  a.p = p;
+  a.group = p.H_q / p.c.H_kv;
+  const int heads = heads_of(a.group);
+  a.chunks = (a.group + heads - 1) / heads;
+  a.units = p.sel ? p.c.B * p.c.H_kv : p.c.B;
+  a.rows = p.sel ? a.chunks : p.c.H_kv * a.chunks;
+  a.ctas = sm_count();
+  a.min_run = kPairs;
+  a.wait_ns = wait_ns;
+  if (a.ctas < 1) return -1;
+  CUtensorMap k, v;
+  if (!make_pool_map(&k, p.c.k, p.c, p.c.k_page_bytes) || !make_pool_map(&v, p.c.v, p.c, p.c.v_page_bytes))
+    return -1;
+  if (heads == 8) {
+    if (p.c.d == 128) return p.c.e4m3 ? launch<128, true, 1>(a, k, v, stream) : launch<128, false, 1>(a, k, v, stream);
+    return p.c.e4m3 ? launch<64, true, 1>(a, k, v, stream) : launch<64, false, 1>(a, k, v, stream);
   }
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  if (p.c.d == 128) return p.c.e4m3 ? launch<128, true, 2>(a, k, v, stream) : launch<128, false, 2>(a, k, v, stream);
+  return p.c.e4m3 ? launch<64, true, 2>(a, k, v, stream) : launch<64, false, 2>(a, k, v, stream);
 }
 
 }  // namespace cm

@@ -56,7 +56,7 @@ struct DecodeParams {
   void* workspace;
 };
 size_t decode_workspace_bytes(int B, int H_q, int H_kv, int d);
-int launch_attn_decode(const DecodeParams& p, cudaStream_t stream);
+int launch_attn_decode(const DecodeParams& p, uint64_t wait_ns, cudaStream_t stream);
 
 struct SelectParams {
   KvView c;
