@@ -212,7 +212,7 @@ CM_API int cm_attn_decode(const cm_kv_cache* cache, const cm_kv_seqs* seqs,
 CM_API int cm_select_pages_workspace_size(int B, int H_kv, int max_pages, size_t* bytes) {
   if (!bytes || B < 1 || H_kv < 1 || max_pages < 1) return CM_ERR_INVALID_ARG;
   if (B > kMaxB || H_kv > 1024 || max_pages > 32768) return CM_ERR_UNSUPPORTED;
-  *bytes = static_cast<size_t>(B) * H_kv * max_pages * 4;
+  *bytes = static_cast<size_t>(B) * H_kv * cm::score_pitch(max_pages) * 4;
   return CM_OK;
 }
 

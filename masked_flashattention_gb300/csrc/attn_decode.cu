@@ -889,8 +889,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   int64_t* rests = starts + kPairs;                                          // [kPairs]: tiles into it
   int64_t* total_at = rests + kPairs;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(total_at + 1);
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  let_next_start();
   if ((base & 1023u) != 0) {
+    wait_for_previous();
     if (tid == 0) {
       set_status(a.p.c.status, kDevBadMeta, 0x1ff);
       reinterpret_cast<int4*>(a.p.workspace)[blockIdx.x] = make_int4(0, 0, 0, 0);
@@ -908,6 +909,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&vmap);
   }
   fence_barrier_init();
+  wait_for_previous();
 
   // tiles of all units: each thread adds up a run of them, then a scan over the threads
   const int per = (a.units + kThreads - 1) / kThreads;
@@ -996,7 +998,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D, bool E4M3, int NB>
 __global__ void __launch_bounds__(D) join_kernel(const __grid_constant__ DecodeArgs a) {
   constexpr int kHeads = 8 * NB;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_previous();
   const int4 head = reinterpret_cast<const int4*>(a.p.workspace)[blockIdx.x];
   const int n = min(head.x, a.ctas - static_cast<int>(blockIdx.x)), h = blockIdx.y;
   if (n < 2) return;
@@ -1044,23 +1046,16 @@ int sm_count() {
 }
 
 template <int D, bool E4M3, int NB>
-int launch(DecodeArgs& a, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream) {
+int launch(const DecodeArgs& a, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream) {
   using C = Cfg<D, E4M3, NB>;
   if (cudaFuncSetAttribute(decode_kernel<D, E4M3, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            C::kSmem) != cudaSuccess)
     return -1;
-  decode_kernel<D, E4M3, NB><<<a.ctas, kThreads, C::kSmem, stream>>>(a, k, v);
-  if (cudaGetLastError() != cudaSuccess) return -1;
-  cudaLaunchAttribute overlap;
-  overlap.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  overlap.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.ctas, a.group < C::kHeads ? a.group : C::kHeads);
-  cfg.blockDim = dim3(D);
-  cfg.stream = stream;
-  cfg.attrs = &overlap;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<D, E4M3, NB>, static_cast<const DecodeArgs&>(a)) == cudaSuccess ? 0 : -1;
+  return launch_after(decode_kernel<D, E4M3, NB>, dim3(a.ctas), kThreads, C::kSmem, stream, a, k, v) &&
+                 launch_after(join_kernel<D, E4M3, NB>, dim3(a.ctas, a.group < C::kHeads ? a.group : C::kHeads), D,
+                              0, stream, a)
+             ? 0
+             : -1;
 }
 
 // Heads of a row: 8 where a group has no more, else 16 (a larger group takes several rows, whose

@@ -129,6 +129,8 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams 
   constexpr int kItem = E4M3 ? 1 : 2;
   __shared__ float red[kThreads / 32][2][D];
 
+  let_next_start();
+  wait_for_previous();
   const int b = blockIdx.z, P = 1 << p.c.log2_page;
   int start, count, base;
   const bool good = new_tokens(p, b, start, count, base);
@@ -286,14 +288,11 @@ int launch_kv_append(const AppendParams& p, cudaStream_t stream) {
   // the most pages a run of max_new tokens can touch (no tokens still write new_lens)
   const int segs = p.max_new > 0 ? (p.max_new + P - 2) / P + 1 : 1;
   const dim3 grid((heads + units - 1) / units, segs, p.c.B);
-  if (p.c.d == 128) {
-    if (p.c.e4m3) kv_append_kernel<128, true><<<grid, kThreads, 0, stream>>>(p);
-    else kv_append_kernel<128, false><<<grid, kThreads, 0, stream>>>(p);
-  } else {
-    if (p.c.e4m3) kv_append_kernel<64, true><<<grid, kThreads, 0, stream>>>(p);
-    else kv_append_kernel<64, false><<<grid, kThreads, 0, stream>>>(p);
-  }
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  const bool ok = p.c.d == 128 ? (p.c.e4m3 ? launch_after(kv_append_kernel<128, true>, grid, kThreads, 0, stream, p)
+                                           : launch_after(kv_append_kernel<128, false>, grid, kThreads, 0, stream, p))
+                               : (p.c.e4m3 ? launch_after(kv_append_kernel<64, true>, grid, kThreads, 0, stream, p)
+                                           : launch_after(kv_append_kernel<64, false>, grid, kThreads, 0, stream, p));
+  return ok ? 0 : -1;
 }
 
 }  // namespace cm

@@ -65,9 +65,31 @@ struct SelectParams {
   int H_q, keep_first, keep_last, sel_max;
   int32_t* sel;
   int32_t* nsel;
-  float* scores;  // workspace [B][H_kv][max_pages]
+  float* scores;  // workspace [B][H_kv][score_pitch(max_pages)]
 };
+// scores of a row, padded so that every row starts on 16 bytes
+__host__ __device__ constexpr int score_pitch(int max_pages) { return (max_pages + 3) & ~3; }
 int launch_select_pages(const SelectParams& p, cudaStream_t stream);
+
+// Launches that follow one another in a serving step (append, scores, selection, attention, joining)
+// are a few microseconds each: every kernel lets the next one's blocks start early and waits for
+// the one before it to complete, memory included, before it reads or writes anything in memory.
+template <class F, class... A>
+bool launch_after(F* kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, const A&... args) {
+  cudaLaunchAttribute overlap;
+  overlap.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  overlap.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &overlap;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
+}
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ---- device helpers shared by the kernels ---------------------------------------------------
 
