@@ -346,7 +346,7 @@ typedef struct cm_kv_seqs {
  *   k, v    H_kv heads; q (may be NULL) H_q heads, rotated into q_out; k_out (may be NULL) receives
  *           the rotated keys.  q_out may be q, and k_out k, with the same strides; otherwise
  *           outputs overlap nothing else.
- *   cu_new  packed tokens: device int32 [B + 1], sequence b's are tokens cu_new[b] .. cu_new[b+1]-1
+ *   cu_new  packed tokens: device int32 [B + 1], ascending, sequence b's are tokens cu_new[b] .. cu_new[b+1]-1
  *           of n_tokens (the sequence strides are not used).  NULL: padded tokens, sequence b's
  *           are tokens 0 .. n_new[b]-1 of n_tokens; n_new (device int32 [B]) NULL: all n_tokens.
  *   max_new the most tokens any sequence appends in this call (host), at most n_tokens.

@@ -128,6 +128,8 @@ CM_API int cm_kv_append(const cm_kv_cache* cache, const cm_kv_seqs* seqs, const 
     return CM_ERR_INVALID_ARG;
   if (t->new_lens && (!good_ints(t->new_lens) || t->new_lens == seqs->lens))
     return CM_ERR_INVALID_ARG;
+  if ((t->cu_new ? t->n_tokens : static_cast<int64_t>(seqs->B) * t->max_new) > (1LL << 30))
+    return CM_ERR_UNSUPPORTED;
   if ((t->max_new + cache->page_size - 2) / cache->page_size + 1 > 65535) return CM_ERR_UNSUPPORTED;
   cm::AppendParams p;
   p.c = view(cache, seqs);

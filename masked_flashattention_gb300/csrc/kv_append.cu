@@ -1,13 +1,16 @@
 // Append of new tokens to a paged key-value cache, with the rotation of queries and keys and the
-// page summaries (cm_kv_append).
+// page summaries (cm_kv_append): two kernels.
 //
-// A token at position p of its sequence goes to row p % P of page table[p / P].  A unit of work is
-// one head's rows of one page: the tokens of a sequence that fall into the same page.  A warp holds
-// 16 rows of a unit (P / 16 warps a unit, 8 warps a CTA), 8 channels a lane in one 16-byte load,
-// all of its rows' loads in flight at once; the partner of a channel half the rotated width away
-// comes from another lane by shuffle.  A unit owns its page's summary, so the largest and smallest
-// keys need no atomics: they are taken over the page's rows in the warp's registers, then over the
-// unit's warps through shared memory.
+// append_kernel.  What bounds it: each new query, key and value is read once and written once, and
+// a row of the rotation's table is read per token.  A CTA takes 1 to 8 tokens with all their heads;
+// a thread owns 16 channels of a token in two 16-byte pieces, the partners of a rotation among
+// them (pieces j and j + rot / 16 of the rotated channels), so nothing crosses lanes, and goes
+// through the heads with the token's cosines and sines in registers.  The first heads' loads do not depend on
+// where the token goes, so they are in flight while its sequence, position and page are looked up.
+//
+// summary_kernel.  One warp a (page, head) that the call touched: the largest and smallest of the
+// page's stored keys, taken anew, so that a summary never depends on how its tokens arrived and
+// needs no atomics.
 //
 // Numerics: the rotation is fp32 with every product and sum rounded once (no fused
 // multiply-add), so that it equals the formula evaluated step by step; one rounding to bf16, and
@@ -64,45 +67,6 @@ __device__ __forceinline__ void unpack8_e4m3(const uint2& w, float scale, float 
   }
 }
 
-// Rotates the 8 channels [8c, 8c + 8) of a row held by this lane; `row` is the row's table
-// entry [rot / 2][2].  Every lane of the warp takes part in the shuffles.
-__device__ __forceinline__ void rotate8(float (&x)[8], const float* row, int c, int rot,
-                                        bool interleaved, bool active) {
-  if (interleaved) {
-    if (active && 8 * c < rot) {
-      const float4* t = reinterpret_cast<const float4*>(row) + 2 * c;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float4 f = __ldg(t + i);  // cos, sin of two pairs
-        const float a = x[4 * i], b = x[4 * i + 1], e = x[4 * i + 2], g = x[4 * i + 3];
-        x[4 * i] = __fsub_rn(__fmul_rn(a, f.x), __fmul_rn(b, f.y));
-        x[4 * i + 1] = __fadd_rn(__fmul_rn(b, f.x), __fmul_rn(a, f.y));
-        x[4 * i + 2] = __fsub_rn(__fmul_rn(e, f.z), __fmul_rn(g, f.w));
-        x[4 * i + 3] = __fadd_rn(__fmul_rn(g, f.z), __fmul_rn(e, f.w));
-      }
-    }
-    return;
-  }
-  const int half = rot >> 4;  // lanes of one half of the rotated channels
-  const bool low = c < half, in = c < 2 * half;
-  const int lane = lane_id();
-  const int partner = in ? (low ? lane + half : lane - half) : lane;
-  float y[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(0xFFFFFFFFu, x[i], partner);
-  if (active && in) {
-    const float4* t = reinterpret_cast<const float4*>(row) + 4 * (low ? c : c - half);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 f = __ldg(t + i);
-      const float p0 = __fmul_rn(x[2 * i], f.x), q0 = __fmul_rn(y[2 * i], f.y);
-      const float p1 = __fmul_rn(x[2 * i + 1], f.z), q1 = __fmul_rn(y[2 * i + 1], f.w);
-      x[2 * i] = low ? __fsub_rn(p0, q0) : __fadd_rn(p0, q0);
-      x[2 * i + 1] = low ? __fsub_rn(p1, q1) : __fadd_rn(p1, q1);
-    }
-  }
-}
-
 // What a sequence appends: false (and the status word) where it is out of range.
 __device__ __forceinline__ bool new_tokens(const AppendParams& p, int b, int& start, int& count,
                                            int& base) {
@@ -121,177 +85,260 @@ __device__ __forceinline__ bool new_tokens(const AppendParams& p, int b, int& st
          (p.rot_dim == 0 || count == 0 || end <= p.rope_len);
 }
 
-template <int D, bool E4M3>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams p) {
-  constexpr int kLanes = D / 8;       // lanes of a row
-  constexpr int kRows = 32 / kLanes;  // rows a warp touches at once
-  constexpr int kSteps = 16 / kRows;
-  constexpr int kItem = E4M3 ? 1 : 2;
-  __shared__ float red[kThreads / 32][2][D];
+// Rotates two pieces of 8 channels: (lo[i], hi[i]) are pairs, or each piece holds 4 pairs of its own.
+// cs: cosine and sine of the 8 pairs.
+__device__ __forceinline__ void rotate16(float (&lo)[8], float (&hi)[8], const float2 (&cs)[8], bool interleaved) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float& x = interleaved ? (i < 4 ? lo[2 * (i & 3)] : hi[2 * (i & 3)]) : lo[i];
+    float& y = interleaved ? (i < 4 ? lo[2 * (i & 3) + 1] : hi[2 * (i & 3) + 1]) : hi[i];
+    const float a = x, b = y;
+    x = __fsub_rn(__fmul_rn(a, cs[i].x), __fmul_rn(b, cs[i].y));
+    y = __fadd_rn(__fmul_rn(b, cs[i].x), __fmul_rn(a, cs[i].y));
+  }
+}
 
+struct Token {
+  int seq, place, pos;  // sequence (-1: none), number among its new tokens, position
+  int page;             // -1: outside the pool
+};
+
+template <int D, bool E4M3, bool INTER>
+__global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p, int log2_tokens) {
+  constexpr int kPer = D / 16;  // threads of a token's head
+  constexpr int kAtOnce = 4;    // heads whose loads are in flight
+  constexpr int kItem = E4M3 ? 1 : 2;
+  __shared__ Token tokens[8];
   let_next_start();
   wait_for_previous();
-  const int b = blockIdx.z, P = 1 << p.c.log2_page;
-  int start, count, base;
-  const bool good = new_tokens(p, b, start, count, base);
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
-    if (!good) set_status(p.c.status, kDevBadMeta, b);
-    if (p.new_lens) p.new_lens[b] = good ? start + count : start;
+  const int tid = threadIdx.x, P = 1 << p.c.log2_page, n = 1 << log2_tokens;
+  const int j = tid % kPer, tt = (tid / kPer) & (n - 1), h0 = (tid / kPer) >> log2_tokens;
+  const int step = kThreads / kPer >> log2_tokens;
+  const bool packed = p.cu_new != nullptr;
+  const int total = packed ? p.n_tokens : p.c.B * p.max_new;
+  const int i0 = blockIdx.x << log2_tokens, i = i0 + tt;
+  const int heads = p.H_q + 2 * p.c.H_kv;
+
+  // channels of the thread: pieces of 8
+  const int pairs = p.rot_dim >> 4;  // threads that rotate
+  const bool turns = j < pairs;
+  const int c0 = 8 * (turns ? j : 2 * j), c1 = 8 * (turns ? j + pairs : 2 * j + 1);
+
+  const int row_seq = packed ? 0 : i / max(p.max_new, 1), row_tok = packed ? i : i - row_seq * p.max_new;
+  auto source = [&](int h) -> const __nv_bfloat16* {
+    const bool q = h < p.H_q, k = h < p.H_q + p.c.H_kv;
+    const Strides& s = q ? p.qs : k ? p.ks : p.vs;
+    return (q ? p.q : k ? p.k : p.v) + (q ? h : k ? h - p.H_q : h - p.H_q - p.c.H_kv) * s.head +
+           (packed ? 0 : row_seq * s.seq) + row_tok * s.token;
+  };
+  uint4 w[kAtOnce][2];
+  auto load = [&](int h) {
+#pragma unroll
+    for (int x = 0; x < kAtOnce; ++x)
+      if (h + x * step < heads && i < total) {
+        const __nv_bfloat16* s = source(h + x * step);
+        w[x][0] = *reinterpret_cast<const uint4*>(s + c0);
+        w[x][1] = *reinterpret_cast<const uint4*>(s + c1);
+      }
+  };
+  load(h0);
+
+  // the tokens' sequences; the first block also writes the new lengths and reports bad sequences
+  if (tid < n) tokens[tid].seq = -1;
+  __syncthreads();
+  const bool first = blockIdx.x == 0;
+  if (packed || first) {
+    for (int b = tid; b < p.c.B; b += kThreads) {
+      int start, count, base;
+      const bool good = new_tokens(p, b, start, count, base);
+      if (first) {
+        if (!good) set_status(p.c.status, kDevBadMeta, b);
+        if (p.new_lens) p.new_lens[b] = good ? start + count : start;
+      }
+      if (packed && good)
+        for (int x = max(base, i0); x < min(base + count, i0 + n); ++x) {
+          tokens[x - i0].seq = b;
+          tokens[x - i0].place = x - base;
+          tokens[x - i0].pos = start + x - base;
+        }
+    }
   }
-  if (!good) return;
-  const int place = (start >> p.c.log2_page) + blockIdx.y;  // page of the sequence
-  const int first = place << p.c.log2_page;
-  const int lo = max(start, first), hi = min(start + count, first + P);
-  if (lo >= hi) return;
-  const int page = p.c.table[static_cast<size_t>(b) * p.c.max_pages + place];
-  const bool paged = static_cast<unsigned>(page) < static_cast<unsigned>(p.c.num_pages);
-  if (!paged && blockIdx.x == 0 && threadIdx.x == 0) set_status(p.c.status, kDevBadMeta, b);
+  if (packed) __syncthreads();
+  if (tid < n) {
+    Token& t = tokens[tid];
+    if (!packed && i0 + tid < total) {
+      const int b = (i0 + tid) / p.max_new, place = i0 + tid - b * p.max_new;
+      int start, count, base;
+      if (new_tokens(p, b, start, count, base) && place < count) {
+        t.seq = b;
+        t.place = place;
+        t.pos = start + place;
+      }
+    }
+    if (t.seq >= 0) {
+      t.page = p.c.table[static_cast<int64_t>(t.seq) * p.c.max_pages + (t.pos >> p.c.log2_page)];
+      if (static_cast<unsigned>(t.page) >= static_cast<unsigned>(p.c.num_pages)) {
+        set_status(p.c.status, kDevBadMeta, t.seq);
+        t.page = -1;
+      }
+    }
+  }
+  __syncthreads();
+  const Token t = tokens[tt];
+  if (t.seq < 0) return;
 
-  const int warps = P / 16;  // of a unit
-  const int warp = threadIdx.x / 32, lane = lane_id();
-  const int chunk = warp & (warps - 1);
-  const int head = blockIdx.x * (8 / warps) + warp / warps;  // keys, values, then queries
-  const int H_kv = p.c.H_kv;
-  const bool is_k = head < H_kv, is_v = !is_k && head < 2 * H_kv;
-  const bool is_q = head >= 2 * H_kv && head < 2 * H_kv + p.H_q;
-  const int h = is_k ? head : is_v ? head - H_kv : head - 2 * H_kv;
+  float2 cs[8];
+  if (turns) {
+    const float4* row = reinterpret_cast<const float4*>(p.rope + static_cast<int64_t>(t.pos) * p.rot_dim);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const float4 f = __ldg(row + (INTER ? (x < 2 ? 2 * j + x : 2 * (j + pairs) + x - 2) : 4 * j + x));
+      cs[2 * x] = make_float2(f.x, f.y);
+      cs[2 * x + 1] = make_float2(f.z, f.w);
+    }
+  }
+  for (int h = h0; h < heads; h += kAtOnce * step) {
+    if (h != h0) load(h);
+#pragma unroll
+    for (int x = 0; x < kAtOnce; ++x) {
+      const int head = h + x * step;
+      if (head >= heads) break;
+      const bool is_q = head < p.H_q, is_v = head >= p.H_q + p.c.H_kv;
+      const int hh = is_q ? head : is_v ? head - p.H_q - p.c.H_kv : head - p.H_q;
+      float lo[8], hi[8];
+      unpack8(w[x][0], lo);
+      unpack8(w[x][1], hi);
+      uint4 out0 = w[x][0], out1 = w[x][1];
+      if (turns && !is_v) {
+        rotate16(lo, hi, cs, INTER);
+        out0 = pack8(lo);
+        out1 = pack8(hi);
+      }
+      __nv_bfloat16* to = is_q ? p.q_out : is_v ? nullptr : p.k_out;
+      if (to) {
+        const Strides& s = is_q ? p.qos : p.kos;
+        to += hh * s.head + (packed ? 0 : row_seq * s.seq) + row_tok * s.token;
+        *reinterpret_cast<uint4*>(to + c0) = out0;
+        *reinterpret_cast<uint4*>(to + c1) = out1;
+      }
+      if (is_q || t.page < 0) continue;
+      char* row = (is_v ? p.c.v + t.page * p.c.v_page_bytes : p.c.k + t.page * p.c.k_page_bytes) +
+                  ((static_cast<int64_t>(hh) << p.c.log2_page) + (t.pos & (P - 1))) * (D * kItem);
+      if constexpr (E4M3) {
+        const float scale = __ldg((is_v ? p.c.v_scale : p.c.k_scale) + hh);
+        unpack8(out0, lo);
+        unpack8(out1, hi);
+        *reinterpret_cast<uint2*>(row + c0) = pack8_e4m3(lo, scale);
+        *reinterpret_cast<uint2*>(row + c1) = pack8_e4m3(hi, scale);
+      } else {
+        *reinterpret_cast<uint4*>(row + c0 * 2) = out0;
+        *reinterpret_cast<uint4*>(row + c1 * 2) = out1;
+      }
+    }
+  }
+}
+
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(kThreads) summary_kernel(const AppendParams p) {
+  constexpr int kLanes = D / 8;       // lanes of a row
+  constexpr int kRows = 32 / kLanes;  // rows of a load
+  constexpr int kItem = E4M3 ? 1 : 2;
+  let_next_start();
+  wait_for_previous();
+  const int b = blockIdx.z, P = 1 << p.c.log2_page, lane = lane_id();
+  const int h = blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32;
+  int start, count, base;
+  if (!new_tokens(p, b, start, count, base) || count == 0 || h >= p.c.H_kv) return;
+  const int place = (start >> p.c.log2_page) + blockIdx.y, first = place << p.c.log2_page;
+  const int held = min(start + count - first, P);  // tokens of the page
+  if (held <= 0) return;
+  const int page = p.c.table[static_cast<int64_t>(b) * p.c.max_pages + place];
+  if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.c.num_pages)) return;
   const int c = lane & (kLanes - 1), sub = lane / kLanes;
-  const bool summed = is_k && p.c.summary != nullptr && paged;
-
+  const char* rows = p.c.k + page * p.c.k_page_bytes + ((static_cast<int64_t>(h) << p.c.log2_page) * D + c * 8) * kItem;
+  const float scale = E4M3 ? p.c.k_scale[h] : 1.f;
   float high[8], low[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     high[i] = -INFINITY;
     low[i] = INFINITY;
   }
-  if (is_k || is_v || is_q) {
-    const __nv_bfloat16* src = is_k ? p.k : is_v ? p.v : p.q;
-    const Strides& ss = is_k ? p.ks : is_v ? p.vs : p.qs;
-    src += h * ss.head + (p.cu_new ? base * ss.token : b * ss.seq) + c * 8;
-    char* pool = is_k ? p.c.k : p.c.v;
-    char* rows = paged && !is_q
-                     ? pool + page * (is_k ? p.c.k_page_bytes : p.c.v_page_bytes) +
-                           ((static_cast<int64_t>(h) << p.c.log2_page) * D + c * 8) * kItem
-                     : nullptr;
-    const float scale = E4M3 && !is_q ? (is_k ? p.c.k_scale[h] : p.c.v_scale[h]) : 1.f;
-    uint4 w[kSteps];
+  for (int r0 = 0; r0 < held; r0 += 8 * kRows) {
+    uint4 w[8];
 #pragma unroll
-    for (int j = 0; j < kSteps; ++j) {
-      const int r = chunk * 16 + j * kRows + sub, pos = first + r;
-      w[j] = make_uint4(0, 0, 0, 0);
-      if (pos >= lo && pos < hi) {
-        w[j] = *reinterpret_cast<const uint4*>(src + (pos - start) * ss.token);
-      } else if (summed && pos < lo) {  // a token the page held before
-        if (E4M3) {
-          const uint2 u = *reinterpret_cast<const uint2*>(rows + r * D);
-          w[j].x = u.x;
-          w[j].y = u.y;
-        } else {
-          w[j] = *reinterpret_cast<const uint4*>(rows + r * D * 2);
-        }
+    for (int i = 0; i < 8; ++i) {
+      const int r = min(r0 + i * kRows + sub, held - 1);  // the last token again does no harm
+      if constexpr (E4M3) {
+        const uint2 u = *reinterpret_cast<const uint2*>(rows + r * D);
+        w[i] = make_uint4(u.x, u.y, 0, 0);
+      } else {
+        w[i] = *reinterpret_cast<const uint4*>(rows + r * D * 2);
       }
     }
 #pragma unroll
-    for (int j = 0; j < kSteps; ++j) {
-      const int r = chunk * 16 + j * kRows + sub, pos = first + r;
-      const bool active = pos >= lo && pos < hi, held = summed && pos < lo;
+    for (int i = 0; i < 8; ++i) {
       float x[8];
-      unpack8(w[j], x);
-      if (!is_v && p.rot_dim)
-        rotate8(x, p.rope + static_cast<int64_t>(active ? pos : 0) * p.rot_dim, c, p.rot_dim,
-                p.interleaved != 0, active);
-      if (active) {
-        const uint4 out = pack8(x);
-        __nv_bfloat16* to = is_q ? p.q_out : is_k ? p.k_out : nullptr;
-        if (to) {
-          const Strides& os = is_q ? p.qos : p.kos;
-          to += h * os.head + (p.cu_new ? base * os.token : b * os.seq) + c * 8;
-          *reinterpret_cast<uint4*>(to + (pos - start) * os.token) = out;
-        }
-        unpack8(out, x);
-        if (rows) {
-          if (E4M3) {
-            const uint2 u = pack8_e4m3(x, scale);
-            *reinterpret_cast<uint2*>(rows + r * D) = u;
-            if (summed) unpack8_e4m3(u, scale, x);
-          } else {
-            *reinterpret_cast<uint4*>(rows + r * D * 2) = out;
-          }
-        }
-      } else if (held) {
-        if (E4M3) unpack8_e4m3(make_uint2(w[j].x, w[j].y), scale, x);
-        else unpack8(w[j], x);
-      }
-      if (summed && (active || held)) {
+      if constexpr (E4M3) unpack8_e4m3(make_uint2(w[i].x, w[i].y), scale, x);
+      else unpack8(w[i], x);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          high[i] = fmaxf(high[i], x[i]);
-          low[i] = fminf(low[i], x[i]);
-        }
+      for (int k = 0; k < 8; ++k) {  // NaN loses to any number
+        high[k] = fmaxf(high[k], x[k]);
+        low[k] = fminf(low[k], x[k]);
       }
     }
   }
-  if (p.c.summary == nullptr) return;
-  // rows of the warp, then warps of the unit
+  float a = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
+  for (int i = 0; i < 8; ++i) {
 #pragma unroll
     for (int d = kLanes; d < 32; d <<= 1) {
       high[i] = fmaxf(high[i], __shfl_xor_sync(0xFFFFFFFFu, high[i], d));
       low[i] = fminf(low[i], __shfl_xor_sync(0xFFFFFFFFu, low[i], d));
     }
-  if (summed && lane < kLanes) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      red[warp][0][c * 8 + i] = high[i];
-      red[warp][1][c * 8 + i] = low[i];
-    }
+    a = fmaxf(a, fmaxf(fabsf(high[i]), fabsf(low[i])));
   }
-  __syncthreads();
-  if (!summed || chunk != 0) return;
-  for (int o = 1; o < warps; ++o)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      high[i] = fmaxf(high[i], red[warp + o][0][c * 8 + i]);
-      low[i] = fminf(low[i], red[warp + o][1][c * 8 + i]);
-    }
-  float a = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) a = fmaxf(a, fmaxf(fabsf(high[i]), fabsf(low[i])));
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, d));
+  for (int d = 1; d < kLanes; d <<= 1) a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, d));
   const int e = scale_exponent(a);
   const float inv = pow2_bits(-e);
-  if (lane < kLanes) {
-    uint32_t up[2] = {0, 0}, down[2] = {0, 0};
+  if (lane >= kLanes) return;
+  uint32_t up[2] = {0, 0}, down[2] = {0, 0};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int u = static_cast<int>(fminf(fmaxf(ceilf(high[i] * inv), -127.f), 127.f));
-      const int l = static_cast<int>(fminf(fmaxf(floorf(low[i] * inv), -127.f), 127.f));
-      up[i >> 2] |= static_cast<uint32_t>(u & 0xFF) << (8 * (i & 3));
-      down[i >> 2] |= static_cast<uint32_t>(l & 0xFF) << (8 * (i & 3));
-    }
-    const int64_t at = static_cast<int64_t>(page) * H_kv + h;
-    int8_t* s = p.c.summary + at * 2 * D + c * 8;
-    *reinterpret_cast<uint2*>(s) = make_uint2(up[0], up[1]);
-    *reinterpret_cast<uint2*>(s + D) = make_uint2(down[0], down[1]);
-    if (lane == 0) p.c.summary_scale[at] = pow2_bits(e);
+  for (int i = 0; i < 8; ++i) {
+    const int u = static_cast<int>(fminf(fmaxf(ceilf(high[i] * inv), -127.f), 127.f));
+    const int l = static_cast<int>(fminf(fmaxf(floorf(low[i] * inv), -127.f), 127.f));
+    up[i >> 2] |= static_cast<uint32_t>(u & 0xFF) << (8 * (i & 3));
+    down[i >> 2] |= static_cast<uint32_t>(l & 0xFF) << (8 * (i & 3));
   }
+  const int64_t at = static_cast<int64_t>(page) * p.c.H_kv + h;
+  int8_t* s = p.c.summary + at * 2 * D + c * 8;
+  *reinterpret_cast<uint2*>(s) = make_uint2(up[0], up[1]);
+  *reinterpret_cast<uint2*>(s + D) = make_uint2(down[0], down[1]);
+  if (lane == 0) p.c.summary_scale[at] = pow2_bits(e);
+}
+
+template <int D, bool E4M3>
+bool launch(const AppendParams& p, cudaStream_t stream) {
+  const int total = p.cu_new ? p.n_tokens : p.c.B * p.max_new;
+  // tokens of a CTA: one while there are few (16 CTAs an SM at most), up to 8 that share the lookups
+  int log2_tokens = 0;
+  while (log2_tokens < 3 && total >> log2_tokens > 152 * 16) ++log2_tokens;
+  const int blocks = total > 0 ? (total + (1 << log2_tokens) - 1) >> log2_tokens : 1;  // new_lens needs one
+  if (!launch_after(p.interleaved ? append_kernel<D, E4M3, true> : append_kernel<D, E4M3, false>, dim3(blocks),
+                    kThreads, 0, stream, p, log2_tokens))
+    return false;
+  if (!p.c.summary || p.max_new == 0) return true;
+  const int P = 1 << p.c.log2_page, warps = p.c.H_kv < 8 ? p.c.H_kv : 8;
+  // the most pages a run of max_new tokens can touch
+  const dim3 grid((p.c.H_kv + warps - 1) / warps, (p.max_new + P - 2) / P + 1, p.c.B);
+  return launch_after(summary_kernel<D, E4M3>, grid, 32 * warps, 0, stream, p);
 }
 
 }  // namespace
 
 int launch_kv_append(const AppendParams& p, cudaStream_t stream) {
-  const int P = 1 << p.c.log2_page;
-  const int heads = 2 * p.c.H_kv + (p.q ? p.H_q : 0);
-  const int units = 128 / P;  // a CTA
-  // the most pages a run of max_new tokens can touch (no tokens still write new_lens)
-  const int segs = p.max_new > 0 ? (p.max_new + P - 2) / P + 1 : 1;
-  const dim3 grid((heads + units - 1) / units, segs, p.c.B);
-  const bool ok = p.c.d == 128 ? (p.c.e4m3 ? launch_after(kv_append_kernel<128, true>, grid, kThreads, 0, stream, p)
-                                           : launch_after(kv_append_kernel<128, false>, grid, kThreads, 0, stream, p))
-                               : (p.c.e4m3 ? launch_after(kv_append_kernel<64, true>, grid, kThreads, 0, stream, p)
-                                           : launch_after(kv_append_kernel<64, false>, grid, kThreads, 0, stream, p));
+  const bool ok = p.c.d == 128 ? (p.c.e4m3 ? launch<128, true>(p, stream) : launch<128, false>(p, stream))
+                               : (p.c.e4m3 ? launch<64, true>(p, stream) : launch<64, false>(p, stream));
   return ok ? 0 : -1;
 }
 
