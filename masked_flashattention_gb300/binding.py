@@ -9,6 +9,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 
 import torch
 
@@ -490,21 +491,22 @@ class KVCache:
         if v_shape != shape or v.dtype != k.dtype or v.device != k.device:
             raise ValueError("v must have the shape, type and device of k")
         n, H, P, d = shape
+        self.device, self.index = k.device, k.get_device()
         e4m3 = k.dtype == torch.float8_e4m3fn
         for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
             if (t is not None) != e4m3:
                 raise ValueError("an e4m3 cache takes k_scale and v_scale, a bf16 cache neither")
             if e4m3:
-                _kv_tensor(t, name, torch.float32, (H,), k.device)
+                _kv_tensor(t, name, torch.float32, (H,), self.index)
         if (summary is None) != (summary_scale is None):
             raise ValueError("summary and summary_scale come together")
         if summary is not None:
-            _kv_tensor(summary, "summary", torch.int8, (n, H, 2, d), k.device)
-            _kv_tensor(summary_scale, "summary_scale", torch.float32, (n, H), k.device)
+            _kv_tensor(summary, "summary", torch.int8, (n, H, 2, d), self.index)
+            _kv_tensor(summary_scale, "summary_scale", torch.float32, (n, H), self.index)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.summary, self.summary_scale = summary, summary_scale
         self.num_pages, self.H_kv, self.page_size, self.d = n, H, P, d
-        self.device = k.device
+        self.scale = 1.0 / math.sqrt(d)  # of scores, where a call names none
         self.status = torch.zeros(1, dtype=torch.int32, device=k.device)
         self.c = cm_kv_cache(n, P, H, d, CM_KV_E4M3 if e4m3 else CM_KV_BF16, k_stride, v_stride,
                              k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale),
@@ -528,33 +530,54 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _kv_tensor(t, name, dtype, shape, device):
-    if not (t.dtype == dtype and t.shape == shape and t.device == device and t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on {device}")
+def _kv_tensor(t, name, dtype, shape, device: int):
+    if not (t.dtype is dtype and t.shape == shape and t.get_device() == device
+            and t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on cuda:{device}")
+
+
+# These calls are a few microseconds of GPU work each, so their checks are written to be quick: one
+# device number instead of device objects, strides read once, one constructor for a whole struct.
+def _kv_stream(cache: KVCache, stream) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(cache.index)
+    return _stream(stream)
 
 
 def _kv_seqs(cache: KVCache, page_table, lens) -> cm_kv_seqs:
-    dev = cache.device
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"the cache is on {dev}, which is not the current device")
-    if not (page_table.dim() == 2 and page_table.dtype == torch.int32
-            and page_table.device == dev and page_table.is_contiguous()):
-        raise ValueError(f"page_table must be a contiguous int32 tensor [B, max_pages] on {dev}")
+    dev = cache.index
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"the cache is on {cache.device}, which is not the current device")
+    if not (page_table.dim() == 2 and page_table.dtype is torch.int32
+            and page_table.get_device() == dev and page_table.is_contiguous()):
+        raise ValueError("page_table must be a contiguous int32 tensor [B, max_pages] on "
+                         f"{cache.device}")
     B, n = page_table.shape
     _kv_tensor(lens, "lens", torch.int32, (B,), dev)
     return cm_kv_seqs(B, n, page_table.data_ptr(), lens.data_ptr())
 
 
 def _tokens(t, name, cache: KVCache, packed: bool):
-    """Strides {sequence, head, token} of new tokens: packed [n, H, d] or padded [B, H, T, d]."""
-    if not (t.dtype == torch.bfloat16 and t.device == cache.device
-            and t.dim() == (3 if packed else 4) and t.shape[-1] == cache.d
-            and t.stride(-1) == 1):
+    """Shape and strides {sequence, head, token} of new tokens: packed [n, H, d] or padded
+    [B, H, T, d].  The stride of an axis with one entry is 0: any will do."""
+    shape, s = t.shape, t.stride()
+    if not (t.dtype is torch.bfloat16 and t.get_device() == cache.index
+            and len(s) == (3 if packed else 4) and shape[-1] == cache.d and s[-1] == 1):
         raise ValueError(f"{name} must be a bf16 tensor " +
                          ("[n, H, d]" if packed else "[B, H, T, d]") +
                          f" on {cache.device} with d = {cache.d} contiguous")
-    s = [x if n > 1 else 0 for x, n in zip(t.stride(), t.shape)]  # one row: any stride will do
-    return (0, s[1], s[0]) if packed else s[:3]
+    if 1 in shape:
+        s = [x if n > 1 else 0 for n, x in zip(shape, s)]
+    return shape, (0, s[1], s[0]) if packed else s[:3]
+
+
+_NONE3 = (0, 0, 0)
+_NEW = struct.Struct("5P15q2P6i2P")  # cm_kv_new, field by field
+assert _NEW.size == ctypes.sizeof(cm_kv_new)
+
+
+def _addr(t):
+    return 0 if t is None else t.data_ptr()
 
 
 def cm_kv_append(cache: KVCache, page_table, lens, k, v, q=None, q_out=None, k_out=None, rope=None,
@@ -568,48 +591,47 @@ def cm_kv_append(cache: KVCache, page_table, lens, k, v, q=None, q_out=None, k_o
     [positions, rot_dim / 2, 2] of cosines and sines.  new_lens (int32 [B]) receives the new
     lengths."""
     seqs = _kv_seqs(cache, page_table, lens)
-    dev, packed = cache.device, cu_new is not None
-    t = cm_kv_new()
-    t.k_stride[:] = _tokens(k, "k", cache, packed)
-    t.v_stride[:] = _tokens(v, "v", cache, packed)
-    shape = k.shape
-    if shape[1] != cache.H_kv or v.shape != shape or not (packed or shape[0] == seqs.B):
+    B, dev, packed = seqs.B, cache.index, cu_new is not None
+    shape, ks = _tokens(k, "k", cache, packed)
+    v_shape, vs = _tokens(v, "v", cache, packed)
+    if shape[1] != cache.H_kv or v_shape != shape or not (packed or shape[0] == B):
         raise ValueError("k and v must have the cache's heads, one shape and one row a sequence")
     n = shape[0] if packed else shape[2]
-    t.k, t.v = k.data_ptr(), v.data_ptr()
+    qs = qos = kos = _NONE3
+    H_q = rope_len = rot_dim = 0
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out come together")
     if q is not None:
-        t.q_stride[:] = _tokens(q, "q", cache, packed)
-        t.q_out_stride[:] = _tokens(q_out, "q_out", cache, packed)
-        if q.shape != q_out.shape or q.shape[0] != shape[0] or q.shape[2:] != shape[2:]:
+        q_shape, qs = _tokens(q, "q", cache, packed)
+        o_shape, qos = _tokens(q_out, "q_out", cache, packed)
+        H_q = q_shape[1]
+        if q_shape != o_shape or q_shape[0] != shape[0] or q_shape[2:] != shape[2:]:
             raise ValueError("q and q_out must have one shape, with the tokens of k")
-        t.q, t.q_out, t.H_q = q.data_ptr(), q_out.data_ptr(), q.shape[1]
     if k_out is not None:
-        t.k_out_stride[:] = _tokens(k_out, "k_out", cache, packed)
-        if k_out.shape != shape:
+        o_shape, kos = _tokens(k_out, "k_out", cache, packed)
+        if o_shape != shape:
             raise ValueError("k_out must have the shape of k")
-        t.k_out = k_out.data_ptr()
     if packed:
         if n_new is not None:
             raise ValueError("n_new is for padded tokens, cu_new for packed ones")
-        _kv_tensor(cu_new, "cu_new", torch.int32, (seqs.B + 1,), dev)
-        t.cu_new = cu_new.data_ptr()
+        _kv_tensor(cu_new, "cu_new", torch.int32, (B + 1,), dev)
     elif n_new is not None:
-        _kv_tensor(n_new, "n_new", torch.int32, (seqs.B,), dev)
-        t.n_new = n_new.data_ptr()
-    t.n_tokens, t.max_new = n, n if max_new is None else max_new
+        _kv_tensor(n_new, "n_new", torch.int32, (B,), dev)
     if rope is not None:
-        if not (rope.dim() == 3 and rope.shape[2] == 2):
+        rope_len, half, two = rope.shape
+        if two != 2:
             raise ValueError("rope must be [positions, rot_dim / 2, 2]")
-        _kv_tensor(rope, "rope", torch.float32, rope.shape, dev)
-        t.rope, t.rope_len, t.rot_dim = rope.data_ptr(), rope.shape[0], 2 * rope.shape[1]
-        t.interleaved = interleaved
+        _kv_tensor(rope, "rope", torch.float32, (rope_len, half, 2), dev)
+        rot_dim = 2 * half
     if new_lens is not None:
-        _kv_tensor(new_lens, "new_lens", torch.int32, (seqs.B,), dev)
-        t.new_lens = new_lens.data_ptr()
-    _check(lib().cm_kv_append(cache._ref, ctypes.byref(seqs), ctypes.byref(t), _stream(stream)),
-           "cm_kv_append")
+        _kv_tensor(new_lens, "new_lens", torch.int32, (B,), dev)
+    tok = cm_kv_new.from_buffer_copy(_NEW.pack(
+        k.data_ptr(), v.data_ptr(), _addr(q), _addr(q_out), _addr(k_out), *ks, *vs, *qs, *qos, *kos,
+        _addr(cu_new), _addr(n_new), n, n if max_new is None else max_new, H_q, rot_dim,
+        interleaved, rope_len, _addr(rope), _addr(new_lens)))
+    rc = lib().cm_kv_append(cache._ref, ctypes.byref(seqs), ctypes.byref(tok),
+                            _kv_stream(cache, stream))
+    _check(rc, "cm_kv_append")
 
 
 def cm_attn_decode_workspace_size(B: int, H_q: int, H_kv: int, d: int) -> int:
@@ -620,11 +642,17 @@ def cm_attn_decode_workspace_size(B: int, H_q: int, H_kv: int, d: int) -> int:
 
 
 def _one_token(t, name, cache: KVCache, B: int):
-    if not (t.dtype == torch.bfloat16 and t.dim() == 3 and t.device == cache.device
-            and t.shape[0] == B and t.shape[2] == cache.d and t.stride(2) == 1):
+    shape, s = t.shape, t.stride()
+    if not (t.dtype is torch.bfloat16 and len(s) == 3 and t.get_device() == cache.index
+            and shape[0] == B and shape[2] == cache.d and s[2] == 1):
         raise ValueError(f"{name} must be a bf16 tensor [B, H_q, d] on {cache.device} with d = "
                          f"{cache.d} contiguous")
-    return _Strides2(*(x if n > 1 else 0 for x, n in zip(t.stride()[:2], t.shape)))
+    return _Strides2(s[0] if B > 1 else 0, s[1] if shape[1] > 1 else 0)
+
+
+def _workspace(w, cache: KVCache):
+    if not (w.get_device() == cache.index and w.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous tensor on {cache.device}")
 
 
 def cm_attn_decode(cache: KVCache, page_table, lens, q, o, lse, workspace: torch.Tensor,
@@ -634,33 +662,28 @@ def cm_attn_decode(cache: KVCache, page_table, lens, q, o, lse, workspace: torch
     [B, H_q, d]; lse fp32 [B, H_q] or None.  desc: the mask, whose row lens[b] - 1 the token sees by;
     or sel (int32 [B, H_kv, n]) with nsel (int32 [B, H_kv]): the pages to attend to."""
     seqs = _kv_seqs(cache, page_table, lens)
-    B, H = seqs.B, q.shape[1]
+    B, dev, H = seqs.B, cache.index, q.shape[1]
     qs, os = _one_token(q, "q", cache, B), _one_token(o, "o", cache, B)
-    if o.shape != q.shape:
+    if o.shape[1] != H:
         raise ValueError("o shape mismatch")
     if lse is not None:
-        _kv_tensor(lse, "lse", torch.float32, (B, H), cache.device)
+        _kv_tensor(lse, "lse", torch.float32, (B, H), dev)
     sel_max = 0
     if (sel is None) != (nsel is None):
         raise ValueError("sel and nsel come together")
     if sel is not None:
         sel_max = sel.shape[-1]
-        _kv_tensor(sel, "sel", torch.int32, (B, cache.H_kv, sel_max), cache.device)
-        _kv_tensor(nsel, "nsel", torch.int32, (B, cache.H_kv), cache.device)
+        _kv_tensor(sel, "sel", torch.int32, (B, cache.H_kv, sel_max), dev)
+        _kv_tensor(nsel, "nsel", torch.int32, (B, cache.H_kv), dev)
     _workspace(workspace, cache)
-    if desc is not None and desc.itab_f.device != cache.device:
+    if desc is not None and desc.itab_f.get_device() != dev:
         raise ValueError(f"desc must be on {cache.device}")
-    scale = 1.0 / math.sqrt(cache.d) if scale is None else scale
-    _check(lib().cm_attn_decode(cache._ref, ctypes.byref(seqs),
-                                ctypes.byref(desc.c) if desc is not None else None, _ptr(sel),
-                                _ptr(nsel), sel_max, q.data_ptr(), qs, o.data_ptr(), os, _ptr(lse),
-                                H, scale, workspace.data_ptr(), workspace.nbytes, _stream(stream)),
-           "cm_attn_decode")
-
-
-def _workspace(w, cache: KVCache):
-    if not (w.device == cache.device and w.is_contiguous()):
-        raise ValueError(f"workspace must be a contiguous tensor on {cache.device}")
+    rc = lib().cm_attn_decode(cache._ref, ctypes.byref(seqs),
+                              None if desc is None else ctypes.byref(desc.c), _ptr(sel),
+                              _ptr(nsel), sel_max, q.data_ptr(), qs, o.data_ptr(), os, _ptr(lse),
+                              H, cache.scale if scale is None else scale, workspace.data_ptr(),
+                              workspace.nbytes, _kv_stream(cache, stream))
+    _check(rc, "cm_attn_decode")
 
 
 def cm_select_pages_workspace_size(B: int, H_kv: int, max_pages: int) -> int:
@@ -682,14 +705,14 @@ def cm_select_pages(cache: KVCache, page_table, lens, q, sel, nsel, workspace: t
         raise ValueError("the cache has no page summaries")
     if not (sel.dim() == 3 and sel.shape[2] > 0):
         raise ValueError("sel must be [B, H_kv, n]")
-    _kv_tensor(sel, "sel", torch.int32, (B, cache.H_kv, sel.shape[2]), cache.device)
-    _kv_tensor(nsel, "nsel", torch.int32, (B, cache.H_kv), cache.device)
+    _kv_tensor(sel, "sel", torch.int32, (B, cache.H_kv, sel.shape[2]), cache.index)
+    _kv_tensor(nsel, "nsel", torch.int32, (B, cache.H_kv), cache.index)
     _workspace(workspace, cache)
     qs = _one_token(q, "q", cache, B)
     _check(lib().cm_select_pages(cache._ref, ctypes.byref(seqs), q.data_ptr(), qs, q.shape[1],
                                  keep_first, keep_last, sel.data_ptr(), nsel.data_ptr(),
                                  sel.shape[2], workspace.data_ptr(), workspace.nbytes,
-                                 _stream(stream)),
+                                 _kv_stream(cache, stream)),
            "cm_select_pages")
 
 
