@@ -31,8 +31,6 @@
 namespace cm {
 namespace {
 
-constexpr int kPairs = 4;           // warp pairs of a CTA
-constexpr int kThreads = 64 * kPairs;
 constexpr int kTileKeys = 32;
 constexpr int kMaxCtas = 320;
 constexpr int kMaxIntervals = 8;
@@ -44,28 +42,38 @@ constexpr int kFirst = 1;   // first tile of the warp's part of the row
 constexpr int kLast = 2;    // last tile of that part
 constexpr int kStarts = 4;  // the part begins where the row begins
 constexpr int kEnds = 8;    // the part ends where the row ends
+constexpr int kFlagBits = 4;  // above them: the CTAs that hold parts of the row
 
+// Shared memory: 32 keys of 128 bf16 channels, K and V, are 16 KB, and 4 pairs with 3 such stages keep
+// 100 KB or more of an SM's reads in flight, twice what the memory's latency asks for.  The smaller rows take
+// more instructions a byte, so 8 pairs share the ring's memory (one computing warp a scheduler
+// left an e4m3 cache at 47 % of the bandwidth).  Their 16 warps start with 128 registers a thread and
+// trade: 184 for a computing warp, 72 for a fetching one.
 template <int D, bool E4M3, int NB>
 struct Cfg {
   static constexpr int kItem = E4M3 ? 1 : 2;
   static constexpr int kRowBytes = D * kItem;
+  static constexpr int kPairs = kRowBytes == 256 ? 4 : 8;  // warp pairs of a CTA
+  static constexpr int kThreads = 64 * kPairs;
   static constexpr int kBoxBytes = kRowBytes < 128 ? kRowBytes : 128;  // inner width of a TMA box
   static constexpr int kBoxes = kRowBytes / kBoxBytes;
   static constexpr int kMatrix = kTileKeys * kRowBytes;
   static constexpr int kStage = 2 * kMatrix;  // K, then V
-  static constexpr int kStages = 49152 / kStage < 8 ? 49152 / kStage : 8;
   static constexpr int kHeads = 8 * NB;
-  static constexpr int kHeadPitch = D + 4;  // floats; keeps a warp's fragment stores free of conflicts
+  // floats of a head in a part: 4 spare keep a warp's fragment stores free of conflicts, where there is room
+  static constexpr int kHeadPitch = NB == 1 ? D + 4 : D;
   static constexpr int kPiece = kHeads * kHeadPitch * 4 + 2 * kHeads * 4;  // O, m, l
+  static constexpr int kFit = (static_cast<int>(kSmemMax) - 1024 - kPairs * kPiece) / (kPairs * kStage);
+  static constexpr int kStages = kFit < 8 ? kFit : 8;
   static constexpr int kRing = kPairs * kStages * kStage;
   static constexpr int kOffPiece = kRing;
   static constexpr int kOffMeta = kOffPiece + kPairs * kPiece;
   static constexpr int kOffBars = kOffMeta + kPairs * kStages * 16;
   static constexpr int kOffHead = kOffBars + kPairs * kStages * 16;   // int4 per piece
   static constexpr int kOffMisc = kOffHead + 2 * kPairs * 16;         // starts, counts, abort flag
-  static constexpr int kSmem = kOffMisc + 128;
-  static_assert(kSmem <= static_cast<int>(kSmemMax), "shared memory");
-  static_assert(kPairs * kPiece >= kThreads * 8, "the scan borrows the pieces' memory");
+  static constexpr int kSmem = kOffMisc + 256;
+  static_assert(kStages >= 2 && kSmem <= static_cast<int>(kSmemMax), "shared memory");
+  static_assert(kOffPiece % 16 == 0 && kPiece % 16 == 0 && kOffMeta % 16 == 0, "alignment");
   static_assert(kStages * kStage >= kPiece, "the last piece of a warp borrows its ring");
 };
 
@@ -87,6 +95,7 @@ struct DecodeArgs {
   DecodeParams p;
   int chunks;   // rows of one key-value head: ceil(group / heads of a row)
   int group;
+  int heads;    // of a row: 8 or 16
   int units;    // B, or B * H_kv where pages are selected
   int rows;     // of a unit
   int ctas;
@@ -243,6 +252,7 @@ struct Chunk {
   int page0, page1;      // pages of the tile (page1: second half of a tile of two 16-key pages); -1: none
   int key0, key1;        // first keys of these
   bool full;             // every key of the tile is visible
+  bool whole;            // the chunk is a whole row
 };
 
 struct Walk {
@@ -253,15 +263,29 @@ struct Walk {
 
 template <int D>
 __device__ __forceinline__ void next_chunk(const DecodeArgs& a, Walk& w, Chunk& k, int lane) {
-  k.n = 0;
-  if (w.pos >= w.end) return;
+  if (w.pos >= w.end) {
+    k.n = 0;
+    return;
+  }
   while (w.c >= w.plan.tiles || w.m >= a.rows) {  // next row, next unit (some have no tiles)
     if (w.plan.tiles > 0 && w.m + 1 < a.rows) {
       ++w.m;
       w.c = 0;
+      if (k.whole && w.end - w.pos >= w.plan.tiles) {  // the last chunk was all of a row with the same tiles
+        ++k.row;
+        const int bh = k.row / a.chunks;
+        k.h = bh - bh / a.p.c.H_kv * a.p.c.H_kv;
+        k.n = w.plan.tiles;
+        w.c = k.n;
+        w.pos += k.n;
+        return;
+      }
     } else {
       ++w.u;
-      if (w.u >= a.units) return;  // not reached: the run ends with the last tile
+      if (w.u >= a.units) {  // not reached: the run ends with the last tile
+        k.n = 0;
+        return;
+      }
       w.m = 0;
       w.c = 0;
       w.plan = make_plan(a, w.u, lane);
@@ -274,6 +298,7 @@ __device__ __forceinline__ void next_chunk(const DecodeArgs& a, Walk& w, Chunk& 
   k.h = bh - bh / p.c.H_kv * p.c.H_kv;
   k.c0 = w.c;
   k.n = static_cast<int>(min(min(static_cast<int64_t>(32), static_cast<int64_t>(w.plan.tiles - w.c)), w.end - w.pos));
+  k.whole = k.n == w.plan.tiles;
   const int c = w.c + lane;
   const bool in = lane < k.n;
   const int pages = (w.plan.len + P - 1) >> log2_page;
@@ -366,6 +391,7 @@ __device__ __forceinline__ int fetch(const DecodeArgs& a, const CUtensorMap* kma
   int issued = 0;
   const int64_t begin = w.pos, end = w.end;
   Chunk next;
+  next.whole = false;
   next_chunk<D>(a, w, next, lane);
   bool ok = true;
   while (next.n > 0 && ok) {
@@ -407,7 +433,7 @@ __device__ __forceinline__ int fetch(const DecodeArgs& a, const CUtensorMap* kma
         if (c == plan.tiles - 1) flags |= kLast | kEnds;
         if (at + j == end - 1) flags |= kLast;
         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(meta + stage * 16), "r"(cur.row),
-                     "r"(seen), "r"(flags), "r"(parts)
+                     "r"(seen), "r"(flags | (parts << kFlagBits)), "r"(next.n > 0 ? next.row : -1)
                      : "memory");
         const uint32_t k_at = ring + stage * C::kStage, v_at = k_at + C::kMatrix;
         const int half = log2_page == 4 ? 2 : 1;  // boxes of 16 or 32 keys
@@ -454,38 +480,48 @@ __device__ __forceinline__ int fetch(const DecodeArgs& a, const CUtensorMap* kma
 // Query fragments of a row: B operand [16 channels x 8 heads] of each step, thread (head lane / 4,
 // channels by lane % 4).  bf16 steps take channels 2t, 2t+1 and 2t+8, 2t+9; e4m3 steps take
 // 4t .. 4t+3, the order in which a lane gets the keys' bytes.
-template <int D, bool E4M3, int NB>
-__device__ __forceinline__ void load_q(const DecodeArgs& a, int row, int lane,
-                                       uint32_t (&q)[NB][D / 16][2], float (&scale)[NB][2]) {
+template <int D, bool E4M3>
+__device__ __forceinline__ void read_q(const DecodeArgs& a, int row, int n, int lane, uint32_t (&q)[D / 16][2]) {
   const DecodeParams& p = a.p;
   const int bh = row / a.chunks, chunk = row - bh * a.chunks;
   const int b = bh / p.c.H_kv, h = bh - b * p.c.H_kv;
-  const float base = p.scale * 1.4426950408889634f * (E4M3 ? p.c.k_scale[h] : 1.f);
+  const int i = chunk * a.heads + n * 8 + lane / 4;
+  const bool in = i < a.group;
+  const __nv_bfloat16* src = p.q + b * p.qs.seq + static_cast<int64_t>(h * a.group + (in ? i : 0)) * p.qs.head;
+#pragma unroll
+  for (int s = 0; s < D / 16; ++s) {
+    if constexpr (E4M3) {
+      const uint2 w = in ? *reinterpret_cast<const uint2*>(src + s * 16 + (lane & 3) * 4) : make_uint2(0, 0);
+      q[s][0] = w.x;
+      q[s][1] = w.y;
+    } else {
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        q[s][x] = in ? *reinterpret_cast<const uint32_t*>(src + s * 16 + x * 8 + (lane & 3) * 2) : 0u;
+    }
+  }
+}
+
+// Factor of the scores (log2 units) of the lane's two columns; for an e4m3 cache the fragments become
+// fp16, scaled by a power of two per head to a largest value in [1, 2).
+template <int D, bool E4M3, int NB>
+__device__ __forceinline__ void scale_q(const DecodeArgs& a, int row, int lane, uint32_t (&q)[NB][D / 16][2],
+                                        float (&scale)[NB][2]) {
+  const int bh = row / a.chunks;
+  const float base = a.p.scale * 1.4426950408889634f * (E4M3 ? a.p.c.k_scale[bh - bh / a.p.c.H_kv * a.p.c.H_kv] : 1.f);
 #pragma unroll
   for (int n = 0; n < NB; ++n) {
-    const int i = chunk * 8 * NB + n * 8 + lane / 4;
-    const bool in = i < a.group;
-    const __nv_bfloat16* src = p.q + b * p.qs.seq + static_cast<int64_t>(h * a.group + (in ? i : 0)) * p.qs.head;
     if constexpr (!E4M3) {
-#pragma unroll
-      for (int s = 0; s < D / 16; ++s)
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-          q[n][s][x] = in ? *reinterpret_cast<const uint32_t*>(src + s * 16 + x * 8 + (lane & 3) * 2) : 0u;
       scale[n][0] = scale[n][1] = base;
     } else {
       float top = 0.f;
 #pragma unroll
-      for (int s = 0; s < D / 16; ++s) {
-        const uint2 w = in ? *reinterpret_cast<const uint2*>(src + s * 16 + (lane & 3) * 4) : make_uint2(0, 0);
-        q[n][s][0] = w.x;
-        q[n][s][1] = w.y;
+      for (int s = 0; s < D / 16; ++s)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           top = fmaxf(top, fabsf(__uint_as_float(q[n][s][x] << 16)));
           top = fmaxf(top, fabsf(__uint_as_float(q[n][s][x] & 0xFFFF0000u)));
         }
-      }
       top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
       const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -100), 100);
@@ -499,7 +535,7 @@ __device__ __forceinline__ void load_q(const DecodeArgs& a, int row, int lane,
           q[n][s][x] = *reinterpret_cast<const uint32_t*>(&f);
         }
       const float mine = base * pow2_bits(e);
-      scale[n][0] = __shfl_sync(0xFFFFFFFFu, mine, (lane & 3) * 8);      // heads of the lane's columns
+      scale[n][0] = __shfl_sync(0xFFFFFFFFu, mine, (lane & 3) * 8);  // heads of the lane's columns
       scale[n][1] = __shfl_sync(0xFFFFFFFFu, mine, (lane & 3) * 8 + 4);
     }
   }
@@ -709,6 +745,11 @@ __device__ __forceinline__ void compute(const DecodeArgs& a, char* smem, uint32_
                                         uint32_t bars, int pair, const WaitCtl& wait, int lane) {
   using C = Cfg<D, E4M3, NB>;
   State<D, E4M3, NB> t;
+  // the next row's queries, on their way while the last tile of a row is computed; 16 heads' would take the
+  // registers of the accumulators
+  constexpr bool kAhead = NB == 1;
+  uint32_t ahead[kAhead ? D / 16 : 1][2];
+  int ahead_row = -1;
   int4* heads = reinterpret_cast<int4*>(smem + C::kOffHead) + 2 * pair;
   bool starts = false;
   for (int done = 0;; ++done) {
@@ -720,7 +761,21 @@ __device__ __forceinline__ void compute(const DecodeArgs& a, char* smem, uint32_
     if (row < 0) return;
     if (flags & kFirst) {
       starts = flags & kStarts;
-      load_q<D, E4M3, NB>(a, row, lane, t.q, t.scale);
+      if constexpr (kAhead) {
+        if (ahead_row == row) {
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            t.q[0][i][0] = ahead[i][0];
+            t.q[0][i][1] = ahead[i][1];
+          }
+        } else {
+          read_q<D, E4M3>(a, row, 0, lane, t.q[0]);
+        }
+      } else {
+#pragma unroll
+        for (int n = 0; n < NB; ++n) read_q<D, E4M3>(a, row, n, lane, t.q[n]);
+      }
+      scale_q<D, E4M3, NB>(a, row, lane, t.q, t.scale);
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
         t.m[n][0] = t.m[n][1] = -INFINITY;
@@ -730,6 +785,10 @@ __device__ __forceinline__ void compute(const DecodeArgs& a, char* smem, uint32_
 #pragma unroll
           for (int i = 0; i < 4; ++i) t.o[n][j][i] = 0.f;
       }
+    }
+    if constexpr (kAhead) {
+      ahead_row = flags & kLast ? static_cast<int>(x.w) : -1;
+      if (ahead_row >= 0) read_q<D, E4M3>(a, ahead_row, 0, lane, ahead);
     }
     const uint32_t k_at = ring + stage * C::kStage;
     compute_tile<D, E4M3, NB>(t, k_at, k_at + C::kMatrix, x.y, lane);
@@ -800,7 +859,7 @@ __device__ __forceinline__ void compute(const DecodeArgs& a, char* smem, uint32_
       }
     }
     if (lane == 0)
-      heads[slot] = make_int4(row, (starts ? kStarts : 0) | (flags & kEnds), static_cast<int>(x.w), 1);
+      heads[slot] = make_int4(row, (starts ? kStarts : 0) | (flags & kEnds), flags >> kFlagBits, 1);
   }
 }
 
@@ -812,21 +871,21 @@ __device__ __forceinline__ void join_warps(const DecodeArgs& a, char* smem, int 
   const int4* heads = reinterpret_cast<const int4*>(smem + C::kOffHead);
   const int c0 = (tid & 15) * 4;  // channels c0 .. c0+3 of each 64
   int carried = 0, carried_row = 0;
-  for (int i = 0; i < 2 * kPairs;) {
+  for (int i = 0; i < 2 * C::kPairs;) {
     if (!heads[i].w) {
       ++i;
       continue;
     }
     const int4 first = heads[i];
     int j = i, ends = 0;
-    while (j < 2 * kPairs && (!heads[j].w || heads[j].x == first.x)) {
+    while (j < 2 * C::kPairs && (!heads[j].w || heads[j].x == first.x)) {
       if (heads[j].w) ends = heads[j].y & kEnds;
       ++j;
     }
     const bool starts = first.y & kStarts;
     const RowAt r = row_at<E4M3, NB>(a, first.x);
     const Part out = part_at<D>(a.p.workspace, C::kHeads, blockIdx.x, starts ? 1 : 0);
-    for (int h = tid >> 4; h < r.heads; h += 2 * kPairs) {
+    for (int h = tid >> 4; h < r.heads; h += 2 * C::kPairs) {
       float m = -INFINITY, l = 0.f, o[N];
 #pragma unroll
       for (int c = 0; c < N; ++c) o[c] = 0.f;
@@ -878,16 +937,16 @@ __device__ __forceinline__ void join_warps(const DecodeArgs& a, char* smem, int 
 }
 
 template <int D, bool E4M3, int NB>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D, E4M3, NB>::kThreads, 1)
     decode_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap) {
   using C = Cfg<D, E4M3, NB>;
   extern __shared__ __align__(1024) char smem[];  // the swizzled tiles need the alignment
   const uint32_t base = smem_u32(smem);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
-  int64_t* starts = reinterpret_cast<int64_t*>(smem + C::kOffMisc);          // [kPairs]: unit
-  int64_t* rests = starts + kPairs;                                          // [kPairs]: tiles into it
-  int64_t* total_at = rests + kPairs;
+  int64_t* starts = reinterpret_cast<int64_t*>(smem + C::kOffMisc);          // [C::kPairs]: unit
+  int64_t* rests = starts + C::kPairs;                                          // [C::kPairs]: tiles into it
+  int64_t* total_at = rests + C::kPairs;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(total_at + 1);
   let_next_start();
   if ((base & 1023u) != 0) {
@@ -898,11 +957,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     return;
   }
-  if (tid < kPairs * C::kStages) {
+  if (tid < C::kPairs * C::kStages) {
     mbar_init(base + C::kOffBars + tid * 16, 1);
     mbar_init(base + C::kOffBars + tid * 16 + 8, 1);
   }
-  if (tid < 2 * kPairs) reinterpret_cast<int4*>(smem + C::kOffHead)[tid] = make_int4(0, 0, 0, 0);
+  if (tid < 2 * C::kPairs) reinterpret_cast<int4*>(smem + C::kOffHead)[tid] = make_int4(0, 0, 0, 0);
   if (tid == 0) {
     *abort_flag = 0;
     tma_prefetch_desc(&kmap);
@@ -912,7 +971,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   wait_for_previous();
 
   // tiles of all units: each thread adds up a run of them, then a scan over the threads
-  const int per = (a.units + kThreads - 1) / kThreads;
+  const int per = (a.units + C::kThreads - 1) / C::kThreads;
   const int u0 = min(tid * per, a.units), u1 = min(u0 + per, a.units);
   int64_t mine = 0;
   for (int u = u0; u < u1; ++u) {
@@ -940,17 +999,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   for (int w = 0; w < warp; ++w) sum += warp_sum[w];
   int64_t total = 0;
-  for (int w = 0; w < kThreads / 32; ++w) total += warp_sum[w];
+  for (int w = 0; w < C::kThreads / 32; ++w) total += warp_sum[w];
   const int64_t run = max((total + a.ctas - 1) / a.ctas, a.min_run);  // of a CTA
   const int64_t cta0 = min(run * blockIdx.x, total), cta1 = min(cta0 + run, total);
-  const int64_t share = (cta1 - cta0 + kPairs - 1) / kPairs;          // of a warp
+  const int64_t share = (cta1 - cta0 + C::kPairs - 1) / C::kPairs;          // of a warp
 #pragma unroll
-  for (int w = 0; w < kPairs; ++w) {
+  for (int w = 0; w < C::kPairs; ++w) {
     const int64_t at = cta0 + w * share;
     if (at < cta1 && at >= sum - mine && at < sum) {
       int64_t from = sum - mine;
       int u = u0;
-      for (;; ++u) {
+      for (; u + 1 < u1; ++u) {
         const int64_t n = static_cast<int64_t>(unit_tiles(a, u, false)) * a.rows;
         if (at < from + n) break;
         from += n;
@@ -962,14 +1021,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
 
   const WaitCtl wait{abort_flag, a.p.c.status, a.wait_ns};
-  const int pair = warp & (kPairs - 1);
+  const int pair = warp & (C::kPairs - 1);
   const int64_t at = min(cta0 + pair * share, cta1), until = min(at + share, cta1);
   const uint32_t ring = base + pair * C::kStages * C::kStage;
   const uint32_t meta = base + C::kOffMeta + pair * C::kStages * 16;
   const uint32_t bars = base + C::kOffBars + pair * C::kStages * 16;
   int fetched = 0, rest = 0;
+  if constexpr (C::kPairs == 8) {
+    if (warp >= C::kPairs) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+  }
   if (at < until) {
-    if (warp >= kPairs) {
+    if (warp >= C::kPairs) {
       Walk w;
       w.u = static_cast<int>(starts[pair]);
       w.plan = make_plan(a, w.u, lane);
@@ -990,7 +1053,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) reinterpret_cast<int4*>(a.p.workspace)[blockIdx.x] = make_int4(0, 0, 0, 0);
     return;
   }
-  if (tid < 32 * kPairs) join_warps<D, E4M3, NB>(a, smem, tid);
+  if (tid < 32 * C::kPairs) join_warps<D, E4M3, NB>(a, smem, tid);
 }
 
 // Joins the parts of a row that several CTAs hold: CTA x's header says how many there are, its own
@@ -1051,7 +1114,7 @@ int launch(const DecodeArgs& a, const CUtensorMap& k, const CUtensorMap& v, cuda
   if (cudaFuncSetAttribute(decode_kernel<D, E4M3, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            C::kSmem) != cudaSuccess)
     return -1;
-  return launch_after(decode_kernel<D, E4M3, NB>, dim3(a.ctas), kThreads, C::kSmem, stream, a, k, v) &&
+  return launch_after(decode_kernel<D, E4M3, NB>, dim3(a.ctas), C::kThreads, C::kSmem, stream, a, k, v) &&
                  launch_after(join_kernel<D, E4M3, NB>, dim3(a.ctas, a.group < C::kHeads ? a.group : C::kHeads), D,
                               0, stream, a)
              ? 0
@@ -1073,11 +1136,12 @@ int launch_attn_decode(const DecodeParams& p, uint64_t wait_ns, cudaStream_t str
   a.p = p;
   a.group = p.H_q / p.c.H_kv;
   const int heads = heads_of(a.group);
+  a.heads = heads;
   a.chunks = (a.group + heads - 1) / heads;
   a.units = p.sel ? p.c.B * p.c.H_kv : p.c.B;
   a.rows = p.sel ? a.chunks : p.c.H_kv * a.chunks;
   a.ctas = sm_count();
-  a.min_run = kPairs;
+  a.min_run = 4;
   a.wait_ns = wait_ns;
   if (a.ctas < 1) return -1;
   CUtensorMap k, v;
