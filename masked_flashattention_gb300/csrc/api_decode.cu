@@ -206,6 +206,7 @@ CM_API int cm_attn_decode(const cm_kv_cache* cache, const cm_kv_seqs* seqs,
   p.H_q = H_q;
   p.scale = scale;
   p.workspace = workspace;
+  if (!cm::decode_fits(p)) return CM_ERR_UNSUPPORTED;
   return cm::launch_attn_decode(p, cm::wait_limit_ns(), static_cast<cudaStream_t>(stream)) == 0
              ? CM_OK
              : CM_ERR_CUDA;

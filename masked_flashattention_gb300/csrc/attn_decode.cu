@@ -91,6 +91,20 @@ __device__ __forceinline__ Part part_at(void* workspace, int heads, int cta, int
   return {f, f + heads * D, f + heads * (D + 1)};
 }
 
+// Division of 0 <= n < 2^31 by a fixed d >= 1: with 2^s >= d > 2^(s-1) and mul = ceil(2^(31+s) / d), the
+// product's error stays below 2^s / 2^(31+s) * n < 1 / d.
+struct Divisor {
+  uint32_t mul, shift;
+  __device__ __forceinline__ int operator()(int n) const {
+    return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * mul) >> shift);
+  }
+};
+Divisor make_divisor(uint32_t d) {
+  uint32_t s = 0;
+  while ((1u << s) < d) ++s;
+  return {static_cast<uint32_t>(((1ull << (31 + s)) + d - 1) / d), 31 + s};
+}
+
 struct DecodeArgs {
   DecodeParams p;
   int chunks;   // rows of one key-value head: ceil(group / heads of a row)
@@ -99,9 +113,19 @@ struct DecodeArgs {
   int units;    // B, or B * H_kv where pages are selected
   int rows;     // of a unit
   int ctas;
-  int64_t min_run;  // fewest tiles a CTA's run is given
+  int min_run;  // least cost a CTA's run is given
+  Divisor by_chunks, by_heads;  // H_kv
   uint64_t wait_ns;
 };
+
+// Sequence, key-value head and place among its rows of a row.
+struct RowIndex {
+  int b, h, chunk;
+};
+__device__ __forceinline__ RowIndex row_index(const DecodeArgs& a, int row) {
+  const int bh = a.by_chunks(row), b = a.by_heads(bh);
+  return {b, bh - b * a.p.c.H_kv, row - bh * a.chunks};
+}
 
 // ---- instructions -----------------------------------------------------------------------------
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -186,23 +210,25 @@ __device__ __forceinline__ int unit_tiles(const DecodeArgs& a, int u, bool repor
   const int len = unit_length(a, b, report);
   if (a.p.sel) return len ? selected_tiles(a, u) : 0;
   if (a.p.itab == nullptr) return (len + kTileKeys - 1) / kTileKeys;
-  int lo[kMaxIntervals], hi[kMaxIntervals], total = 0;
-#pragma unroll
-  for (int n = 0; n < kMaxIntervals; ++n) {
-    const int2 iv = unit_interval(a, b, n, len);
-    lo[n] = iv.x / kTileKeys;
-    hi[n] = (iv.y + kTileKeys - 1) / kTileKeys;
-  }
-#pragma unroll
-  for (int i = 0; i < kMaxIntervals; ++i) {
-    int from = lo[i];
-#pragma unroll
-    for (int j = 0; j < kMaxIntervals; ++j)
-      if (j != i && (lo[j] < lo[i] || (lo[j] == lo[i] && j < i))) from = max(from, hi[j]);
-    total += max(hi[i] - from, 0);
+  // few units and few intervals: small code (cold instructions cost more than the L1 reads here)
+  int total = 0;
+#pragma unroll 1
+  for (int i = 0; i < a.p.NI; ++i) {
+    const int2 x = unit_interval(a, b, i, len);
+    int from = x.x / kTileKeys;
+#pragma unroll 1
+    for (int j = 0; j < a.p.NI; ++j) {
+      const int2 y = unit_interval(a, b, j, len);
+      const int lo = y.x / kTileKeys;
+      if (j != i && (lo < x.x / kTileKeys || (lo == x.x / kTileKeys && j < i)))
+        from = max(from, (y.y + kTileKeys - 1) / kTileKeys);
+    }
+    total += max((x.y + kTileKeys - 1) / kTileKeys - from, 0);
   }
   return total;
 }
+// What a row costs: its tiles, and about one more for its queries, its end and its output.
+__device__ __forceinline__ int row_cost(int tiles) { return tiles ? tiles + 1 : 0; }
 
 // The same by a warp: lane n < 8 holds interval n.
 struct Plan {
@@ -229,15 +255,15 @@ __device__ __forceinline__ Plan make_plan(const DecodeArgs& a, int u, int lane) 
     return w;
   }
   w.from = lo;
-#pragma unroll
-  for (int j = 0; j < kMaxIntervals; ++j) {
+#pragma unroll 1
+  for (int j = 0; j < a.p.NI; ++j) {
     const int lj = __shfl_sync(0xFFFFFFFFu, lo, j), hj = __shfl_sync(0xFFFFFFFFu, hi, j);
     if (j != lane && (lj < lo || (lj == lo && j < lane))) w.from = max(w.from, hj);
   }
   w.cnt = lane < kMaxIntervals ? max(hi - w.from, 0) : 0;
   w.tiles = 0;
-#pragma unroll
-  for (int j = 0; j < kMaxIntervals; ++j) {
+#pragma unroll 1
+  for (int j = 0; j < a.p.NI; ++j) {
     const int lj = __shfl_sync(0xFFFFFFFFu, lo, j), cj = __shfl_sync(0xFFFFFFFFu, w.cnt, j);
     if (lj < lo || (lj == lo && j < lane)) w.off += cj;
     w.tiles += cj;
@@ -255,49 +281,46 @@ struct Chunk {
   bool whole;            // the chunk is a whole row
 };
 
+// Positions count costs: a row's tiles, then one place without a tile.
 struct Walk {
-  int u, m, c;      // unit, row of the unit, tile of the row: what comes next
-  int64_t pos, end; // of the warp's run
+  int u, m, c;   // unit, row of the unit, tile of the row: what comes next
+  int pos, end;  // of the warp's run
   Plan plan;
 };
 
 template <int D>
 __device__ __forceinline__ void next_chunk(const DecodeArgs& a, Walk& w, Chunk& k, int lane) {
-  if (w.pos >= w.end) {
-    k.n = 0;
-    return;
-  }
-  while (w.c >= w.plan.tiles || w.m >= a.rows) {  // next row, next unit (some have no tiles)
-    if (w.plan.tiles > 0 && w.m + 1 < a.rows) {
+  if (w.c >= w.plan.tiles) {  // next row
+    ++w.pos;
+    w.c = 0;
+    if (w.m + 1 < a.rows) {
       ++w.m;
-      w.c = 0;
       if (k.whole && w.end - w.pos >= w.plan.tiles) {  // the last chunk was all of a row with the same tiles
         ++k.row;
-        const int bh = k.row / a.chunks;
-        k.h = bh - bh / a.p.c.H_kv * a.p.c.H_kv;
-        k.n = w.plan.tiles;
-        w.c = k.n;
+        k.h = row_index(a, k.row).h;
+        k.n = w.c = w.plan.tiles;
         w.pos += k.n;
         return;
       }
-    } else {
-      ++w.u;
-      if (w.u >= a.units) {  // not reached: the run ends with the last tile
-        k.n = 0;
-        return;
-      }
+    } else if (w.pos < w.end) {  // next unit that has tiles: there is one, or the run would have ended
       w.m = 0;
-      w.c = 0;
-      w.plan = make_plan(a, w.u, lane);
+      do {
+        if (w.u + 1 >= a.units) {
+          k.n = 0;
+          return;
+        }
+        w.plan = make_plan(a, ++w.u, lane);
+      } while (w.plan.tiles == 0);
     }
   }
+  k.n = max(min(min(32, w.plan.tiles - w.c), w.end - w.pos), 0);
+  if (k.n == 0) return;
   const DecodeParams& p = a.p;
   const int log2_page = p.c.log2_page, P = 1 << log2_page;
   k.row = w.u * a.rows + w.m;
-  const int bh = k.row / a.chunks;  // sequence * H_kv + head
-  k.h = bh - bh / p.c.H_kv * p.c.H_kv;
+  k.h = row_index(a, k.row).h;
+  const int bh = w.plan.b * p.c.H_kv + k.h;
   k.c0 = w.c;
-  k.n = static_cast<int>(min(min(static_cast<int64_t>(32), static_cast<int64_t>(w.plan.tiles - w.c)), w.end - w.pos));
   k.whole = k.n == w.plan.tiles;
   const int c = w.c + lane;
   const bool in = lane < k.n;
@@ -330,8 +353,8 @@ __device__ __forceinline__ void next_chunk(const DecodeArgs& a, Walk& w, Chunk& 
   } else {
     int tile = c;
     if (p.itab) {
-#pragma unroll
-      for (int j = 0; j < kMaxIntervals; ++j) {
+#pragma unroll 1
+      for (int j = 0; j < p.NI; ++j) {
         const int from = __shfl_sync(0xFFFFFFFFu, w.plan.from, j);
         const int off = __shfl_sync(0xFFFFFFFFu, w.plan.off, j);
         const int cnt = __shfl_sync(0xFFFFFFFFu, w.plan.cnt, j);
@@ -349,8 +372,8 @@ __device__ __forceinline__ void next_chunk(const DecodeArgs& a, Walk& w, Chunk& 
   const bool two = log2_page == 4;
   const int end0 = k.key0 + (two ? 16 : kTileKeys);
   if (p.itab) {
-#pragma unroll
-    for (int j = 0; j < kMaxIntervals; ++j) {
+#pragma unroll 1
+    for (int j = 0; j < p.NI; ++j) {
       const int st = __shfl_sync(0xFFFFFFFFu, w.plan.st, j), en = __shfl_sync(0xFFFFFFFFu, w.plan.en, j);
       k.full |= st <= k.key0 && k.key0 + kTileKeys <= en;
     }
@@ -382,14 +405,14 @@ __device__ __forceinline__ bool warp_wait(const WaitCtl& wait, uint32_t bar, uin
 // waited for, were it to give up.
 template <int D, bool E4M3, int NB>
 __device__ __forceinline__ int fetch(const DecodeArgs& a, const CUtensorMap* kmap,
-                                      const CUtensorMap* vmap, Walk w, uint32_t ring,
-                                      uint32_t meta, uint32_t bars, int64_t run, const WaitCtl& wait,
+                                     const CUtensorMap* vmap, Walk w, uint32_t ring,
+                                     uint32_t meta, uint32_t bars, int run, const WaitCtl& wait,
                                      int lane, int& rest) {
   using C = Cfg<D, E4M3, NB>;
   const DecodeParams& p = a.p;
   const int log2_page = p.c.log2_page, P = 1 << log2_page;
   int issued = 0;
-  const int64_t begin = w.pos, end = w.end;
+  const int begin = w.pos, end = w.end;
   Chunk next;
   next.whole = false;
   next_chunk<D>(a, w, next, lane);
@@ -397,9 +420,11 @@ __device__ __forceinline__ int fetch(const DecodeArgs& a, const CUtensorMap* kma
   while (next.n > 0 && ok) {
     const Chunk cur = next;
     const Plan plan = w.plan;  // of cur's unit
-    const int64_t row_begin = w.pos - cur.n - cur.c0, at = w.pos - cur.n;
-    // parts of the row, one a CTA's run
-    const int parts = static_cast<int>((row_begin + plan.tiles - 1) / run - row_begin / run) + 1;
+    const int at = w.pos - cur.n, row_begin = at - cur.c0;
+    // parts of the row, one a CTA's run; asked for where the row is not all this warp's
+    const int parts = row_begin < begin || row_begin + plan.tiles > end
+                          ? (row_begin + plan.tiles - 1) / run - row_begin / run + 1
+                          : 1;
     next_chunk<D>(a, w, next, lane);  // its loads are on their way while cur is fetched
     for (int j = 0; j < cur.n; ++j) {
       const int stage = issued % C::kStages;
@@ -417,8 +442,8 @@ __device__ __forceinline__ int fetch(const DecodeArgs& a, const CUtensorMap* kma
         bool in = key < plan.len;
         if (p.itab) {
           in = false;
-#pragma unroll
-          for (int n = 0; n < kMaxIntervals; ++n) {
+#pragma unroll 1
+          for (int n = 0; n < p.NI; ++n) {
             const int st = __shfl_sync(0xFFFFFFFFu, plan.st, n), en = __shfl_sync(0xFFFFFFFFu, plan.en, n);
             in |= key >= st && key < en;
           }
@@ -483,8 +508,7 @@ __device__ __forceinline__ int fetch(const DecodeArgs& a, const CUtensorMap* kma
 template <int D, bool E4M3>
 __device__ __forceinline__ void read_q(const DecodeArgs& a, int row, int n, int lane, uint32_t (&q)[D / 16][2]) {
   const DecodeParams& p = a.p;
-  const int bh = row / a.chunks, chunk = row - bh * a.chunks;
-  const int b = bh / p.c.H_kv, h = bh - b * p.c.H_kv;
+  const auto [b, h, chunk] = row_index(a, row);
   const int i = chunk * a.heads + n * 8 + lane / 4;
   const bool in = i < a.group;
   const __nv_bfloat16* src = p.q + b * p.qs.seq + static_cast<int64_t>(h * a.group + (in ? i : 0)) * p.qs.head;
@@ -507,8 +531,7 @@ __device__ __forceinline__ void read_q(const DecodeArgs& a, int row, int n, int 
 template <int D, bool E4M3, int NB>
 __device__ __forceinline__ void scale_q(const DecodeArgs& a, int row, int lane, uint32_t (&q)[NB][D / 16][2],
                                         float (&scale)[NB][2]) {
-  const int bh = row / a.chunks;
-  const float base = a.p.scale * 1.4426950408889634f * (E4M3 ? a.p.c.k_scale[bh - bh / a.p.c.H_kv * a.p.c.H_kv] : 1.f);
+  const float base = a.p.scale * 1.4426950408889634f * (E4M3 ? a.p.c.k_scale[row_index(a, row).h] : 1.f);
 #pragma unroll
   for (int n = 0; n < NB; ++n) {
     if constexpr (!E4M3) {
@@ -562,39 +585,57 @@ struct State {
 template <int D, bool E4M3, int NB>
 __device__ __forceinline__ void compute_tile(State<D, E4M3, NB>& t, uint32_t k_at, uint32_t v_at,
                                              uint32_t seen, int lane) {
-  float s[2][NB][4];
+  // One or two warps a scheduler: latencies are hidden within the warp, by loading ahead of the
+  // products and by two sets of sums each.
+  float s[2][NB][4], s2[2][NB][4];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int n = 0; n < NB; ++n)
 #pragma unroll
-      for (int x = 0; x < 4; ++x) s[i][n][x] = 0.f;
+      for (int x = 0; x < 4; ++x) s[i][n][x] = s2[i][n][x] = 0.f;
   // S^T = K Q^T: matrices of ldmatrix are (keys 0-7, 8-15) x (pieces 2j, 2j+1)
+  constexpr int kSteps = D * (E4M3 ? 1 : 2) / 32, kGroup = kSteps < 4 ? kSteps : 4;
   const int row = lane & 15, col = lane >> 4;
 #pragma unroll
-  for (int j = 0; j < D * (E4M3 ? 1 : 2) / 32; ++j)
+  for (int j0 = 0; j0 < kSteps; j0 += kGroup) {
+    uint32_t w[kGroup][2][4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      uint32_t w[4];
-      ldsm4(w, piece_at<D, E4M3>(k_at, i * 16 + row, 2 * j + col));
-      if constexpr (!E4M3) {
+    for (int j = 0; j < kGroup; ++j)
 #pragma unroll
-        for (int n = 0; n < NB; ++n) mma16816<false>(s[i][n], w, t.q[n][j][0], t.q[n][j][1]);
-      } else {
+      for (int i = 0; i < 2; ++i) ldsm4(w[j][i], piece_at<D, E4M3>(k_at, i * 16 + row, 2 * (j0 + j) + col));
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const uint32_t f[4] = {widen_lo(w[2 * x]), widen_lo(w[2 * x + 1]), widen_hi(w[2 * x]), widen_hi(w[2 * x + 1])};
+    for (int j = 0; j < kGroup; ++j)
 #pragma unroll
-          for (int n = 0; n < NB; ++n) mma16816<true>(s[i][n], f, t.q[n][2 * j + x][0], t.q[n][2 * j + x][1]);
+      for (int i = 0; i < 2; ++i) {
+        if constexpr (!E4M3) {
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+            mma16816<false>(j & 1 ? s2[i][n] : s[i][n], w[j][i], t.q[n][j0 + j][0], t.q[n][j0 + j][1]);
+        } else {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t f[4] = {widen_lo(w[j][i][2 * x]), widen_lo(w[j][i][2 * x + 1]), widen_hi(w[j][i][2 * x]),
+                                   widen_hi(w[j][i][2 * x + 1])};
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+              mma16816<true>(x ? s2[i][n] : s[i][n], f, t.q[n][2 * (j0 + j) + x][0], t.q[n][2 * (j0 + j) + x][1]);
+          }
         }
       }
-    }
+  }
+  // values of the first 16 keys, for the second product
+  constexpr int kValues = E4M3 ? D / 32 : D / 16;
+  const int key = E4M3 ? row : (lane & 7) + ((lane >> 4) << 3), piece = E4M3 ? col : (lane >> 3) & 1;
+  uint32_t v[kValues][4];
+#pragma unroll
+  for (int j = 0; j < kValues; ++j) ldsm4t(v[j], piece_at<D, E4M3>(v_at, key, 2 * j + piece));
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int n = 0; n < NB; ++n)
 #pragma unroll
-      for (int x = 0; x < 4; ++x) s[i][n][x] *= t.scale[n][x & 1];
+      for (int x = 0; x < 4; ++x) s[i][n][x] = (s[i][n][x] + s2[i][n][x]) * t.scale[n][x & 1];
   const bool whole = seen == 0xFFFFFFFFu;
   if (!whole) {  // keys of the lane: lane / 4 and 8 further, of both halves
     const uint32_t bits = seen >> (lane >> 2);
@@ -660,7 +701,9 @@ __device__ __forceinline__ void compute_tile(State<D, E4M3, NB>& t, uint32_t k_a
     }
   }
   // O^T += V^T P^T.  Hidden keys' values are cleared: 0 * NaN is no 0.
-  const int key = (lane & 7) + ((lane >> 4) << 3), piece = (lane >> 3) & 1;
+  // bf16: matrices (keys 0-7, piece 2j), (keys 0-7, 2j+1), (keys 8-15, 2j), (keys 8-15, 2j+1);
+  // e4m3: matrices (keys 0-7, 8-15) x (pieces 2j, 2j+1), of which a lane gets channels 2c, 2c+1 (c = lane / 4)
+  // of keys 2t, 2t+1: row r of the product's tile is channel 2r, row r + 8 channel 2r + 1
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     uint32_t keep[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};  // keys 2t, 2t+1 and 8 further
@@ -671,12 +714,11 @@ __device__ __forceinline__ void compute_tile(State<D, E4M3, NB>& t, uint32_t k_a
         keep[x] = (b & 1u ? 0xFFFFu : 0u) | (b & 2u ? 0xFFFF0000u : 0u);
       }
     }
-    if constexpr (!E4M3) {
-      // matrices (keys 0-7, piece 2j), (keys 0-7, 2j+1), (keys 8-15, 2j), (keys 8-15, 2j+1)
 #pragma unroll
-      for (int j = 0; j < D / 16; ++j) {
-        uint32_t w[4];
-        ldsm4t(w, piece_at<D, E4M3>(v_at, i * 16 + key, 2 * j + piece));
+    for (int j = 0; j < kValues; ++j) {
+      uint32_t w[4] = {v[j][0], v[j][1], v[j][2], v[j][3]};
+      if (i == 0) ldsm4t(v[j], piece_at<D, E4M3>(v_at, 16 + key, 2 * j + piece));
+      if constexpr (!E4M3) {
         if (!whole) {
           w[0] &= keep[0];
           w[1] &= keep[0];
@@ -685,14 +727,7 @@ __device__ __forceinline__ void compute_tile(State<D, E4M3, NB>& t, uint32_t k_a
         }
 #pragma unroll
         for (int n = 0; n < NB; ++n) mma16816<false>(t.o[n][j], w, pb[i][n][0], pb[i][n][1]);
-      }
-    } else {
-      // matrices (keys 0-7, 8-15) x (pieces 2j, 2j+1); a lane gets channels 2c, 2c+1 (c = lane / 4) of
-      // keys 2t, 2t+1: row r of the product's tile is channel 2r, row r + 8 channel 2r + 1
-#pragma unroll
-      for (int j = 0; j < D / 32; ++j) {
-        uint32_t w[4];
-        ldsm4t(w, piece_at<D, E4M3>(v_at, i * 16 + row, 2 * j + col));
+      } else {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const uint32_t u0 = __byte_perm(w[2 * x], 0, 0x3120), u1 = __byte_perm(w[2 * x + 1], 0, 0x3120);
@@ -726,8 +761,7 @@ struct RowAt {
 template <bool E4M3, int NB>
 __device__ __forceinline__ RowAt row_at(const DecodeArgs& a, int row) {
   const DecodeParams& p = a.p;
-  const int bh = row / a.chunks, chunk = row - bh * a.chunks;
-  const int b = bh / p.c.H_kv, h = bh - b * p.c.H_kv;
+  const auto [b, h, chunk] = row_index(a, row);
   const int head = h * a.group + chunk * 8 * NB;
   return {p.o + b * p.os.seq + head * p.os.head,
           p.lse ? p.lse + static_cast<int64_t>(b) * p.H_q + head : nullptr,
@@ -742,14 +776,15 @@ __device__ __forceinline__ float natural_lse(float m, float l) {
 
 template <int D, bool E4M3, int NB>
 __device__ __forceinline__ void compute(const DecodeArgs& a, char* smem, uint32_t ring, uint32_t meta,
-                                        uint32_t bars, int pair, const WaitCtl& wait, int lane) {
+                                        uint32_t bars, int pair, int first_row, const WaitCtl& wait, int lane) {
   using C = Cfg<D, E4M3, NB>;
   State<D, E4M3, NB> t;
-  // the next row's queries, on their way while the last tile of a row is computed; 16 heads' would take the
-  // registers of the accumulators
+  // the next row's queries, on their way while the last tile of a row is computed (the first row's, while
+  // its first tile comes); 16 heads' would take the registers of the accumulators
   constexpr bool kAhead = NB == 1;
   uint32_t ahead[kAhead ? D / 16 : 1][2];
-  int ahead_row = -1;
+  int ahead_row = first_row;
+  if constexpr (kAhead) read_q<D, E4M3>(a, first_row, 0, lane, ahead);
   int4* heads = reinterpret_cast<int4*>(smem + C::kOffHead) + 2 * pair;
   bool starts = false;
   for (int done = 0;; ++done) {
@@ -863,49 +898,51 @@ __device__ __forceinline__ void compute(const DecodeArgs& a, char* smem, uint32_
   }
 }
 
-// Joins the CTA's parts, row by row: 16 threads a head, D / 16 channels a thread.
+// Joins the CTA's parts, row by row: 16 threads a head, D / 16 channels a thread.  Parts lie in the order of
+// the keys; the first of a row says whether the row starts in this CTA, the last whether it ends here.
 template <int D, bool E4M3, int NB>
 __device__ __forceinline__ void join_warps(const DecodeArgs& a, char* smem, int tid) {
   using C = Cfg<D, E4M3, NB>;
   constexpr int N = D / 16;
-  const int4* heads = reinterpret_cast<const int4*>(smem + C::kOffHead);
-  const int c0 = (tid & 15) * 4;  // channels c0 .. c0+3 of each 64
+  const int lane = tid & 31, c0 = (tid & 15) * 4;  // channels c0 .. c0+3 of each 64
+  const int4 mine = lane < 2 * C::kPairs ? reinterpret_cast<const int4*>(smem + C::kOffHead)[lane] : make_int4(0, 0, 0, 0);
+  uint32_t left = __ballot_sync(0xFFFFFFFFu, mine.w);
   int carried = 0, carried_row = 0;
-  for (int i = 0; i < 2 * C::kPairs;) {
-    if (!heads[i].w) {
-      ++i;
-      continue;
+  auto part_of = [&](int s) {
+    return s & 1 ? reinterpret_cast<const float*>(smem + (s >> 1) * C::kStages * C::kStage)
+                 : reinterpret_cast<const float*>(smem + C::kOffPiece + (s >> 1) * C::kPiece);
+  };
+  while (left) {
+    const int i = __ffs(left) - 1, row = __shfl_sync(0xFFFFFFFFu, mine.x, i);
+    const uint32_t parts = __ballot_sync(0xFFFFFFFFu, mine.w && mine.x == row);
+    left &= ~parts;
+    const bool starts = __shfl_sync(0xFFFFFFFFu, mine.y, i) & kStarts;
+    const bool ends = __shfl_sync(0xFFFFFFFFu, mine.y, 31 - __clz(parts)) & kEnds;
+    if (starts && !ends) {
+      carried = __shfl_sync(0xFFFFFFFFu, mine.z, i);
+      carried_row = row;
     }
-    const int4 first = heads[i];
-    int j = i, ends = 0;
-    while (j < 2 * C::kPairs && (!heads[j].w || heads[j].x == first.x)) {
-      if (heads[j].w) ends = heads[j].y & kEnds;
-      ++j;
-    }
-    const bool starts = first.y & kStarts;
-    const RowAt r = row_at<E4M3, NB>(a, first.x);
+    const RowAt r = row_at<E4M3, NB>(a, row);
     const Part out = part_at<D>(a.p.workspace, C::kHeads, blockIdx.x, starts ? 1 : 0);
+#pragma unroll 1
     for (int h = tid >> 4; h < r.heads; h += 2 * C::kPairs) {
       float m = -INFINITY, l = 0.f, o[N];
 #pragma unroll
       for (int c = 0; c < N; ++c) o[c] = 0.f;
-      for (int s = i; s < j; ++s) {
-        if (!heads[s].w) continue;
-        const float* f = s & 1 ? reinterpret_cast<const float*>(smem + (s >> 1) * C::kStages * C::kStage)
-                               : reinterpret_cast<const float*>(smem + C::kOffPiece + (s >> 1) * C::kPiece);
-        const float* ml = f + C::kHeads * C::kHeadPitch;
-        const float ms = ml[h], ls = ml[C::kHeads + h];
-        const float top = fmaxf(m, ms), zero = top == -INFINITY ? 0.f : top;
-        const float fade = ex2_approx(m - zero), w = ex2_approx(ms - zero);
-        m = top;
-        l = l * fade + ls * w;
+      for (uint32_t x = parts; x; x &= x - 1) m = fmaxf(m, part_of(__ffs(x) - 1)[C::kHeads * C::kHeadPitch + h]);
+      const float zero = m == -INFINITY ? 0.f : m;
+      for (uint32_t x = parts; x; x &= x - 1) {
+        const float* f = part_of(__ffs(x) - 1);
+        const float* ml = f + C::kHeads * C::kHeadPitch + h;
+        const float w = ex2_approx(ml[0] - zero);
+        l += ml[C::kHeads] * w;
 #pragma unroll
         for (int g = 0; g < N / 4; ++g) {
-          const float4 x = *reinterpret_cast<const float4*>(f + h * C::kHeadPitch + g * 64 + c0);
-          o[4 * g] = o[4 * g] * fade + x.x * w;
-          o[4 * g + 1] = o[4 * g + 1] * fade + x.y * w;
-          o[4 * g + 2] = o[4 * g + 2] * fade + x.z * w;
-          o[4 * g + 3] = o[4 * g + 3] * fade + x.w * w;
+          const float4 y = *reinterpret_cast<const float4*>(f + h * C::kHeadPitch + g * 64 + c0);
+          o[4 * g] += y.x * w;
+          o[4 * g + 1] += y.y * w;
+          o[4 * g + 2] += y.z * w;
+          o[4 * g + 3] += y.w * w;
         }
       }
       if (starts && ends) {
@@ -927,11 +964,6 @@ __device__ __forceinline__ void join_warps(const DecodeArgs& a, char* smem, int 
         }
       }
     }
-    if (starts && !ends) {
-      carried = first.z;
-      carried_row = first.x;
-    }
-    i = j;
   }
   if (tid == 0) reinterpret_cast<int4*>(a.p.workspace)[blockIdx.x] = make_int4(carried, carried_row, 0, 0);
 }
@@ -944,10 +976,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NB>::kThreads, 1)
   extern __shared__ __align__(1024) char smem[];  // the swizzled tiles need the alignment
   const uint32_t base = smem_u32(smem);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
-  int64_t* starts = reinterpret_cast<int64_t*>(smem + C::kOffMisc);          // [C::kPairs]: unit
-  int64_t* rests = starts + C::kPairs;                                          // [C::kPairs]: tiles into it
-  int64_t* total_at = rests + C::kPairs;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(total_at + 1);
+  int4* starts = reinterpret_cast<int4*>(smem + C::kOffMisc);  // [kPairs]: unit, row, tile
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(starts + C::kPairs);
   let_next_start();
   if ((base & 1023u) != 0) {
     wait_for_previous();
@@ -970,59 +1000,70 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NB>::kThreads, 1)
   fence_barrier_init();
   wait_for_previous();
 
-  // tiles of all units: each thread adds up a run of them, then a scan over the threads
+  // cost of all units: each thread adds up a run of them, then a scan over the threads
   const int per = (a.units + C::kThreads - 1) / C::kThreads;
   const int u0 = min(tid * per, a.units), u1 = min(u0 + per, a.units);
-  int64_t mine = 0;
+  int mine = 0, tiles = 0;
+#pragma unroll 1
   for (int u = u0; u < u1; ++u) {
     const bool owner = u % a.ctas == static_cast<int>(blockIdx.x);
-    const int n = unit_tiles(a, u, owner);
-    mine += static_cast<int64_t>(n) * a.rows;
-    if (n == 0 && owner) {  // nothing visible: zeros
+    tiles = unit_tiles(a, u, owner);
+    mine += row_cost(tiles) * a.rows;
+    if (tiles == 0 && owner) {  // nothing visible: zeros
+#pragma unroll 1
       for (int m = 0; m < a.rows; ++m) {
         const RowAt r = row_at<E4M3, NB>(a, u * a.rows + m);
+#pragma unroll 1
         for (int h = 0; h < r.heads; ++h) {
+#pragma unroll 1
           for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(r.o + h * a.p.os.head + c) = make_uint4(0, 0, 0, 0);
           if (r.lse) r.lse[h] = -INFINITY;
         }
       }
     }
   }
-  int64_t sum = mine;
+  int sum = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int64_t x = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+    const int x = __shfl_up_sync(0xFFFFFFFFu, sum, d);
     if (lane >= d) sum += x;
   }
-  int64_t* warp_sum = reinterpret_cast<int64_t*>(smem + C::kOffPiece);
+  int* warp_sum = reinterpret_cast<int*>(smem + C::kOffPiece);
   if (lane == 31) warp_sum[warp] = sum;
   __syncthreads();
-  for (int w = 0; w < warp; ++w) sum += warp_sum[w];
-  int64_t total = 0;
-  for (int w = 0; w < C::kThreads / 32; ++w) total += warp_sum[w];
-  const int64_t run = max((total + a.ctas - 1) / a.ctas, a.min_run);  // of a CTA
-  const int64_t cta0 = min(run * blockIdx.x, total), cta1 = min(cta0 + run, total);
-  const int64_t share = (cta1 - cta0 + C::kPairs - 1) / C::kPairs;          // of a warp
+  int total = 0;
 #pragma unroll
-  for (int w = 0; w < C::kPairs; ++w) {
-    const int64_t at = cta0 + w * share;
-    if (at < cta1 && at >= sum - mine && at < sum) {
-      int64_t from = sum - mine;
-      int u = u0;
-      for (; u + 1 < u1; ++u) {
-        const int64_t n = static_cast<int64_t>(unit_tiles(a, u, false)) * a.rows;
-        if (at < from + n) break;
-        from += n;
-      }
-      starts[w] = u;
-      rests[w] = at - from;
+  for (int w = 0; w < C::kThreads / 32; ++w) {
+    const int x = warp_sum[w];
+    total += x;
+    if (w < warp) sum += x;
+  }
+  const int run = max((total + a.ctas - 1) / a.ctas, a.min_run);  // of a CTA
+  const int cta0 = min(static_cast<int64_t>(run) * blockIdx.x, static_cast<int64_t>(total));
+  const int cta1 = min(static_cast<int64_t>(cta0) + run, static_cast<int64_t>(total));
+  const int share = (cta1 - cta0 + C::kPairs - 1) / C::kPairs;     // of a warp
+  if (mine > 0 && sum > cta0 && sum - mine < cta1) {
+#pragma unroll 1
+    for (int w = 0; w < C::kPairs; ++w) {
+      const int at = cta0 + w * share;
+      if (at >= cta1 || at < sum - mine || at >= sum) continue;
+      int from = sum - mine, u = u0;
+      if (u1 - u0 > 1)
+        for (;; ++u) {
+          tiles = unit_tiles(a, u, false);
+          const int n = row_cost(tiles) * a.rows;
+          if (at < from + n || u + 1 >= u1) break;
+          from += n;
+        }
+      const int m = (at - from) / row_cost(tiles);
+      starts[w] = make_int4(u, m, at - from - m * row_cost(tiles), 0);
     }
   }
   __syncthreads();
 
   const WaitCtl wait{abort_flag, a.p.c.status, a.wait_ns};
   const int pair = warp & (C::kPairs - 1);
-  const int64_t at = min(cta0 + pair * share, cta1), until = min(at + share, cta1);
+  const int at = min(cta0 + pair * share, cta1), until = min(at + share, cta1);
   const uint32_t ring = base + pair * C::kStages * C::kStage;
   const uint32_t meta = base + C::kOffMeta + pair * C::kStages * 16;
   const uint32_t bars = base + C::kOffBars + pair * C::kStages * 16;
@@ -1034,15 +1075,16 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NB>::kThreads, 1)
   if (at < until) {
     if (warp >= C::kPairs) {
       Walk w;
-      w.u = static_cast<int>(starts[pair]);
+      const int4 from = starts[pair];
+      w.u = from.x;
+      w.m = from.y;
+      w.c = from.z;
       w.plan = make_plan(a, w.u, lane);
-      w.m = static_cast<int>(rests[pair] / w.plan.tiles);
-      w.c = static_cast<int>(rests[pair] - static_cast<int64_t>(w.m) * w.plan.tiles);
       w.pos = at;
       w.end = until;
       fetched = fetch<D, E4M3, NB>(a, &kmap, &vmap, w, ring, meta, bars, run, wait, lane, rest);
     } else {
-      compute<D, E4M3, NB>(a, smem, ring, meta, bars, pair, wait, lane);
+      compute<D, E4M3, NB>(a, smem, ring, meta, bars, pair, starts[pair].x * a.rows + starts[pair].y, wait, lane);
     }
   }
   __syncthreads();
@@ -1067,16 +1109,33 @@ __global__ void __launch_bounds__(D) join_kernel(const __grid_constant__ DecodeA
   if (n < 2) return;
   const RowAt r = row_at<E4M3, NB>(a, head.y);
   if (h >= r.heads) return;
-  float m = -INFINITY;
-  for (int i = 0; i < n; ++i) m = fmaxf(m, part_at<D>(a.p.workspace, kHeads, blockIdx.x + i, i == 0).m[h]);
-  const float zero = m == -INFINITY ? 0.f : m;
-  float l = 0.f, o = 0.f;
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const Part x = part_at<D>(a.p.workspace, kHeads, blockIdx.x + i, i == 0);
-    const float w = ex2_approx(x.m[h] - zero);
-    l += x.l[h] * w;
-    o += x.o[h * D + threadIdx.x] * w;
+  constexpr int kAtOnce = 8;  // parts whose loads are in flight
+  float m = -INFINITY, l = 0.f, o = 0.f;
+  for (int i0 = 0; i0 < n; i0 += kAtOnce) {
+    float pm[kAtOnce], pl[kAtOnce], po[kAtOnce], top = m;
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      pm[i] = -INFINITY;
+      pl[i] = po[i] = 0.f;
+      if (i0 + i < n) {
+        const Part x = part_at<D>(a.p.workspace, kHeads, blockIdx.x + i0 + i, i0 + i == 0);
+        pm[i] = x.m[h];
+        pl[i] = x.l[h];
+        po[i] = x.o[h * D + threadIdx.x];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) top = fmaxf(top, pm[i]);
+    const float zero = top == -INFINITY ? 0.f : top, fade = ex2_approx(m - zero);
+    m = top;
+    l *= fade;
+    o *= fade;
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const float w = ex2_approx(pm[i] - zero);
+      l += pl[i] * w;
+      o += po[i] * w;
+    }
   }
   r.o[h * a.p.os.head + threadIdx.x] = __float2bfloat16(o * inverse(l) * r.v_scale);
   if (r.lse && threadIdx.x == 0) r.lse[h] = natural_lse(m, l);
@@ -1131,6 +1190,13 @@ size_t decode_workspace_bytes(int, int H_q, int H_kv, int d) {
   return kMaxCtas * 16 + static_cast<size_t>(kMaxCtas) * 2 * heads_of(H_q / H_kv) * (d + 2) * 4;
 }
 
+bool decode_fits(const DecodeParams& p) {
+  const int group = p.H_q / p.c.H_kv, heads = heads_of(group);
+  const int64_t rows = static_cast<int64_t>(p.c.B) * p.c.H_kv * ((group + heads - 1) / heads);
+  const int64_t keys = static_cast<int64_t>(p.sel ? p.sel_max : p.c.max_pages) << p.c.log2_page;
+  return rows * ((keys + kTileKeys - 1) / kTileKeys + 1) < (1LL << 31);
+}
+
 int launch_attn_decode(const DecodeParams& p, uint64_t wait_ns, cudaStream_t stream) {
   DecodeArgs a;
   a.p = p;
@@ -1140,6 +1206,8 @@ int launch_attn_decode(const DecodeParams& p, uint64_t wait_ns, cudaStream_t str
   a.chunks = (a.group + heads - 1) / heads;
   a.units = p.sel ? p.c.B * p.c.H_kv : p.c.B;
   a.rows = p.sel ? a.chunks : p.c.H_kv * a.chunks;
+  a.by_chunks = make_divisor(a.chunks);
+  a.by_heads = make_divisor(p.c.H_kv);
   a.ctas = sm_count();
   a.min_run = 4;
   a.wait_ns = wait_ns;

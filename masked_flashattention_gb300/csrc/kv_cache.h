@@ -55,6 +55,8 @@ struct DecodeParams {
   float scale;
   void* workspace;
 };
+// Whether the call's work counts (rows of tiles of 32 keys) stay within 31 bits.
+bool decode_fits(const DecodeParams& p);
 size_t decode_workspace_bytes(int B, int H_q, int H_kv, int d);
 int launch_attn_decode(const DecodeParams& p, uint64_t wait_ns, cudaStream_t stream);
 

@@ -173,7 +173,9 @@ def test_decode_refusals(B):
                 {"desc": _desc(B, B=3)}, {"desc": _desc(B, S=0)}, {"desc": _desc(B, ni_f=0)},
                 {"desc": _desc(B, ni_f=9)}, {"desc": _desc(B, itab_f=None)}, {"desc": _desc(B, itab_f=A16 + 8)}):
         assert _decode(B, **bad) == B.CM_ERR_INVALID_ARG, bad
-    for bad in ({"H_q": 1 << 15}, {"sel": A16, "nsel": A16, "sel_max": 9000}, {"desc": _desc(B, form=1)}):
+    for bad in ({"H_q": 1 << 15}, {"sel": A16, "nsel": A16, "sel_max": 9000}, {"desc": _desc(B, form=1)},
+                {"cache": _cache(B, page_size=128, H_kv=64, k_page_stride=1 << 20, v_page_stride=1 << 20),
+                 "seqs": _seqs(B, B=32767, max_pages=8192), "H_q": 64}):
         assert _decode(B, **bad) == B.CM_ERR_UNSUPPORTED, bad
 
 
