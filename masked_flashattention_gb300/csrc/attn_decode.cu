@@ -74,6 +74,7 @@ struct Cfg {
   static constexpr int kSmem = kOffMisc + 256;
   static_assert(kStages >= 2 && kSmem <= static_cast<int>(kSmemMax), "shared memory");
   static_assert(kOffPiece % 16 == 0 && kPiece % 16 == 0 && kOffMeta % 16 == 0, "alignment");
+  static_assert(kPairs * kPiece >= (2 * kThreads + kThreads / 32) * 4, "the search borrows the pieces' memory");
   static_assert(kStages * kStage >= kPiece, "the last piece of a warp borrows its ring");
 };
 
@@ -114,6 +115,8 @@ struct DecodeArgs {
   int rows;     // of a unit
   int ctas;
   int min_run;  // least cost a CTA's run is given
+  int most_tiles;  // a row can have
+  int whole_rows;  // a CTA's run is cut at rows' ends only
   Divisor by_chunks, by_heads;  // H_kv
   uint64_t wait_ns;
 };
@@ -210,20 +213,30 @@ __device__ __forceinline__ int unit_tiles(const DecodeArgs& a, int u, bool repor
   const int len = unit_length(a, b, report);
   if (a.p.sel) return len ? selected_tiles(a, u) : 0;
   if (a.p.itab == nullptr) return (len + kTileKeys - 1) / kTileKeys;
-  // few units and few intervals: small code (cold instructions cost more than the L1 reads here)
-  int total = 0;
+  int lo[kMaxIntervals], hi[kMaxIntervals], total = 0;
+#pragma unroll
+  for (int n = 0; n < kMaxIntervals; ++n) {
+    const int2 iv = unit_interval(a, b, n, len);
+    lo[n] = iv.x / kTileKeys;
+    hi[n] = (iv.y + kTileKeys - 1) / kTileKeys;
+  }
+  // one interval after another comes to the front (small code: instructions fetched for the first time
+  // cost more than these)
 #pragma unroll 1
-  for (int i = 0; i < a.p.NI; ++i) {
-    const int2 x = unit_interval(a, b, i, len);
-    int from = x.x / kTileKeys;
-#pragma unroll 1
-    for (int j = 0; j < a.p.NI; ++j) {
-      const int2 y = unit_interval(a, b, j, len);
-      const int lo = y.x / kTileKeys;
-      if (j != i && (lo < x.x / kTileKeys || (lo == x.x / kTileKeys && j < i)))
-        from = max(from, (y.y + kTileKeys - 1) / kTileKeys);
+  for (int i = 0; i < kMaxIntervals; ++i) {
+    int from = lo[0];
+#pragma unroll
+    for (int k = 1; k < kMaxIntervals; ++k)
+      if (lo[k] < lo[0] || (lo[k] == lo[0] && i + k >= kMaxIntervals)) from = max(from, hi[k]);
+    total += max(hi[0] - from, 0);
+    const int l = lo[0], h = hi[0];
+#pragma unroll
+    for (int k = 1; k < kMaxIntervals; ++k) {
+      lo[k - 1] = lo[k];
+      hi[k - 1] = hi[k];
     }
-    total += max((x.y + kTileKeys - 1) / kTileKeys - from, 0);
+    lo[kMaxIntervals - 1] = l;
+    hi[kMaxIntervals - 1] = h;
   }
   return total;
 }
@@ -270,6 +283,10 @@ __device__ __forceinline__ Plan make_plan(const DecodeArgs& a, int u, int lane) 
   }
   return w;
 }
+
+struct Place {
+  int u, m, c, tiles;  // unit, row of the unit, tile of the row; the unit's tiles a row
+};
 
 // Up to 32 consecutive tiles of a row, one per lane.
 struct Chunk {
@@ -976,8 +993,10 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NB>::kThreads, 1)
   extern __shared__ __align__(1024) char smem[];  // the swizzled tiles need the alignment
   const uint32_t base = smem_u32(smem);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
-  int4* starts = reinterpret_cast<int4*>(smem + C::kOffMisc);  // [kPairs]: unit, row, tile
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(starts + C::kPairs);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc);
+  // per thread, the cost before its units, and the tiles of its last one; borrowed until the search is done
+  int* before = reinterpret_cast<int*>(smem + C::kOffPiece);
+  int* tiles_of = before + C::kThreads;
   let_next_start();
   if ((base & 1023u) != 0) {
     wait_for_previous();
@@ -1028,7 +1047,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NB>::kThreads, 1)
     const int x = __shfl_up_sync(0xFFFFFFFFu, sum, d);
     if (lane >= d) sum += x;
   }
-  int* warp_sum = reinterpret_cast<int*>(smem + C::kOffPiece);
+  int* warp_sum = tiles_of + C::kThreads;
   if (lane == 31) warp_sum[warp] = sum;
   __syncthreads();
   int total = 0;
@@ -1038,32 +1057,54 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NB>::kThreads, 1)
     total += x;
     if (w < warp) sum += x;
   }
-  const int run = max((total + a.ctas - 1) / a.ctas, a.min_run);  // of a CTA
-  const int cta0 = min(static_cast<int64_t>(run) * blockIdx.x, static_cast<int64_t>(total));
-  const int cta1 = min(static_cast<int64_t>(cta0) + run, static_cast<int64_t>(total));
-  const int share = (cta1 - cta0 + C::kPairs - 1) / C::kPairs;     // of a warp
-  if (mine > 0 && sum > cta0 && sum - mine < cta1) {
+  before[tid] = sum - mine;
+  tiles_of[tid] = tiles;
+  __syncthreads();
+  // the place of a cost below the total: the last thread with no more before its units, then its unit
+  auto locate = [&](int at) {
+    int n = 0;
+#pragma unroll
+    for (int t = 0; t < C::kThreads; t += 32) n += before[t + lane] <= at;
+    const int t = __reduce_add_sync(0xFFFFFFFFu, n) - 1;
+    Place x{t * per, 0, 0, tiles_of[t]};
+    int from = before[t];
+    if (per > 1)
 #pragma unroll 1
-    for (int w = 0; w < C::kPairs; ++w) {
-      const int at = cta0 + w * share;
-      if (at >= cta1 || at < sum - mine || at >= sum) continue;
-      int from = sum - mine, u = u0;
-      if (u1 - u0 > 1)
-        for (;; ++u) {
-          tiles = unit_tiles(a, u, false);
-          const int n = row_cost(tiles) * a.rows;
-          if (at < from + n || u + 1 >= u1) break;
-          from += n;
-        }
-      const int m = (at - from) / row_cost(tiles);
-      starts[w] = make_int4(u, m, at - from - m * row_cost(tiles), 0);
+      for (;; ++x.u) {
+        x.tiles = unit_tiles(a, x.u, false);
+        const int cost = row_cost(x.tiles) * a.rows;
+        if (at < from + cost || x.u + 1 >= a.units) break;
+        from += cost;
+      }
+    x.m = (at - from) / row_cost(x.tiles);
+    x.c = at - from - x.m * row_cost(x.tiles);
+    return x;
+  };
+  const int run = max((total + a.ctas - 1) / a.ctas, a.min_run);  // of a CTA
+  int cta0 = min(static_cast<int64_t>(run) * blockIdx.x, static_cast<int64_t>(total));
+  int cta1 = min(static_cast<int64_t>(cta0) + run, static_cast<int64_t>(total));
+  if (a.whole_rows) {  // from the first row that starts in the run to the end of the last
+    int* bounds = tiles_of + C::kThreads;  // the warps' sums have been read
+    if (warp < 2) {
+      int at = warp ? cta1 : cta0;
+      if (at < total) {
+        const Place x = locate(at);
+        if (x.c) at += row_cost(x.tiles) - x.c;
+      }
+      if (lane == 0) bounds[warp] = at;
     }
+    __syncthreads();
+    cta0 = bounds[0];
+    cta1 = bounds[1];
   }
+  const int share = (cta1 - cta0 + C::kPairs - 1) / C::kPairs;  // of a warp
+  const int pair = warp & (C::kPairs - 1);
+  const int at = min(cta0 + pair * share, cta1), until = min(at + share, cta1);
+  Place place{0, 0, 0, 0};
+  if (at < until) place = locate(at);
   __syncthreads();
 
   const WaitCtl wait{abort_flag, a.p.c.status, a.wait_ns};
-  const int pair = warp & (C::kPairs - 1);
-  const int at = min(cta0 + pair * share, cta1), until = min(at + share, cta1);
   const uint32_t ring = base + pair * C::kStages * C::kStage;
   const uint32_t meta = base + C::kOffMeta + pair * C::kStages * 16;
   const uint32_t bars = base + C::kOffBars + pair * C::kStages * 16;
@@ -1075,16 +1116,15 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NB>::kThreads, 1)
   if (at < until) {
     if (warp >= C::kPairs) {
       Walk w;
-      const int4 from = starts[pair];
-      w.u = from.x;
-      w.m = from.y;
-      w.c = from.z;
+      w.u = place.u;
+      w.m = place.m;
+      w.c = place.c;
       w.plan = make_plan(a, w.u, lane);
       w.pos = at;
       w.end = until;
       fetched = fetch<D, E4M3, NB>(a, &kmap, &vmap, w, ring, meta, bars, run, wait, lane, rest);
     } else {
-      compute<D, E4M3, NB>(a, smem, ring, meta, bars, pair, starts[pair].x * a.rows + starts[pair].y, wait, lane);
+      compute<D, E4M3, NB>(a, smem, ring, meta, bars, pair, place.u * a.rows + place.m, wait, lane);
     }
   }
   __syncthreads();
@@ -1109,7 +1149,7 @@ __global__ void __launch_bounds__(D) join_kernel(const __grid_constant__ DecodeA
   if (n < 2) return;
   const RowAt r = row_at<E4M3, NB>(a, head.y);
   if (h >= r.heads) return;
-  constexpr int kAtOnce = 8;  // parts whose loads are in flight
+  constexpr int kAtOnce = 16;  // parts whose loads are in flight
   float m = -INFINITY, l = 0.f, o = 0.f;
   for (int i0 = 0; i0 < n; i0 += kAtOnce) {
     float pm[kAtOnce], pl[kAtOnce], po[kAtOnce], top = m;
@@ -1168,14 +1208,17 @@ int sm_count() {
 }
 
 template <int D, bool E4M3, int NB>
-int launch(const DecodeArgs& a, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream) {
+int launch(DecodeArgs& a, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream) {
   using C = Cfg<D, E4M3, NB>;
+  // Where no row can have more than 4 tiles a warp pair, rows stay whole: the second kernel, 2 to 3 us on
+  // the GPU and a launch, costs more than the few tiles by which runs then differ.
+  a.whole_rows = a.most_tiles <= 4 * C::kPairs;
   if (cudaFuncSetAttribute(decode_kernel<D, E4M3, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            C::kSmem) != cudaSuccess)
     return -1;
   return launch_after(decode_kernel<D, E4M3, NB>, dim3(a.ctas), C::kThreads, C::kSmem, stream, a, k, v) &&
-                 launch_after(join_kernel<D, E4M3, NB>, dim3(a.ctas, a.group < C::kHeads ? a.group : C::kHeads), D,
-                              0, stream, a)
+                 (a.whole_rows || launch_after(join_kernel<D, E4M3, NB>, dim3(a.ctas, a.group < C::kHeads ? a.group : C::kHeads), D,
+                              0, stream, a))
              ? 0
              : -1;
 }
@@ -1190,11 +1233,14 @@ size_t decode_workspace_bytes(int, int H_q, int H_kv, int d) {
   return kMaxCtas * 16 + static_cast<size_t>(kMaxCtas) * 2 * heads_of(H_q / H_kv) * (d + 2) * 4;
 }
 
+static int64_t most_tiles(const DecodeParams& p) {
+  return ((static_cast<int64_t>(p.sel ? p.sel_max : p.c.max_pages) << p.c.log2_page) + kTileKeys - 1) / kTileKeys;
+}
+
 bool decode_fits(const DecodeParams& p) {
   const int group = p.H_q / p.c.H_kv, heads = heads_of(group);
   const int64_t rows = static_cast<int64_t>(p.c.B) * p.c.H_kv * ((group + heads - 1) / heads);
-  const int64_t keys = static_cast<int64_t>(p.sel ? p.sel_max : p.c.max_pages) << p.c.log2_page;
-  return rows * ((keys + kTileKeys - 1) / kTileKeys + 1) < (1LL << 31);
+  return rows * (most_tiles(p) + 1) < (1LL << 31);
 }
 
 int launch_attn_decode(const DecodeParams& p, uint64_t wait_ns, cudaStream_t stream) {
@@ -1210,6 +1256,7 @@ int launch_attn_decode(const DecodeParams& p, uint64_t wait_ns, cudaStream_t str
   a.by_heads = make_divisor(p.c.H_kv);
   a.ctas = sm_count();
   a.min_run = 4;
+  a.most_tiles = most_tiles(p);
   a.wait_ns = wait_ns;
   if (a.ctas < 1) return -1;
   CUtensorMap k, v;
