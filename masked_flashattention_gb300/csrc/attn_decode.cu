@@ -412,9 +412,29 @@ __device__ __forceinline__ void next_chunk(const DecodeArgs& a, Walk& w, Chunk& 
   w.pos += k.n;
 }
 
-// A warp's wait: whole or not at all, so that its lanes go on together.
-__device__ __forceinline__ bool warp_wait(const WaitCtl& wait, uint32_t bar, uint32_t parity, int where) {
-  return __all_sync(0xFFFFFFFFu, wait(bar, parity, where));
+// A warp's wait: whole or not at all, so that its lanes go on together.  Bounded as WaitCtl's are.  The
+// waits here are a microsecond or two, and a try may sleep longer than that by itself: under a
+// short limit (cm_set_wait_limit_ns) the phase is only looked at.
+__device__ __forceinline__ bool warp_wait(const WaitCtl& w, uint32_t bar, uint32_t parity, int where) {
+  if (w.limit_ns >= 20000) return __all_sync(0xFFFFFFFFu, w(bar, parity, where));
+  const uint64_t t0 = globaltimer_ns();
+  bool got = false;
+  while (!got && !*w.abort) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    got = ok != 0;
+    if (!got && globaltimer_ns() - t0 > w.limit_ns) {
+      *w.abort = 1;
+      set_status(w.status, kDevTimeout, where);
+    }
+  }
+  return __all_sync(0xFFFFFFFFu, got);
 }
 
 // ---- fetching warp ------------------------------------------------------------------------------

@@ -623,3 +623,204 @@ def test_two_streams_with_workspaces_of_their_own(B):
     for i in range(2):
         for o, lse in got[i]:
             assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
+
+
+def test_many_sequences_sharing_pages(B):
+    """More sequences than a block has threads, most of them short or empty, with a common prefix in
+    shared pages; the same through selected pages, one row of pages a sequence and head."""
+    gen = torch.Generator().manual_seed(51)
+    Bn, H, group, P, d = 1300, 2, 2, 16, 64
+    lens = [int(x) for x in torch.randint(0, 50, (Bn,), generator=gen)]
+    for b in range(0, Bn, 3):
+        lens[b] = 0
+    cache, table, _ = _filled(B, [64] * 20, H, P, d, "bf16", gen)
+    own = table.cpu()
+    rows = torch.full((Bn, 4), -7, dtype=torch.int32)
+    for b in range(Bn):
+        rows[b] = own[b % 20]
+        rows[b, 0] = own[0, 0]  # everybody's first page
+    table, n = rows.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda")
+    q = torch.randn(Bn, H * group, d, generator=gen).to(torch.bfloat16).cuda()
+    o, lse = B.decode_attention(cache, table, n, q)
+    _check_decode(cache, table, lens, q, o, lse, 1 / 8, lambda b, g: torch.arange(lens[b]))
+    pages = [(m + P - 1) // P for m in lens]
+    nsel = torch.tensor([[p, max(p - 1, 0)] for p in pages], dtype=torch.int32)
+    sel = torch.arange(4, dtype=torch.int32).repeat(Bn, H, 1)
+    sel[:, 1] += 1  # the second head leaves the first page out
+    o, lse = B.decode_attention(cache, table, n, q, sel=sel.cuda(), nsel=nsel.cuda())
+    assert B.cm_kv_status(cache) == B.CM_OK
+    _check_decode(cache, table, lens, q, o, lse, 1 / 8, lambda b, g: torch.arange(16 if g else 0, max(lens[b], 16 if g else 0)))
+    # a table with room for long sequences takes the other way through the kernel
+    wide = torch.full((Bn, 200), -7, dtype=torch.int32, device="cuda")
+    wide[:, :4] = table
+    o, lse = B.decode_attention(cache, wide, n, q)
+    _check_decode(cache, wide, lens, q, o, lse, 1 / 8, lambda b, g: torch.arange(lens[b]))
+
+
+def test_scales_of_either_sign_and_none(B):
+    gen = torch.Generator().manual_seed(52)
+    lens = [70, 33]
+    for kv in ("bf16", "e4m3"):
+        cache, table, n = _filled(B, lens, 1, 32, 128, kv, gen)
+        q = torch.randn(2, 3, 128, generator=gen).to(torch.bfloat16).cuda()
+        for scale in (0.0, -0.2):
+            o, lse = B.decode_attention(cache, table, n, q, scale=scale)
+            _check_decode(cache, table, lens, q, o, lse, scale, lambda b, g: torch.arange(lens[b]))
+
+
+def test_values_of_one_head_do_not_reach_another(B):
+    """A query of NaN, infinities or zeros spoils its own row alone; infinite keys give what the formula gives."""
+    gen = torch.Generator().manual_seed(53)
+    for kv in ("bf16", "e4m3"):
+        cache, table, n = _filled(B, [50, 50], 2, 16, 64, kv, gen)
+        q = torch.randn(2, 8, 64, generator=gen).to(torch.bfloat16).cuda()
+        want, wl = B.decode_attention(cache, table, n, q)
+        bad = q.clone()
+        bad[0, 1], bad[1, 6, 3], bad[1, 2] = math.nan, math.inf, 0
+        o, lse = B.decode_attention(cache, table, n, bad)
+        assert o[0, 1].isnan().all() and lse[0, 1].isnan() and not o[1, 2].isnan().any()
+        assert abs(lse[1, 2].item() - math.log(50)) < 1e-5
+        keep = torch.ones(2, 8, dtype=torch.bool, device="cuda")
+        keep[0, 1] = keep[1, 6] = keep[1, 2] = False
+        assert torch.equal(o[keep], want[keep]) and torch.equal(lse[keep], wl[keep])
+
+
+def test_many_key_value_heads(B):
+    """12 key-value heads: more than the 8 warps of a block take at once."""
+    gen = torch.Generator().manual_seed(54)
+    H, P, d, lens = 12, 16, 64, [40, 7]
+    cache = B.KVCache.alloc(8, H, P, d, summaries=True)
+    table = torch.randperm(8, generator=gen).to(torch.int32).view(2, 4).cuda()
+    k, v = (torch.randn(2, H, 40, d, generator=gen).to(torch.bfloat16).cuda() for _ in range(2))
+    zero, n = torch.zeros(2, dtype=torch.int32, device="cuda"), torch.tensor(lens, dtype=torch.int32, device="cuda")
+    B.cm_kv_append(cache, table, zero, k, v, n_new=n)
+    pool, _, _, _ = _host(cache)
+    q = torch.randn(2, H, d, generator=gen).to(torch.bfloat16)
+    sel, nsel = B.select_pages(cache, table, n, q.cuda(), 2)
+    for b in range(2):
+        at = table[b, :(lens[b] + P - 1) // P].cpu().long()
+        for h in range(H):
+            parts = [K.summary(K.rows(pool, None, table[b].cpu(), h, torch.arange(i * P, min(lens[b], i * P + P))).float())
+                     for i in range(len(at))]
+            for i, (s, e) in enumerate(parts):
+                assert torch.equal(cache.summary[at[i], h].cpu(), s) and cache.summary_scale[at[i], h].item() == e
+            want = K.pick(K.scores(q[b, h:h + 1], torch.stack([s for s, _ in parts]), [e for _, e in parts]), 2, 0, 0)
+            assert sel[b, h, :len(want)].tolist() == want and nsel[b, h] == len(want)
+    o, lse = B.decode_attention(cache, table, n, q.cuda(), sel=sel, nsel=nsel)
+    chosen = {(b, h): torch.tensor([p for x in sel[b, h].tolist() if x >= 0 for p in range(x * P, min(lens[b], x * P + P))])
+              for b in range(2) for h in range(H)}
+    _check_decode(cache, table, lens, q, o, lse, 1 / 8, lambda b, g: chosen[b, g])
+    assert B.cm_kv_status(cache) == B.CM_OK
+
+
+@pytest.mark.parametrize("equal", [False, True])
+def test_select_among_many_pages(B, equal):
+    """9000 pages of one sequence: the wide form of the selection, and (equal scores) thousands of pages at the
+    border; against a sort of the same scores."""
+    gen = torch.Generator().manual_seed(55)
+    pages, P, d, n = 9000, 16, 64, 1500
+    s = torch.randint(-127, 128, (pages, 1, 2, d), generator=gen, dtype=torch.int8)
+    if equal:
+        s[:] = s[:1]
+        s[::7] = 0
+    cache = B.KVCache.alloc(pages, 1, P, d)
+    cache = B.KVCache(cache.k, cache.v, summary=s.cuda(), summary_scale=torch.ones(pages, 1, device="cuda"))
+    table = torch.randperm(pages, generator=gen).to(torch.int32).view(1, -1)
+    lens = torch.tensor([pages * P - 3], dtype=torch.int32, device="cuda")
+    q = torch.randn(1, 2, d, generator=gen).to(torch.bfloat16)
+    sel, nsel = B.select_pages(cache, table.cuda(), lens, q.cuda(), n, 2, 3)
+    rows, best = s[table[0].long(), 0].to(F64), None
+    for x in q[0].to(F64):
+        f = K.exponent(x.abs().max().item())
+        x = torch.round(x * 2.0 ** -f).clamp(-127, 127)
+        score = (x.clamp(min=0) * rows[:, 0] + x.clamp(max=0) * rows[:, 1]).sum(1) * 2.0 ** f
+        best = score if best is None else torch.maximum(best, score)
+    best[:2] = best[-3:] = math.inf
+    want = torch.sort(torch.sort(best, descending=True, stable=True)[1][:n])[0]
+    assert nsel.item() == n and torch.equal(sel[0, 0].cpu().long(), want)
+    assert B.cm_kv_status(cache) == B.CM_OK
+
+
+def test_pool_beyond_32_bits(B):
+    """Pages whose elements start beyond 2^32: 34,000 pages of 2^17 elements."""
+    gen = torch.Generator().manual_seed(56)
+    pages, H, P, d = 34000, 8, 128, 128
+    k, v = (torch.empty(pages, H, P, d, dtype=torch.float8_e4m3fn, device="cuda") for _ in range(2))
+    scale = torch.full((H,), 0.02, device="cuda")
+    s = torch.empty(pages, H, 2, d, dtype=torch.int8, device="cuda")
+    cache = B.KVCache(k, v, scale, scale, s, torch.empty(pages, H, device="cuda"))
+    table = torch.tensor([[33999, 5, 33000]], dtype=torch.int32, device="cuda")
+    for i in table[0].tolist():
+        k.view(torch.uint8)[i] = 127  # NaN
+        v.view(torch.uint8)[i] = 127
+    n = 300
+    x, y = (torch.randn(1, H, n, d, generator=gen).to(torch.bfloat16).cuda() for _ in range(2))
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    B.cm_kv_append(cache, table, torch.zeros_like(lens), x, y)
+    q = torch.randn(1, H * 2, d, generator=gen).to(torch.bfloat16).cuda()
+    sel, nsel = B.select_pages(cache, table, lens, q, 2)
+    o, lse = B.decode_attention(cache, table, lens, q)
+    assert B.cm_kv_status(cache) == B.CM_OK
+    at = table[0].long()
+    small = B.KVCache(*(t.view(torch.uint8)[at].view(t.dtype) for t in (k, v)), scale, scale, s[at], cache.summary_scale[at])
+    order = torch.arange(3, dtype=torch.int32, device="cuda")[None]
+    _check_decode(small, order, [n], q, o, lse, 1 / math.sqrt(d), lambda b, g: torch.arange(n))
+    got, many = B.select_pages(small, order, lens, q, 2)
+    assert torch.equal(got, sel) and torch.equal(many, nsel)
+
+
+def test_expired_waits_are_reported_and_the_next_call_is_correct(B):
+    """A wait limit of 1 ns makes ordinary waits of the attention kernel expire: CM_ERR_TIMEOUT, and with the
+    default limit the same call succeeds (in both forms: rows kept whole, and rows split)."""
+    gen = torch.Generator().manual_seed(57)
+    for lens in ([100, 300], [5000, 9000]):
+        cache, table, n = _filled(B, lens, 2, 64, 128, "bf16", gen)
+        q = torch.randn(2, 4, 128, generator=gen).to(torch.bfloat16).cuda()
+        B.cm_set_wait_limit_ns(1)
+        try:
+            B.decode_attention(cache, table, n, q)
+            torch.cuda.synchronize()
+        finally:
+            B.cm_set_wait_limit_ns(0)
+        assert B.cm_kv_status(cache) == B.CM_ERR_TIMEOUT
+        o, lse = B.decode_attention(cache, table, n, q)
+        assert B.cm_kv_status(cache) == B.CM_OK
+        _check_decode(cache, table, lens, q, o, lse, 1 / math.sqrt(128), lambda b, g: torch.arange(lens[b]))
+
+
+def test_binding_refusals(B):
+    """What the binding turns down before the library is called."""
+    cache = B.KVCache.alloc(4, 2, 16, 64)
+    table, lens = torch.zeros(1, 4, dtype=torch.int32, device="cuda"), torch.ones(1, dtype=torch.int32, device="cuda")
+    q = torch.zeros(1, 4, 64, dtype=torch.bfloat16, device="cuda")
+    work = torch.empty(B.cm_attn_decode_workspace_size(1, 4, 2, 64), dtype=torch.uint8, device="cuda")
+    k = torch.zeros(1, 2, 3, 64, dtype=torch.bfloat16, device="cuda")
+    cu = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    one = q[:, :2]
+    decode = lambda **x: B.cm_attn_decode(*[x.get(n, y) for n, y in (("cache", cache), ("table", table), ("lens", lens),  # noqa: E731
+                                            ("q", q), ("o", torch.empty_like(q)), ("lse", None), ("work", work))],
+                                          **{n: x[n] for n in ("sel", "nsel") if n in x})
+    sel = torch.zeros(1, 2, 3, dtype=torch.int32, device="cuda")
+    for bad in ({"table": table.long()}, {"table": table[0]}, {"table": table.cpu()}, {"lens": lens.cpu()}, {"lens": lens[:0]},
+                {"q": q.float()}, {"q": q[..., :32]}, {"q": q.transpose(1, 2)}, {"o": q[:, :2].clone()}, {"lse": torch.zeros(1, 4)},
+                {"work": work.cpu()}, {"sel": sel}, {"nsel": sel[..., 0]}, {"sel": sel[:, :1], "nsel": sel[..., 0].contiguous()},
+                {"lens": torch.ones(2, dtype=torch.int32, device="cuda")[::2].expand(1).repeat(2)}):
+        with pytest.raises(ValueError):
+            decode(**bad)
+    for args, more in (((k, k[:, :1]), {}), ((k[:, :1], k[:, :1]), {}), ((k.float(), k), {}), ((k, k), {"q": k}),
+                       ((k, k), {"k_out": k[:, :, :2]}), ((k, k), {"cu_new": cu}), ((one, one), {"cu_new": cu, "n_new": lens}),
+                       ((k, k), {"n_new": cu}), ((k, k), {"rope": torch.zeros(9, 8, 3, device="cuda")}),
+                       ((k, k), {"rope": torch.zeros(9, 8, 2)}), ((k, k), {"new_lens": lens.long()})):
+        with pytest.raises(ValueError):
+            B.cm_kv_append(cache, table, lens, *args, **more)
+    with pytest.raises(B.CMError):
+        B.cm_kv_append(cache, table, lens, k, k, new_lens=lens)  # lens is read while it would be written
+    with pytest.raises(B.CMError):
+        decode(work=work[:16])
+    with pytest.raises(ValueError):
+        B.select_pages(cache, table, lens, q, 2)  # no summaries
+    e4m3 = torch.zeros(4, 2, 16, 64, device="cuda").to(torch.float8_e4m3fn)
+    for args in ((e4m3, e4m3), (cache.k, e4m3), (cache.k, cache.v[:2]), (cache.k.transpose(1, 2), cache.v),
+                 (cache.k, cache.v, lens.float(), lens.float()), (cache.k, cache.v, None, None, torch.zeros(1, device="cuda"))):
+        with pytest.raises(ValueError):
+            B.KVCache(*args)
