@@ -711,8 +711,10 @@ __device__ __forceinline__ void compute_tile(State<D, E4M3, NB>& t, uint32_t k_a
         }
       }
   }
-  // P^T as the B operand [16 keys x 8 heads]
-  uint32_t pb[2][NB][2];
+  // P^T as the B operand [16 keys x 8 heads].  fp16 P (beside an e4m3 cache) keeps 11 bits; bf16 P would
+  // keep 8 and be off by as much as the rounded output, so its remainder goes through a second product
+  // with the same values.
+  uint32_t pb[2][NB][2], rest[2][NB][2];
 #pragma unroll
   for (int n = 0; n < NB; ++n) {
     const float m0 = t.m[n][0] == -INFINITY ? 0.f : t.m[n][0], m1 = t.m[n][1] == -INFINITY ? 0.f : t.m[n][1];
@@ -732,6 +734,8 @@ __device__ __forceinline__ void compute_tile(State<D, E4M3, NB>& t, uint32_t k_a
           w = *reinterpret_cast<const uint32_t*>(&f);
         } else {
           w = pack_bf16x2(e[2 * x], e[2 * x + 1]);
+          rest[i][n][x] = movm_trans(pack_bf16x2(e[2 * x] - __uint_as_float(w << 16),
+                                                 e[2 * x + 1] - __uint_as_float(w & 0xFFFF0000u)));
         }
         pb[i][n][x] = movm_trans(w);
       }
@@ -763,7 +767,10 @@ __device__ __forceinline__ void compute_tile(State<D, E4M3, NB>& t, uint32_t k_a
           w[3] &= keep[1];
         }
 #pragma unroll
-        for (int n = 0; n < NB; ++n) mma16816<false>(t.o[n][j], w, pb[i][n][0], pb[i][n][1]);
+        for (int n = 0; n < NB; ++n) {
+          mma16816<false>(t.o[n][j], w, rest[i][n][0], rest[i][n][1]);
+          mma16816<false>(t.o[n][j], w, pb[i][n][0], pb[i][n][1]);
+        }
       } else {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
