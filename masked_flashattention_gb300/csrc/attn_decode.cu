@@ -74,7 +74,7 @@ struct Cfg {
   static constexpr int kSmem = kOffMisc + 256;
   static_assert(kStages >= 2 && kSmem <= static_cast<int>(kSmemMax), "shared memory");
   static_assert(kOffPiece % 16 == 0 && kPiece % 16 == 0 && kOffMeta % 16 == 0, "alignment");
-  static_assert(kPairs * kPiece >= (2 * kThreads + kThreads / 32) * 4, "the search borrows the pieces' memory");
+  static_assert(kPairs * kPiece >= (3 * kThreads + kThreads / 32) * 4, "the search borrows the pieces' memory");
   static_assert(kStages * kStage >= kPiece, "the last piece of a warp borrows its ring");
 };
 
@@ -187,9 +187,8 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int3
 // key-value head of a sequence.  Intervals [st, en) of keys become tile ranges; a tile that several touch
 // belongs to the first in the order of the ranges' starts, so with `before` that order, interval i
 // owns the tiles [max(a_i, max of b_j before i), b_i).
-__device__ __forceinline__ int unit_length(const DecodeArgs& a, int b, bool report) {
+__device__ __forceinline__ int checked_length(const DecodeArgs& a, int b, int len, bool report) {
   const DecodeParams& p = a.p;
-  const int len = p.c.lens[b];
   const bool good = len >= 0 &&
                     static_cast<int64_t>(len) <= (static_cast<int64_t>(p.c.max_pages) << p.c.log2_page) &&
                     (p.itab == nullptr || len <= p.S);
@@ -204,14 +203,15 @@ __device__ __forceinline__ int2 unit_interval(const DecodeArgs& a, int b, int n,
   const int s = max(iv.x, 0), e = min(iv.y, len);
   return e > s ? make_int2(s, e) : make_int2(0, 0);
 }
-__device__ __forceinline__ int selected_tiles(const DecodeArgs& a, int u) {
-  const int n = min(max(a.p.nsel[u], 0), a.p.sel_max);
-  return a.p.c.log2_page == 4 ? (n + 1) / 2 : n << (a.p.c.log2_page - 5);
-}
-__device__ __forceinline__ int unit_tiles(const DecodeArgs& a, int u, bool report) {
-  const int b = a.p.sel ? u / a.p.c.H_kv : u;
-  const int len = unit_length(a, b, report);
-  if (a.p.sel) return len ? selected_tiles(a, u) : 0;
+// Tiles of a unit's rows, and its sequence's length (0 where that is out of range).
+__device__ __forceinline__ int unit_tiles(const DecodeArgs& a, int u, bool report, int& len) {
+  const int b = a.p.sel ? a.by_heads(u) : u;
+  const int held = a.p.c.lens[b], chosen = a.p.sel ? a.p.nsel[u] : 0;  // both on their way at once
+  len = checked_length(a, b, held, report);
+  if (a.p.sel) {
+    const int n = len ? min(max(chosen, 0), a.p.sel_max) : 0;
+    return a.p.c.log2_page == 4 ? (n + 1) / 2 : n << (a.p.c.log2_page - 5);
+  }
   if (a.p.itab == nullptr) return (len + kTileKeys - 1) / kTileKeys;
   int lo[kMaxIntervals], hi[kMaxIntervals], total = 0;
 #pragma unroll
@@ -249,24 +249,17 @@ struct Plan {
   int st, en;         // keys of the lane's interval
   int from, cnt, off; // its own tiles, and their place in the unit's order
 };
-__device__ __forceinline__ Plan make_plan(const DecodeArgs& a, int u, int lane) {
+__device__ __forceinline__ Plan make_plan(const DecodeArgs& a, int u, int len, int tiles, int lane) {
   Plan w;
-  w.b = a.p.sel ? u / a.p.c.H_kv : u;
-  w.len = unit_length(a, w.b, false);
+  w.b = a.p.sel ? a.by_heads(u) : u;
+  w.len = len;
+  w.tiles = tiles;
   w.st = w.en = w.from = w.cnt = w.off = 0;
-  if (a.p.sel) {
-    w.tiles = w.len ? selected_tiles(a, u) : 0;
-    return w;
-  }
+  if (a.p.itab == nullptr) return w;  // its tiles in order, every key below the length
   const int2 iv = lane < kMaxIntervals ? unit_interval(a, w.b, lane, w.len) : make_int2(0, 0);
   w.st = iv.x;
   w.en = iv.y;
   const int lo = iv.x / kTileKeys, hi = (iv.y + kTileKeys - 1) / kTileKeys;
-  if (a.p.itab == nullptr) {  // one interval
-    w.cnt = lane == 0 ? hi : 0;
-    w.tiles = __shfl_sync(0xFFFFFFFFu, hi, 0);
-    return w;
-  }
   w.from = lo;
 #pragma unroll 1
   for (int j = 0; j < a.p.NI; ++j) {
@@ -274,18 +267,17 @@ __device__ __forceinline__ Plan make_plan(const DecodeArgs& a, int u, int lane) 
     if (j != lane && (lj < lo || (lj == lo && j < lane))) w.from = max(w.from, hj);
   }
   w.cnt = lane < kMaxIntervals ? max(hi - w.from, 0) : 0;
-  w.tiles = 0;
 #pragma unroll 1
   for (int j = 0; j < a.p.NI; ++j) {
     const int lj = __shfl_sync(0xFFFFFFFFu, lo, j), cj = __shfl_sync(0xFFFFFFFFu, w.cnt, j);
     if (lj < lo || (lj == lo && j < lane)) w.off += cj;
-    w.tiles += cj;
   }
   return w;
 }
 
 struct Place {
-  int u, m, c, tiles;  // unit, row of the unit, tile of the row; the unit's tiles a row
+  int u, m, c;     // unit, row of the unit, tile of the row
+  int len, tiles;  // of the unit
 };
 
 // Up to 32 consecutive tiles of a row, one per lane.
@@ -326,7 +318,9 @@ __device__ __forceinline__ void next_chunk(const DecodeArgs& a, Walk& w, Chunk& 
           k.n = 0;
           return;
         }
-        w.plan = make_plan(a, ++w.u, lane);
+        int len;
+        const int tiles = unit_tiles(a, ++w.u, false, len);
+        w.plan = make_plan(a, w.u, len, tiles, lane);
       } while (w.plan.tiles == 0);
     }
   }
@@ -347,7 +341,7 @@ __device__ __forceinline__ void next_chunk(const DecodeArgs& a, Walk& w, Chunk& 
   k.full = false;
   if (p.sel) {
     const int32_t* sel = p.sel + static_cast<int64_t>(bh) * p.sel_max;
-    const int entries = min(max(p.nsel[bh], 0), p.sel_max);
+    const int entries = log2_page == 4 ? min(p.nsel[bh], p.sel_max) : 0;  // there may be one page too few for the last tile
     const int e0 = log2_page == 4 ? 2 * c : c >> (log2_page - 5);
     if (in) {
       place0 = sel[e0];
@@ -800,16 +794,20 @@ struct RowAt {
   __nv_bfloat16* o;  // first head of the row
   float* lse;
   int heads;         // of the row
-  float v_scale;
+  int h;             // key-value head
 };
-template <bool E4M3, int NB>
+template <int NB>
 __device__ __forceinline__ RowAt row_at(const DecodeArgs& a, int row) {
   const DecodeParams& p = a.p;
   const auto [b, h, chunk] = row_index(a, row);
   const int head = h * a.group + chunk * 8 * NB;
   return {p.o + b * p.os.seq + head * p.os.head,
           p.lse ? p.lse + static_cast<int64_t>(b) * p.H_q + head : nullptr,
-          min(8 * NB, a.group - chunk * 8 * NB), E4M3 ? p.c.v_scale[h] : 1.f};
+          min(8 * NB, a.group - chunk * 8 * NB), h};
+}
+template <bool E4M3>
+__device__ __forceinline__ float value_scale(const DecodeArgs& a, int h) {
+  return E4M3 ? __ldg(a.p.c.v_scale + h) : 1.f;
 }
 
 // 1 / l, 0 for a row that saw nothing (l = 0 and O = 0: the output is 0)
@@ -883,10 +881,11 @@ __device__ __forceinline__ void compute(const DecodeArgs& a, char* smem, uint32_
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) t.l[n][i] += __shfl_xor_sync(0xFFFFFFFFu, t.l[n][i], d);
     if (starts && (flags & kEnds)) {  // the whole row
-      const RowAt r = row_at<E4M3, NB>(a, row);
+      const RowAt r = row_at<NB>(a, row);
+      const float v_scale = value_scale<E4M3>(a, r.h);
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
-        const float i0 = inverse(t.l[n][0]) * r.v_scale, i1 = inverse(t.l[n][1]) * r.v_scale;
+        const float i0 = inverse(t.l[n][0]) * v_scale, i1 = inverse(t.l[n][1]) * v_scale;
         const int h0 = n * 8 + (lane & 3) * 2;
         if constexpr (E4M3) {
 #pragma unroll
@@ -966,23 +965,34 @@ __device__ __forceinline__ void join_warps(const DecodeArgs& a, char* smem, int 
       carried = __shfl_sync(0xFFFFFFFFu, mine.z, i);
       carried_row = row;
     }
-    const RowAt r = row_at<E4M3, NB>(a, row);
+    const RowAt r = row_at<NB>(a, row);
     const Part out = part_at<D>(a.p.workspace, C::kHeads, blockIdx.x, starts ? 1 : 0);
 #pragma unroll 1
     for (int h = tid >> 4; h < r.heads; h += 2 * C::kPairs) {
       float m = -INFINITY, l = 0.f, o[N];
 #pragma unroll
       for (int c = 0; c < N; ++c) o[c] = 0.f;
-      for (uint32_t x = parts; x; x &= x - 1) m = fmaxf(m, part_of(__ffs(x) - 1)[C::kHeads * C::kHeadPitch + h]);
+      // a warp holds one part of a row at most
+      float pm[C::kPairs], pl[C::kPairs];
+      const float* from[C::kPairs];
+#pragma unroll
+      for (int x = 0; x < C::kPairs; ++x) {
+        const uint32_t which = (parts >> (2 * x)) & 3u;
+        from[x] = part_of(2 * x + (which >> 1)) + h * C::kHeadPitch + c0;
+        const float* ml = part_of(2 * x + (which >> 1)) + C::kHeads * C::kHeadPitch + h;
+        pm[x] = which ? ml[0] : -INFINITY;
+        pl[x] = which ? ml[C::kHeads] : 0.f;
+        m = fmaxf(m, pm[x]);
+      }
       const float zero = m == -INFINITY ? 0.f : m;
-      for (uint32_t x = parts; x; x &= x - 1) {
-        const float* f = part_of(__ffs(x) - 1);
-        const float* ml = f + C::kHeads * C::kHeadPitch + h;
-        const float w = ex2_approx(ml[0] - zero);
-        l += ml[C::kHeads] * w;
+#pragma unroll
+      for (int x = 0; x < C::kPairs; ++x) {
+        if (((parts >> (2 * x)) & 3u) == 0) continue;
+        const float w = ex2_approx(pm[x] - zero);
+        l += pl[x] * w;
 #pragma unroll
         for (int g = 0; g < N / 4; ++g) {
-          const float4 y = *reinterpret_cast<const float4*>(f + h * C::kHeadPitch + g * 64 + c0);
+          const float4 y = *reinterpret_cast<const float4*>(from[x] + g * 64);
           o[4 * g] += y.x * w;
           o[4 * g + 1] += y.y * w;
           o[4 * g + 2] += y.z * w;
@@ -990,7 +1000,7 @@ __device__ __forceinline__ void join_warps(const DecodeArgs& a, char* smem, int 
         }
       }
       if (starts && ends) {
-        const float inv = inverse(l) * r.v_scale;
+        const float inv = inverse(l) * value_scale<E4M3>(a, r.h);
 #pragma unroll
         for (int g = 0; g < N / 4; ++g)
           *reinterpret_cast<uint2*>(r.o + h * a.p.os.head + g * 64 + c0) =
@@ -1021,7 +1031,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NB>::kThreads, 1)
   const uint32_t base = smem_u32(smem);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc);
-  // per thread, the cost before its units, and the tiles of its last one; borrowed until the search is done
+  // per thread, the cost before its units, and the tiles and the length of its last one; borrowed until the search is done
   int* before = reinterpret_cast<int*>(smem + C::kOffPiece);
   int* tiles_of = before + C::kThreads;
   let_next_start();
@@ -1046,19 +1056,22 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NB>::kThreads, 1)
   fence_barrier_init();
   wait_for_previous();
 
+  if (E4M3 && tid * 32 < a.p.c.H_kv) {  // the scales are wanted at the start and at the end of a row
+    asm volatile("prefetch.global.L1 [%0];" ::"l"(a.p.c.k_scale + tid * 32));
+    asm volatile("prefetch.global.L1 [%0];" ::"l"(a.p.c.v_scale + tid * 32));
+  }
   // cost of all units: each thread adds up a run of them, then a scan over the threads
   const int per = (a.units + C::kThreads - 1) / C::kThreads;
   const int u0 = min(tid * per, a.units), u1 = min(u0 + per, a.units);
-  int mine = 0, tiles = 0;
+  int mine = 0, tiles = 0, len = 0;
 #pragma unroll 1
   for (int u = u0; u < u1; ++u) {
-    const bool owner = u % a.ctas == static_cast<int>(blockIdx.x);
-    tiles = unit_tiles(a, u, owner);
+    tiles = unit_tiles(a, u, true, len);
     mine += row_cost(tiles) * a.rows;
-    if (tiles == 0 && owner) {  // nothing visible: zeros
+    if (tiles == 0 && u % a.ctas == static_cast<int>(blockIdx.x)) {  // nothing visible: zeros
 #pragma unroll 1
       for (int m = 0; m < a.rows; ++m) {
-        const RowAt r = row_at<E4M3, NB>(a, u * a.rows + m);
+        const RowAt r = row_at<NB>(a, u * a.rows + m);
 #pragma unroll 1
         for (int h = 0; h < r.heads; ++h) {
 #pragma unroll 1
@@ -1074,7 +1087,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NB>::kThreads, 1)
     const int x = __shfl_up_sync(0xFFFFFFFFu, sum, d);
     if (lane >= d) sum += x;
   }
-  int* warp_sum = tiles_of + C::kThreads;
+  int* len_of = tiles_of + C::kThreads;
+  int* warp_sum = len_of + C::kThreads;
   if (lane == 31) warp_sum[warp] = sum;
   __syncthreads();
   int total = 0;
@@ -1086,6 +1100,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NB>::kThreads, 1)
   }
   before[tid] = sum - mine;
   tiles_of[tid] = tiles;
+  len_of[tid] = len;
   __syncthreads();
   // the place of a cost below the total: the last thread with no more before its units, then its unit
   auto locate = [&](int at) {
@@ -1093,12 +1108,12 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NB>::kThreads, 1)
 #pragma unroll
     for (int t = 0; t < C::kThreads; t += 32) n += before[t + lane] <= at;
     const int t = __reduce_add_sync(0xFFFFFFFFu, n) - 1;
-    Place x{t * per, 0, 0, tiles_of[t]};
+    Place x{t * per, 0, 0, len_of[t], tiles_of[t]};
     int from = before[t];
     if (per > 1)
 #pragma unroll 1
       for (;; ++x.u) {
-        x.tiles = unit_tiles(a, x.u, false);
+        x.tiles = unit_tiles(a, x.u, false, x.len);
         const int cost = row_cost(x.tiles) * a.rows;
         if (at < from + cost || x.u + 1 >= a.units) break;
         from += cost;
@@ -1111,7 +1126,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NB>::kThreads, 1)
   int cta0 = min(static_cast<int64_t>(run) * blockIdx.x, static_cast<int64_t>(total));
   int cta1 = min(static_cast<int64_t>(cta0) + run, static_cast<int64_t>(total));
   if (a.whole_rows) {  // from the first row that starts in the run to the end of the last
-    int* bounds = tiles_of + C::kThreads;  // the warps' sums have been read
+    int* bounds = warp_sum;  // the sums have been read
     if (warp < 2) {
       int at = warp ? cta1 : cta0;
       if (at < total) {
@@ -1127,7 +1142,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NB>::kThreads, 1)
   const int share = (cta1 - cta0 + C::kPairs - 1) / C::kPairs;  // of a warp
   const int pair = warp & (C::kPairs - 1);
   const int at = min(cta0 + pair * share, cta1), until = min(at + share, cta1);
-  Place place{0, 0, 0, 0};
+  Place place{0, 0, 0, 0, 0};
   if (at < until) place = locate(at);
   __syncthreads();
 
@@ -1146,7 +1161,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NB>::kThreads, 1)
       w.u = place.u;
       w.m = place.m;
       w.c = place.c;
-      w.plan = make_plan(a, w.u, lane);
+      w.plan = make_plan(a, w.u, place.len, place.tiles, lane);
       w.pos = at;
       w.end = until;
       fetched = fetch<D, E4M3, NB>(a, &kmap, &vmap, w, ring, meta, bars, run, wait, lane, rest);
@@ -1171,26 +1186,38 @@ template <int D, bool E4M3, int NB>
 __global__ void __launch_bounds__(D) join_kernel(const __grid_constant__ DecodeArgs a) {
   constexpr int kHeads = 8 * NB;
   wait_for_previous();
-  const int4 head = reinterpret_cast<const int4*>(a.p.workspace)[blockIdx.x];
-  const int n = min(head.x, a.ctas - static_cast<int>(blockIdx.x)), h = blockIdx.y;
-  if (n < 2) return;
-  const RowAt r = row_at<E4M3, NB>(a, head.y);
-  if (h >= r.heads) return;
   constexpr int kAtOnce = 16;  // parts whose loads are in flight
-  float m = -INFINITY, l = 0.f, o = 0.f;
-  for (int i0 = 0; i0 < n; i0 += kAtOnce) {
-    float pm[kAtOnce], pl[kAtOnce], po[kAtOnce], top = m;
+  constexpr int kGuess = 4;    // parts that are loaded beside the header that says how many there are
+  const int h = blockIdx.y, left = a.ctas - static_cast<int>(blockIdx.x);
+  float pm[kAtOnce], pl[kAtOnce], po[kAtOnce];
+  auto load = [&](int i, int at, bool in) {
+    const Part x = part_at<D>(a.p.workspace, kHeads, blockIdx.x + at, at == 0);
+    pm[i] = in ? x.m[h] : -INFINITY;
+    pl[i] = in ? x.l[h] : 0.f;
+    po[i] = in ? x.o[h * D + threadIdx.x] : 0.f;
+  };
 #pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
+  for (int i = 0; i < kGuess; ++i) load(i, i, i < left);
+  const int4 head = reinterpret_cast<const int4*>(a.p.workspace)[blockIdx.x];
+  const int n = min(head.x, left);
+  if (n < 2) return;
+  const RowAt r = row_at<NB>(a, head.y);
+  if (h >= r.heads) return;
+  const float v_scale = value_scale<E4M3>(a, r.h);
+#pragma unroll
+  for (int i = 2; i < kGuess; ++i)
+    if (i >= n) {  // not of this row
       pm[i] = -INFINITY;
       pl[i] = po[i] = 0.f;
-      if (i0 + i < n) {
-        const Part x = part_at<D>(a.p.workspace, kHeads, blockIdx.x + i0 + i, i0 + i == 0);
-        pm[i] = x.m[h];
-        pl[i] = x.l[h];
-        po[i] = x.o[h * D + threadIdx.x];
-      }
     }
+#pragma unroll
+  for (int i = kGuess; i < kAtOnce; ++i) load(i, i, i < n);
+  float m = -INFINITY, l = 0.f, o = 0.f;
+  for (int i0 = 0; i0 < n; i0 += kAtOnce) {
+    if (i0 > 0)
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) load(i, i0 + i, i0 + i < n);
+    float top = m;
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i) top = fmaxf(top, pm[i]);
     const float zero = top == -INFINITY ? 0.f : top, fade = ex2_approx(m - zero);
@@ -1204,7 +1231,7 @@ __global__ void __launch_bounds__(D) join_kernel(const __grid_constant__ DecodeA
       o += po[i] * w;
     }
   }
-  r.o[h * a.p.os.head + threadIdx.x] = __float2bfloat16(o * inverse(l) * r.v_scale);
+  r.o[h * a.p.os.head + threadIdx.x] = __float2bfloat16(o * inverse(l) * v_scale);
   if (r.lse && threadIdx.x == 0) r.lse[h] = natural_lse(m, l);
 }
 
