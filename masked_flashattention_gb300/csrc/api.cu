@@ -7,6 +7,7 @@
 
 #include "../../include/cm.h"
 #include "kernels.h"
+#include "kv_cache.h"
 #include "program.h"
 #include "ptx.cuh"
 

@@ -4,7 +4,6 @@
 #include <cstdint>
 
 #include "../../include/cm.h"
-#include "kernels.h"
 #include "kv_cache.h"
 #include "ptx.cuh"
 

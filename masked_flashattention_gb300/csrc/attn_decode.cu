@@ -23,6 +23,7 @@
 // An e4m3 cache is widened to fp16 (exactly) between shared memory and the product; queries become
 // fp16 scaled by a power of two per head so that none overflows.
 #include <cuda_fp16.h>
+#include <atomic>
 
 #include "kv_cache.h"
 #include "ptx.cuh"
@@ -1253,23 +1254,31 @@ bool make_pool_map(CUtensorMap* map, const void* base, const KvView& c, int64_t 
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
-    return -1;
+constexpr int kMaxDevices = 64;  // beyond them, the properties below are asked for at every call
+
+int sm_count(int dev) {
+  static std::atomic<int> known[kMaxDevices];
+  int n = dev < kMaxDevices ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return -1;
+    if (dev < kMaxDevices) known[dev].store(n, std::memory_order_relaxed);
+  }
   return n < kMaxCtas ? n : kMaxCtas;
 }
 
 template <int D, bool E4M3, int NB>
-int launch(DecodeArgs& a, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream) {
+int launch(DecodeArgs& a, int dev, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream) {
   using C = Cfg<D, E4M3, NB>;
   // Where no row can have more than 4 tiles a warp pair, rows stay whole: the second kernel, 2 to 3 us on
   // the GPU and a launch, costs more than the few tiles by which runs then differ.
   a.whole_rows = a.most_tiles <= 4 * C::kPairs;
-  if (cudaFuncSetAttribute(decode_kernel<D, E4M3, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           C::kSmem) != cudaSuccess)
-    return -1;
+  static std::atomic<bool> allowed[kMaxDevices];  // the shared memory it needs
+  if (dev >= kMaxDevices || !allowed[dev].load(std::memory_order_relaxed)) {
+    if (cudaFuncSetAttribute(decode_kernel<D, E4M3, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             C::kSmem) != cudaSuccess)
+      return -1;
+    if (dev < kMaxDevices) allowed[dev].store(true, std::memory_order_relaxed);
+  }
   return launch_after(decode_kernel<D, E4M3, NB>, dim3(a.ctas), C::kThreads, C::kSmem, stream, a, k, v) &&
                  (a.whole_rows || launch_after(join_kernel<D, E4M3, NB>, dim3(a.ctas, a.group < C::kHeads ? a.group : C::kHeads), D,
                               0, stream, a))
@@ -1308,7 +1317,9 @@ int launch_attn_decode(const DecodeParams& p, uint64_t wait_ns, cudaStream_t str
   a.rows = p.sel ? a.chunks : p.c.H_kv * a.chunks;
   a.by_chunks = make_divisor(a.chunks);
   a.by_heads = make_divisor(p.c.H_kv);
-  a.ctas = sm_count();
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return -1;
+  a.ctas = sm_count(dev);
   a.min_run = 4;
   a.most_tiles = most_tiles(p);
   a.wait_ns = wait_ns;
@@ -1317,11 +1328,11 @@ int launch_attn_decode(const DecodeParams& p, uint64_t wait_ns, cudaStream_t str
   if (!make_pool_map(&k, p.c.k, p.c, p.c.k_page_bytes) || !make_pool_map(&v, p.c.v, p.c, p.c.v_page_bytes))
     return -1;
   if (heads == 8) {
-    if (p.c.d == 128) return p.c.e4m3 ? launch<128, true, 1>(a, k, v, stream) : launch<128, false, 1>(a, k, v, stream);
-    return p.c.e4m3 ? launch<64, true, 1>(a, k, v, stream) : launch<64, false, 1>(a, k, v, stream);
+    if (p.c.d == 128) return p.c.e4m3 ? launch<128, true, 1>(a, dev, k, v, stream) : launch<128, false, 1>(a, dev, k, v, stream);
+    return p.c.e4m3 ? launch<64, true, 1>(a, dev, k, v, stream) : launch<64, false, 1>(a, dev, k, v, stream);
   }
-  if (p.c.d == 128) return p.c.e4m3 ? launch<128, true, 2>(a, k, v, stream) : launch<128, false, 2>(a, k, v, stream);
-  return p.c.e4m3 ? launch<64, true, 2>(a, k, v, stream) : launch<64, false, 2>(a, k, v, stream);
+  if (p.c.d == 128) return p.c.e4m3 ? launch<128, true, 2>(a, dev, k, v, stream) : launch<128, false, 2>(a, dev, k, v, stream);
+  return p.c.e4m3 ? launch<64, true, 2>(a, dev, k, v, stream) : launch<64, false, 2>(a, dev, k, v, stream);
 }
 
 }  // namespace cm

@@ -16,9 +16,6 @@ const DevProg* spec_program(const cm_spec* s);
 // not possible.
 const void* pair_generated_kernel(const cm_spec* fwd, const cm_spec* bwd);
 
-// Limit of each bounded wait inside the kernels (cm_set_wait_limit_ns).
-uint64_t wait_limit_ns();
-
 struct FwdParams {
   const int32_t* itab;   // forward Interval Table [B][NI][S][2]
   const uint32_t* bm;    // forward bitmaps [B][NT][W]

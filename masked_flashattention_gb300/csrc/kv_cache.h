@@ -7,6 +7,9 @@
 
 namespace cm {
 
+// Limit of each bounded wait inside the kernels (cm_set_wait_limit_ns; kept in api.cu).
+uint64_t wait_limit_ns();
+
 // The cache and the sequences of a call (cm_kv_cache and cm_kv_seqs, checked).
 struct KvView {
   char* k;
