@@ -1188,8 +1188,12 @@ __global__ void __launch_bounds__(D) join_kernel(const __grid_constant__ DecodeA
   constexpr int kHeads = 8 * NB;
   wait_for_previous();
   constexpr int kAtOnce = 16;  // parts whose loads are in flight
-  constexpr int kGuess = 4;    // parts that are loaded beside the header that says how many there are
-  const int h = blockIdx.y, left = a.ctas - static_cast<int>(blockIdx.x);
+  const int4 head = reinterpret_cast<const int4*>(a.p.workspace)[blockIdx.x];
+  const int n = min(head.x, a.ctas - static_cast<int>(blockIdx.x)), h = blockIdx.y;
+  if (n < 2) return;
+  const RowAt r = row_at<NB>(a, head.y);
+  if (h >= r.heads) return;
+  const float v_scale = value_scale<E4M3>(a, r.h);
   float pm[kAtOnce], pl[kAtOnce], po[kAtOnce];
   auto load = [&](int i, int at, bool in) {
     const Part x = part_at<D>(a.p.workspace, kHeads, blockIdx.x + at, at == 0);
@@ -1197,27 +1201,10 @@ __global__ void __launch_bounds__(D) join_kernel(const __grid_constant__ DecodeA
     pl[i] = in ? x.l[h] : 0.f;
     po[i] = in ? x.o[h * D + threadIdx.x] : 0.f;
   };
-#pragma unroll
-  for (int i = 0; i < kGuess; ++i) load(i, i, i < left);
-  const int4 head = reinterpret_cast<const int4*>(a.p.workspace)[blockIdx.x];
-  const int n = min(head.x, left);
-  if (n < 2) return;
-  const RowAt r = row_at<NB>(a, head.y);
-  if (h >= r.heads) return;
-  const float v_scale = value_scale<E4M3>(a, r.h);
-#pragma unroll
-  for (int i = 2; i < kGuess; ++i)
-    if (i >= n) {  // not of this row
-      pm[i] = -INFINITY;
-      pl[i] = po[i] = 0.f;
-    }
-#pragma unroll
-  for (int i = kGuess; i < kAtOnce; ++i) load(i, i, i < n);
   float m = -INFINITY, l = 0.f, o = 0.f;
   for (int i0 = 0; i0 < n; i0 += kAtOnce) {
-    if (i0 > 0)
 #pragma unroll
-      for (int i = 0; i < kAtOnce; ++i) load(i, i0 + i, i0 + i < n);
+    for (int i = 0; i < kAtOnce; ++i) load(i, i0 + i, i0 + i < n);
     float top = m;
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i) top = fmaxf(top, pm[i]);
