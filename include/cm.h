@@ -333,7 +333,7 @@ typedef struct cm_kv_cache {
 } cm_kv_cache;
 
 /* The sequences of a call: page_table device int32 [B][max_pages], lens device int32 [B].
- * Entries of the table past a sequence's tokens are never read.  B at most 32767; max_pages *
+ * Entries of the table past a sequence's tokens may hold anything.  B at most 32767; max_pages *
  * page_size at most 2^27; for cm_attn_decode, the keys a table (or a selection) has room for, times
  * B * H_q, below 2^39. */
 typedef struct cm_kv_seqs {

@@ -1,40 +1,49 @@
-// Selection of the pages a new token attends to (cm_select_pages): two kernels.
+// Selection of the pages a new token attends to (cm_select_pages): one kernel, one cluster of blocks a row (a
+// sequence's key-value head).
 //
-// score_kernel.  What bounds it: the summaries, 2 d + 4 bytes a page and key-value head, each read
-// once.  A warp takes one key-value head and up to 128 pages of a sequence, 16 at a time: the
-// summaries go from memory straight into the A operand of an integer tensor-core product
-// (m16n8k32, 16 pages x 8 query heads), 16 bytes a lane; since a dot product takes its channels in any order, the
-// lanes' own 16 bytes serve as the k index and nothing is rearranged.  With x split into its positive
-// and negative part, the score is one dot product over 2 d channels:
+// Scores.  What bounds them: the summaries, 2 d + 4 bytes a page and key-value head, each read once.  A
+// warp takes 32 pages at a time: the summaries go from memory straight into the A operand of a tensor-core
+// product (m16n8k16, 16 pages x 8 query heads), 16 bytes a lane; since a dot product takes its channels
+// in any order, the lanes' own 16 bytes serve as the k index and nothing is rearranged.  With x split
+// into its positive and negative part, the score is one dot product over 2 d channels:
 //   sum_c (x_c > 0 ? x_c largest_c : x_c smallest_c) = x+ . largest + x- . smallest.
-// Sums are 32-bit integers (at most 2 * 128 * 127^2 < 2^23), and fp32 holds them and their
-// scaling by powers of two exactly, so no order of summation shows in the selection.
+// An 8-bit integer product would be its natural form, but this GPU takes 65 cycles for an m16n8k32 of
+// that type (8 for an m16n8k16 of fp16, measured), which bound the kernel.  A byte y + 128 behind a
+// zero byte is the fp16 number (y + 128) * 2^-24, so one permutation a channel pair makes
+// the operand, and 128 * sum x is taken off at the end.  Every partial sum is a whole number below 2^23 (2 * 128 *
+// 127 * 255) times 2^-24: fp32 holds it, and the scaling by powers of two, exactly, so no order of summation
+// shows in the selection.  A row's blocks take every cs-th 32 pages, so that any length is dealt out
+// evenly; one block a row where there are rows enough for the GPU, up to 8 where there are few.
 //
-// pick_kernel.  One block a row.  Every thread holds consecutive pages in registers.  A histogram of
-// 1024 equal ranges of the row's scores finds the range that the last page taken falls into; only
-// the few pages in that range are ranked against each other (a bisection over the score's bits where they
-// are many, as with equal scores), and two scans over the block write the pages in order.
+// Choice, by a row's first block: every thread holds consecutive pages in registers.  A histogram of 1024
+// equal ranges of the row's scores finds the range that the last page taken falls into; only the few
+// pages in that range are ranked against each other (a bisection over the score's bits where they are
+// many, as with equal scores), and scans over the block write the pages in order.
+//
+// Two kernels, scores by a warp a head with 16 to 64 pages, then this choice, took 19.7 us for 32
+// sequences of up to 1024 pages and 8.7 us for 1 of 2048: rounding the queries for so few pages a warp took
+// more instructions than the products.
+#include <cuda_fp16.h>
+#include <type_traits>
+
 #include "kv_cache.h"
 #include "ptx.cuh"
 
 namespace cm {
 namespace {
 
-constexpr int kScoreWarps = 8;
-constexpr int kMaxSteps = 8;   // of 16 pages a warp
 constexpr int kBins = 1024;
 constexpr int kListed = 1024;  // pages of a range that are ranked by comparing all pairs
 
-__device__ __forceinline__ void mma16832_s8(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                            uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+__device__ __forceinline__ void mma16816_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
-      : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ int pages_of(const SelectParams& p, int b, bool report) {
-  const int len = p.c.lens[b];
+__device__ __forceinline__ int pages_of(const SelectParams& p, int b, int len, bool report) {
   if (len < 0 || static_cast<int64_t>(len) > (static_cast<int64_t>(p.c.max_pages) << p.c.log2_page)) {
     if (report) set_status(p.c.status, kDevBadMeta, b);
     return 0;
@@ -42,129 +51,147 @@ __device__ __forceinline__ int pages_of(const SelectParams& p, int b, bool repor
   return (len + (1 << p.c.log2_page) - 1) >> p.c.log2_page;
 }
 
-// 8-bit queries of up to 8 heads, x+ then x-, into the warp's shared memory; returns the power of two of head
-// lane / 4 (each head's 4 lanes hold D / 4 channels each).
-template <int D, int PITCH>
-__device__ __forceinline__ float quantise(const __nv_bfloat16* q, int64_t head_stride, int heads, int8_t* to,
-                                          int lane) {
-  const int h = lane >> 2, c0 = (lane & 3) * (D / 4);
-  uint4 w[D / 32];
-  float top = 0.f;
+// 8-bit queries of up to 8 heads as fp16, x+ then x-, in shared memory; the powers of two of their scales, and
+// 128 * sum x: a warp a head, D / 32 channels a lane.
+template <int D, int T>
+__device__ __forceinline__ void quantise(const SelectParams& p, const __nv_bfloat16* q, int heads, __half* to,
+                                         int pitch, float* power, float* excess) {
+  constexpr int kWords = D / 64;  // of two channels
+  const int lane = lane_id();
+  for (int h = threadIdx.x / 32; h < 8; h += T / 32) {
+    uint32_t w[kWords];
+    float top = 0.f;
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i) {
-    w[i] = h < heads ? *reinterpret_cast<const uint4*>(q + h * head_stride + c0 + 8 * i) : make_uint4(0, 0, 0, 0);
-    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u[j] << 16)), fabsf(__uint_as_float(u[j] & 0xFFFF0000u))));
-  }
-  top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-  top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-  const int f = scale_exponent(top);
-  const float inv = pow2_bits(-f);
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) {
-    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-    uint32_t pos[2] = {0, 0}, neg[2] = {0, 0};
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float v = __uint_as_float(j & 1 ? u[j >> 1] & 0xFFFF0000u : u[j >> 1] << 16);
-      const int x = static_cast<int>(fminf(fmaxf(rintf(v * inv), -127.f), 127.f));
-      pos[j >> 2] |= static_cast<uint32_t>(max(x, 0)) << (8 * (j & 3));
-      neg[j >> 2] |= static_cast<uint32_t>(min(x, 0) & 0xFF) << (8 * (j & 3));
+    for (int i = 0; i < kWords; ++i) {
+      w[i] = h < heads ? *reinterpret_cast<const uint32_t*>(q + h * p.qs.head + lane * 2 * kWords + 2 * i) : 0u;
+      top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xFFFF0000u))));
     }
-    *reinterpret_cast<uint2*>(to + h * PITCH + c0 + 8 * i) = make_uint2(pos[0], pos[1]);
-    *reinterpret_cast<uint2*>(to + h * PITCH + D + c0 + 8 * i) = make_uint2(neg[0], neg[1]);
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+    const int f = scale_exponent(top);
+    const float inv = pow2_bits(-f);
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      const float a = fminf(fmaxf(rintf(__uint_as_float(w[i] << 16) * inv), -127.f), 127.f);
+      const float b = fminf(fmaxf(rintf(__uint_as_float(w[i] & 0xFFFF0000u) * inv), -127.f), 127.f);
+      __half2* row = reinterpret_cast<__half2*>(to + h * pitch + lane * 2 * kWords) + i;
+      row[0] = __floats2half2_rn(fmaxf(a, 0.f), fmaxf(b, 0.f));
+      row[D / 2] = __floats2half2_rn(fminf(a, 0.f), fminf(b, 0.f));
+      sum += a + b;
+    }
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+    if (lane == 0) {
+      power[h] = pow2_bits(f);
+      excess[h] = 128.f * sum;
+    }
   }
-  return pow2_bits(f);
 }
 
+// Summaries of 16 pages as a lane holds them: 16-byte pieces of pages lane / 4 and 8 further.
 template <int D>
-__global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const SelectParams p, int steps) {
-  constexpr int kPitch = 2 * D + 64;  // keeps the fragments' reads free of bank conflicts
-  constexpr int kLoads = 2 * D / 64;  // 16-byte loads of a lane for one row
-  __shared__ __align__(16) int8_t queries[kScoreWarps][8 * kPitch];
-  let_next_start();
-  wait_for_previous();
-  const int warp = threadIdx.x / 32, lane = lane_id(), t = lane & 3, r = lane >> 2;
-  const int b = blockIdx.z, g = blockIdx.y * (blockDim.x / 32) + warp, first = blockIdx.x * 16 * steps;
-  if (g >= p.c.H_kv) return;
-  const int pages = pages_of(p, b, blockIdx.x == 0 && threadIdx.x == 0);
-  if (first >= pages) return;
-  const int group = p.H_q / p.c.H_kv, n = min(16 * steps, pages - first);
-  // page numbers: page 32 i + lane of the warp's
-  int number[kMaxSteps / 2];
-#pragma unroll
-  for (int i = 0; i < kMaxSteps / 2; ++i) {
-    number[i] = -1;
-    if (32 * i + lane < n) {
-      number[i] = p.c.table[static_cast<int64_t>(b) * p.c.max_pages + first + 32 * i + lane];
-      if (static_cast<unsigned>(number[i]) >= static_cast<unsigned>(p.c.num_pages)) {
-        set_status(p.c.status, kDevBadMeta, b);
-        number[i] = -1;
-      }
-    }
-  }
-  float best[kMaxSteps][2];
-#pragma unroll
-  for (int s = 0; s < kMaxSteps; ++s) best[s][0] = best[s][1] = -INFINITY;
-  for (int h0 = 0; h0 < group; h0 += 8) {
-    const int heads = min(8, group - h0);
-    const __nv_bfloat16* q = p.q + b * p.qs.seq + static_cast<int64_t>(g * group + h0) * p.qs.head;
-    __syncwarp();
-    const float power = quantise<D, kPitch>(q, p.qs.head, heads, queries[warp], lane);
-    __syncwarp();
-    uint4 x[kLoads];
-#pragma unroll
-    for (int j = 0; j < kLoads; ++j)
-      x[j] = *reinterpret_cast<const uint4*>(&queries[warp][r * kPitch + j * 64 + t * 16]);
-    const float power0 = __shfl_sync(0xFFFFFFFFu, power, t * 8), power1 = __shfl_sync(0xFFFFFFFFu, power, t * 8 + 4);
-#pragma unroll
-    for (int s = 0; s < kMaxSteps; ++s) {
-      if (16 * s >= n) break;
-      int64_t at[2];
-      uint4 y[2][kLoads];
-      float scale[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int page = __shfl_sync(0xFFFFFFFFu, number[s / 2], (s & 1) * 16 + i * 8 + r);
-        at[i] = page < 0 ? -1 : static_cast<int64_t>(page) * p.c.H_kv + g;
-        scale[i] = page < 0 ? 0.f : __ldg(p.c.summary_scale + at[i]);
-#pragma unroll
-        for (int j = 0; j < kLoads; ++j)
-          y[i][j] = page < 0 ? make_uint4(0, 0, 0, 0)
-                             : __ldg(reinterpret_cast<const uint4*>(p.c.summary + at[i] * 2 * D + j * 64 + t * 16));
-      }
-      int c[4] = {0, 0, 0, 0};
-#pragma unroll
-      for (int j = 0; j < kLoads; ++j) {
-        mma16832_s8(c, y[0][j].x, y[1][j].x, y[0][j].y, y[1][j].y, x[j].x, x[j].y);
-        mma16832_s8(c, y[0][j].z, y[1][j].z, y[0][j].w, y[1][j].w, x[j].z, x[j].w);
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (at[i] < 0) continue;
-        if (2 * t < heads) best[s][i] = fmaxf(best[s][i], static_cast<float>(c[2 * i]) * power0 * scale[i]);
-        if (2 * t + 1 < heads) best[s][i] = fmaxf(best[s][i], static_cast<float>(c[2 * i + 1]) * power1 * scale[i]);
-      }
-    }
-  }
-  float* out = p.scores + (static_cast<int64_t>(b) * p.c.H_kv + g) * score_pitch(p.c.max_pages);
-#pragma unroll
-  for (int s = 0; s < kMaxSteps; ++s)
+struct Summaries {
+  static constexpr int kLoads = 2 * D / 64;
+  uint4 y[2][kLoads];
+  float scale[2];  // -1: no such page
+  __device__ __forceinline__ void load(const SelectParams& p, int g, int number, int half, int lane) {
+    const int t = lane & 3, r = lane >> 2;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      float v = best[s][i];
-      v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 1));
-      v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 2));
-      const int m = 16 * s + 8 * i + r;
-      if (t == 0 && m < n) out[first + m] = v;
+      const int page = __shfl_sync(0xFFFFFFFFu, number, half * 16 + i * 8 + r);
+      const int64_t at = static_cast<int64_t>(page) * p.c.H_kv + g;
+      scale[i] = page < 0 ? -1.f : __ldg(p.c.summary_scale + at);
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j)
+        y[i][j] = page < 0 ? make_uint4(0, 0, 0, 0)
+                           : __ldg(reinterpret_cast<const uint4*>(p.c.summary + at * 2 * D + j * 64 + t * 16));
     }
+  }
+};
+
+// The block's share of a row's scores: 32 pages a warp, every cs-th such piece.
+template <int D, int T>
+__device__ __forceinline__ void score_pages(const SelectParams& p, int b, int g, int pages, int rank, int cs, int number,
+                                            float* out, __half* queries, float* power, float* excess) {
+  constexpr int kPitch = 2 * D + 32;  // 64 spare bytes keep the fragments' reads free of bank conflicts
+  constexpr int kLoads = Summaries<D>::kLoads;
+  const int warp = threadIdx.x / 32, lane = lane_id(), t = lane & 3, r = lane >> 2;
+  const int group = p.H_q / p.c.H_kv;
+  const int32_t* table = p.c.table + static_cast<int64_t>(b) * p.c.max_pages;
+  const int piece0 = warp * cs + rank;
+#pragma unroll 1
+  for (int h0 = 0; h0 < group; h0 += 8) {
+    const int heads = min(8, group - h0);
+    if (h0 > 0) __syncthreads();
+    quantise<D, T>(p, p.q + b * p.qs.seq + static_cast<int64_t>(g * group + h0) * p.qs.head, heads, queries, kPitch, power, excess);
+    __syncthreads();
+    uint4 x[kLoads][2];  // channels of the lane's 16 bytes
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        x[j][i] = *reinterpret_cast<const uint4*>(queries + r * kPitch + j * 64 + t * 16 + i * 8);
+    const float excess0 = excess[2 * t], excess1 = excess[2 * t + 1];
+    const float power0 = power[2 * t], power1 = power[2 * t + 1];
+    const bool in0 = 2 * t < heads, in1 = 2 * t + 1 < heads;
+    const int stride = 32 * (T / 32) * cs;  // pages from a warp's piece to its next
+    int next = number;
+#pragma unroll 1
+    for (int m0 = 32 * piece0; m0 < pages; m0 += stride) {
+      int page = m0 + lane < pages ? next : -1;
+      if (m0 + lane < pages && static_cast<unsigned>(page) >= static_cast<unsigned>(p.c.num_pages)) {
+        set_status(p.c.status, kDevBadMeta, b);
+        page = -1;
+      }
+      Summaries<D> now[2];
+      now[0].load(p, g, page, 0, lane);
+      now[1].load(p, g, page, 1, lane);
+      const int ahead = m0 + stride + lane;
+      next = ahead < pages ? table[ahead] : -1;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        float c[4] = {0.f, 0.f, 0.f, 0.f};
+        auto product = [&](uint32_t y0, uint32_t y1, uint32_t b0, uint32_t b1) {  // 4 channels a lane
+          y0 ^= 0x80808080u;
+          y1 ^= 0x80808080u;
+          mma16816_f16(c, __byte_perm(y0, 0, 0x4140), __byte_perm(y1, 0, 0x4140), __byte_perm(y0, 0, 0x4342),
+                       __byte_perm(y1, 0, 0x4342), b0, b1);
+        };
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+          const uint4 y0 = now[half].y[0][j], y1 = now[half].y[1][j];
+          product(y0.x, y1.x, x[j][0].x, x[j][0].y);
+          product(y0.y, y1.y, x[j][0].z, x[j][0].w);
+          product(y0.z, y1.z, x[j][1].x, x[j][1].y);
+          product(y0.w, y1.w, x[j][1].z, x[j][1].w);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float scale = now[half].scale[i];
+          float v = -INFINITY;
+          if (scale >= 0.f) {
+            if (in0) v = __fmaf_rn(c[2 * i], 16777216.f, -excess0) * power0 * scale;
+            if (in1) v = fmaxf(v, __fmaf_rn(c[2 * i + 1], 16777216.f, -excess1) * power1 * scale);
+          }
+          v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 1));
+          v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 2));
+          const int at = m0 + 16 * half + 8 * i + r;
+          if (t == 0 && at < pages) {
+            if (h0 > 0) v = fmaxf(v, __ldcg(out + at));  // of the group's heads before
+            out[at] = v;
+          }
+        }
+      }
+    }
+  }
 }
 
 // Exclusive scan of one number a thread over the block; `total` is the sum.  `sums` [32].
+template <int T>
 __device__ __forceinline__ int block_scan(int x, int* sums, int& total) {
-  const int lane = lane_id(), warp = threadIdx.x / 32, warps = blockDim.x / 32;
+  const int lane = lane_id(), warp = threadIdx.x / 32;
+  constexpr int warps = T / 32;
   int s = x;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -191,39 +218,59 @@ __device__ __forceinline__ uint32_t key_of(float s) {
   return u ^ (u & 0x80000000u ? 0xFFFFFFFFu : 0x80000000u);
 }
 
-template <int E>  // pages of a thread
-__global__ void __launch_bounds__(1024) pick_kernel(const SelectParams p) {
+template <int D, int T, int E>  // T threads, E pages of a thread
+__global__ void __launch_bounds__(T, 512 / T) select_kernel(const SelectParams p, int cs) {
+  __shared__ __align__(16) __half queries[8 * (2 * D + 32)];
+  __shared__ float power[8], excess[8];
   __shared__ int bins[kBins + kBins / 32];  // one spare word a 32, for the scan's reads
   __shared__ uint32_t listed[kListed];
   __shared__ int sums[32];
   __shared__ float range[2][32];
   __shared__ int found[4];                  // range, pages needed of it, pages in it
-  __shared__ uint32_t limit[2];             // score of the last page taken, pages of that score taken
+  __shared__ uint32_t limit[3];             // score of the last page taken; pages of it taken, and in all
   let_next_start();
   wait_for_previous();
-  const int b = blockIdx.y, tid = threadIdx.x, lane = lane_id(), warp = tid / 32, warps = blockDim.x / 32;
-  const int64_t row = static_cast<int64_t>(b) * p.c.H_kv + blockIdx.x;
-  const int pages = pages_of(p, b, false), take = min(pages, p.sel_max);
+  const int g = blockIdx.x / cs, rank = blockIdx.x - g * cs, b = blockIdx.y;
+  const int tid = threadIdx.x, lane = lane_id(), warp = tid / 32;
+  constexpr int warps = T / 32;
+  const int64_t row = static_cast<int64_t>(b) * p.c.H_kv + g;
+  // the first page numbers are read beside the length, before it is known how many of them count
+  const int first = 32 * (warp * cs + rank) + lane;
+  const int number = first < p.c.max_pages ? p.c.table[static_cast<int64_t>(b) * p.c.max_pages + first] : -1;
+  const int len = p.c.lens[b];
+  const int pages = pages_of(p, b, len, g == 0 && rank == 0 && tid == 0);
+  const int take = min(pages, p.sel_max), last = pages - p.keep_last;
   int32_t* sel = p.sel + row * p.sel_max;
-  if (tid == 0) p.nsel[row] = take;
-  for (int i = take + tid; i < p.sel_max; i += blockDim.x) sel[i] = -1;
-  if (take == pages) {
-    for (int i = tid; i < pages; i += blockDim.x) sel[i] = i;
+  if (rank == 0) {
+    if (tid == 0) p.nsel[row] = take;
+    for (int i = take + tid; i < p.sel_max; i += T) sel[i] = -1;
+  }
+  if (take == pages) {  // all of them: the same answer in every block of the row
+    if (rank == 0)
+      for (int i = tid; i < pages; i += T) sel[i] = i;
     return;
   }
-  const float* from = p.scores + row * score_pitch(p.c.max_pages) + tid * E;
-  const int base = tid * E, last = pages - p.keep_last;
+  float* scores = p.scores + row * score_pitch(p.c.max_pages);
+  score_pages<D, T>(p, b, g, pages, rank, cs, number, scores, queries, power, excess);
+  if (cs > 1) {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (rank != 0) return;
+  } else {
+    __syncthreads();
+  }
+  const int base = tid * E;
   float s[E];
-  float low = INFINITY, high = -INFINITY;
 #pragma unroll
   for (int e = 0; e < E; e += 4) {
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (base + e < pages) v = *reinterpret_cast<const float4*>(from + e);
+    if (base + e < pages) v = __ldcg(reinterpret_cast<const float4*>(scores + base + e));
     s[e] = v.x;
     s[e + 1] = v.y;
     s[e + 2] = v.z;
     s[e + 3] = v.w;
   }
+  float low = INFINITY, high = -INFINITY;
   // pages in the running: neither kept anyway nor behind the end
   auto runs = [&](int e) { return base + e >= p.keep_first && base + e < last; };
 #pragma unroll
@@ -241,7 +288,7 @@ __global__ void __launch_bounds__(1024) pick_kernel(const SelectParams p) {
     range[0][warp] = low;
     range[1][warp] = high;
   }
-  for (int i = tid; i < kBins + kBins / 32; i += blockDim.x) bins[i] = 0;
+  for (int i = tid; i < kBins + kBins / 32; i += T) bins[i] = 0;
   __syncthreads();
   low = lane < warps ? range[0][lane] : INFINITY;
   high = lane < warps ? range[1][lane] : -INFINITY;
@@ -266,25 +313,29 @@ __global__ void __launch_bounds__(1024) pick_kernel(const SelectParams p) {
   const int need = take - min(p.keep_first, pages) - p.keep_last;  // of those in the running; may be 0
   if (warp == 0) {  // lane 0 has the highest 32 ranges
     int mine = 0;
-    for (int i = 0; i < 32; ++i) mine += bins[(31 - lane) * 33 + i];
-    int above = mine;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int y = __shfl_up_sync(0xFFFFFFFFu, above, d);
-      if (lane >= d) above += y;
-    }
-    above -= mine;
-    if (above < need && above + mine >= need) {
-      int i = 31;
-      for (; above + bins[(31 - lane) * 33 + i] < need; --i) above += bins[(31 - lane) * 33 + i];
-      found[0] = (31 - lane) * 32 + i;
-      found[1] = need - above;
-      found[2] = bins[(31 - lane) * 33 + i];
+    for (int i = 0; i < 32; ++i) mine += bins[(31 - lane) * 33 + i];
+    auto scan = [&](int x) {  // of the lanes up to this one
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xFFFFFFFFu, x, d);
+        if (lane >= d) x += y;
+      }
+      return x;
+    };
+    const int sum = scan(mine), part = __ffs(__ballot_sync(0xFFFFFFFFu, sum >= need)) - 1;
+    const int above = __shfl_sync(0xFFFFFFFFu, sum - mine, max(part, 0));
+    const int count = bins[(31 - max(part, 0)) * 33 + 31 - lane];  // lane 0 has the highest range of the 32
+    const int upto = above + scan(count), one = __ffs(__ballot_sync(0xFFFFFFFFu, upto >= need)) - 1;
+    if (lane == one && part >= 0) {
+      found[0] = (31 - part) * 32 + 31 - lane;
+      found[1] = need - (upto - count);
+      found[2] = count;
     }
   }
   if (tid == 0) {
     found[3] = 0;
-    limit[0] = limit[1] = 0;
+    limit[0] = limit[1] = limit[2] = 0;
   }
   __syncthreads();
   const int bin = need > 0 ? found[0] : kBins, want = found[1], many = found[2];
@@ -293,7 +344,7 @@ __global__ void __launch_bounds__(1024) pick_kernel(const SelectParams p) {
     for (int e = 0; e < E; ++e)
       if (runs(e) && bin_of(s[e]) == bin) listed[atomicAdd(&found[3], 1)] = key_of(s[e]);
     __syncthreads();
-    for (int i = tid; i < many; i += blockDim.x) {
+    for (int i = tid; i < many; i += T) {
       const uint32_t k = listed[i];
       int above = 0, equal = 0;
       for (int j = 0; j < many; ++j) {
@@ -303,6 +354,7 @@ __global__ void __launch_bounds__(1024) pick_kernel(const SelectParams p) {
       if (above < want && above + equal >= want) {  // the same numbers from every page of this score
         limit[0] = k;
         limit[1] = want - above;
+        limit[2] = equal;
       }
     }
     __syncthreads();
@@ -315,69 +367,88 @@ __global__ void __launch_bounds__(1024) pick_kernel(const SelectParams p) {
 #pragma unroll
       for (int e = 0; e < E; ++e) n += runs(e) && bin_of(s[e]) == bin && key_of(s[e]) >= trial;
       int total;
-      block_scan(n, sums, total);
+      block_scan<T>(n, sums, total);
       if (total >= want) k = trial;
     }
     int n = 0;
 #pragma unroll
     for (int e = 0; e < E; ++e) n += runs(e) && bin_of(s[e]) == bin && key_of(s[e]) > k;
-    block_scan(n, sums, above);
+    block_scan<T>(n, sums, above);
     if (tid == 0) {
       limit[0] = k;
       limit[1] = want - above;
+      limit[2] = many;  // not counted: at least limit[1]
     }
     __syncthreads();
   }
   const uint32_t border = limit[0];
   const int ties = static_cast<int>(limit[1]);
   // in order: the pages of the border's score, then all pages taken
-  uint32_t taken = 0, equal = 0;
+  using Mask = std::conditional_t<(E > 32), uint64_t, uint32_t>;
+  Mask taken = 0, equal = 0;
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     if (base + e >= pages) continue;
     if (!runs(e)) {
-      taken |= 1u << e;
+      taken |= Mask(1) << e;
       continue;
     }
     const int i = bin_of(s[e]);
     const uint32_t k = key_of(s[e]);
-    if (i > bin || (i == bin && k > border)) taken |= 1u << e;
-    if (i == bin && k == border) equal |= 1u << e;
+    if (i > bin || (i == bin && k > border)) taken |= Mask(1) << e;
+    if (i == bin && k == border) equal |= Mask(1) << e;
   }
   int total;
-  int rank = block_scan(__popc(equal), sums, total);
+  if (limit[2] == limit[1]) {
+    taken |= equal;
+  } else {  // the first of equals
+    int rank = block_scan<T>(__popcll(equal), sums, total);
 #pragma unroll
-  for (int e = 0; e < E; ++e)
-    if ((equal >> e) & 1u) {
-      if (rank < ties) taken |= 1u << e;
-      ++rank;
-    }
-  int at = block_scan(__popc(taken), sums, total);
+    for (int e = 0; e < E; ++e)
+      if ((equal >> e) & 1u) {
+        if (rank < ties) taken |= Mask(1) << e;
+        ++rank;
+      }
+  }
+  int at = block_scan<T>(__popcll(taken), sums, total);
 #pragma unroll
   for (int e = 0; e < E; ++e)
     if ((taken >> e) & 1u) sel[at++] = base + e;
 }
 
+template <int D, int T, int E>
+bool launch(const SelectParams& p, cudaStream_t stream) {
+  const int64_t rows = static_cast<int64_t>(p.c.B) * p.c.H_kv;
+  // blocks of a row: as many as leave every block of all rows resident (512 threads an SM), and 32 pages for
+  // each of their warps
+  int cs = 1;
+  while (cs < 8 && rows * 2 * cs <= 152 * (512 / T) && p.c.max_pages > T * cs) cs *= 2;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cs;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.c.H_kv * cs, p.c.B);
+  cfg.blockDim = dim3(T);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, select_kernel<D, T, E>, p, cs) == cudaSuccess;
+}
+
+template <int D>
+bool launch(const SelectParams& p, cudaStream_t stream) {
+  if (p.c.max_pages <= 2048) return launch<D, 256, 8>(p, stream);
+  if (p.c.max_pages <= 8192) return launch<D, 512, 16>(p, stream);
+  return launch<D, 512, 64>(p, stream);
+}
+
 }  // namespace
 
 int launch_select_pages(const SelectParams& p, cudaStream_t stream) {
-  const int warps = p.c.H_kv < kScoreWarps ? p.c.H_kv : kScoreWarps;
-  // pages of a warp: enough warps to fill the GPU first (152 SMs x 16), then fewer queries to round
-  int steps = 1;
-  while (steps < kMaxSteps &&
-         static_cast<int64_t>(p.c.B) * p.c.H_kv * ((p.c.max_pages + 32 * steps - 1) / (32 * steps)) >= 152 * 16)
-    steps *= 2;
-  const dim3 grid((p.c.max_pages + 16 * steps - 1) / (16 * steps), (p.c.H_kv + warps - 1) / warps, p.c.B);
-  const bool scored = p.c.d == 128 ? launch_after(score_kernel<128>, grid, 32 * warps, 0, stream, p, steps)
-                                   : launch_after(score_kernel<64>, grid, 32 * warps, 0, stream, p, steps);
-  if (!scored) return -1;
-  const dim3 rows(p.c.H_kv, p.c.B);
-  const int e = p.c.max_pages <= 8192 ? 8 : 32;
-  const int threads = ((p.c.max_pages + e - 1) / e + 31) / 32 * 32;
-  return (e == 8 ? launch_after(pick_kernel<8>, rows, threads, 0, stream, p)
-                 : launch_after(pick_kernel<32>, rows, threads, 0, stream, p))
-             ? 0
-             : -1;
+  return (p.c.d == 128 ? launch<128>(p, stream) : launch<64>(p, stream)) ? 0 : -1;
 }
 
 }  // namespace cm
