@@ -129,7 +129,6 @@ CM_API int cm_kv_append(const cm_kv_cache* cache, const cm_kv_seqs* seqs, const 
     return CM_ERR_INVALID_ARG;
   if ((t->cu_new ? t->n_tokens : static_cast<int64_t>(seqs->B) * t->max_new) > (1LL << 30))
     return CM_ERR_UNSUPPORTED;
-  if ((t->max_new + cache->page_size - 2) / cache->page_size + 1 > 65535) return CM_ERR_UNSUPPORTED;
   cm::AppendParams p;
   p.c = view(cache, seqs);
   p.k = static_cast<const __nv_bfloat16*>(t->k);
@@ -152,6 +151,7 @@ CM_API int cm_kv_append(const cm_kv_cache* cache, const cm_kv_seqs* seqs, const 
   p.rope_len = t->rope_len;
   p.rope = t->rope;
   p.new_lens = t->new_lens;
+  if (cm::append_page_blocks(p) > (1LL << 30)) return CM_ERR_UNSUPPORTED;
   return cm::launch_kv_append(p, static_cast<cudaStream_t>(stream)) == 0 ? CM_OK : CM_ERR_CUDA;
 }
 

@@ -156,19 +156,63 @@ __device__ __forceinline__ void rotate_pieces(uint4& w0, uint4& w1, const float2
   w1 = pack8(hi);
 }
 
+// Sequence and page (of those that it adds to) of page number `item` of all that the call touches; false where
+// there are fewer.  SCAN: items are dealt out without gaps, by a scan over the sequences, 256 at a time, in which
+// the whole block takes part; else a sequence has `segs` of them, and those it does not need end at once.
+template <bool SCAN>
+__device__ __forceinline__ bool find_page(const AppendParams& p, int item, int segs, int& b, int& seg) {
+  if constexpr (!SCAN) {
+    b = item / segs;
+    seg = item - b * segs;
+    return true;
+  }
+  __shared__ int sums[kThreads / 32], found[2];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
+  if (tid == 0) found[0] = -1;
+  for (int b0 = 0, before = 0; b0 < p.c.B && before <= item; b0 += kThreads) {
+    int start, count, base, pages = 0;
+    if (b0 + tid < p.c.B && new_tokens(p, b0 + tid, start, count, base) && count > 0)
+      pages = ((start + count - 1) >> p.c.log2_page) - (start >> p.c.log2_page) + 1;
+    int sum = pages;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int x = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+      if (lane >= d) sum += x;
+    }
+    __syncthreads();  // the sums before have been read
+    if (lane == 31) sums[warp] = sum;
+    __syncthreads();
+    sum += before;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) sum += sums[w];
+      before += sums[w];
+    }
+    if (item >= sum - pages && item < sum) {
+      found[0] = b0 + tid;
+      found[1] = item - (sum - pages);
+    }
+  }
+  __syncthreads();
+  b = found[0];
+  seg = found[1];
+  return b >= 0;
+}
+
 // A block's share of the second role.
-template <int D, bool E4M3, bool INTER>
+template <int D, bool E4M3, bool INTER, bool SCAN>
 __device__ __forceinline__ void store_keys_by_page(const AppendParams& p, int segs, uint4* ring) {
   constexpr int kPer = D / 16;       // threads of a row
   constexpr int kRows = 32 / kPer;   // rows of a step
   constexpr int kItem = E4M3 ? 1 : 2;
   const int tid = threadIdx.x, lane = tid & 31, P = 1 << p.c.log2_page;
   const int head_blocks = (p.c.H_kv + kThreads / 32 - 1) / (kThreads / 32);
-  const int rest = blockIdx.x / head_blocks, b = rest / segs;
-  const int h = (blockIdx.x - rest * head_blocks) * (kThreads / 32) + tid / 32;
-  int start, count, base;
+  const int item = blockIdx.x / head_blocks;
+  const int h = (blockIdx.x - item * head_blocks) * (kThreads / 32) + tid / 32;
+  int b, seg, start, count, base;
+  if (!find_page<SCAN>(p, item, segs, b, seg)) return;
   if (!new_tokens(p, b, start, count, base) || h >= p.c.H_kv) return;
-  const int place = (start >> p.c.log2_page) + rest - b * segs, first = place << p.c.log2_page;
+  const int place = (start >> p.c.log2_page) + seg, first = place << p.c.log2_page;
   const int lo = max(start, first) - first, hi = min(start + count, first + P) - first;  // new rows of the page
   if (lo >= hi) return;
   const int page = p.c.table[static_cast<int64_t>(b) * p.c.max_pages + place];
@@ -300,7 +344,7 @@ __device__ __forceinline__ void store_keys_by_page(const AppendParams& p, int se
 }
 
 // Blocks 0 .. page_blocks-1 have the second role.
-template <int D, bool E4M3, bool INTER>
+template <int D, bool E4M3, bool INTER, bool SCAN>
 __global__ void __launch_bounds__(kThreads, 4)
     append_kernel(const AppendParams p, int log2_tokens, int page_blocks, int segs) {
   constexpr int kPer = D / 16;  // threads of a token's head
@@ -310,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 4)
   let_next_start();
   wait_for_previous();
   if (static_cast<int>(blockIdx.x) < page_blocks) {
-    store_keys_by_page<D, E4M3, INTER>(p, segs, ring);
+    store_keys_by_page<D, E4M3, INTER, SCAN>(p, segs, ring);
     return;
   }
   const int block = blockIdx.x - page_blocks;
@@ -431,6 +475,24 @@ __global__ void __launch_bounds__(kThreads, 4)
   }
 }
 
+// The most pages a run of max_new tokens can touch.
+int append_segments(const AppendParams& p) {
+  const int P = 1 << p.c.log2_page;
+  return (p.max_new + P - 2) / P + 1;
+}
+// Pages that blocks are launched for, and whether they are dealt out by a scan.  Packed tokens: every page but a
+// sequence's first and last takes a page's worth of them, so a batch of a few long prompts among many
+// single tokens has far fewer than `segs` for each sequence.  A block that finds nothing to do takes about
+// 1 us of one of 608 places, the scan's barriers about 0.5 us of each block that has work: it pays from a
+// few rounds of idle blocks on.
+int64_t append_pages(const AppendParams& p, bool& scan) {
+  const int64_t all = static_cast<int64_t>(append_segments(p)) * p.c.B;
+  const int64_t most = (p.n_tokens >> p.c.log2_page) + 2 * static_cast<int64_t>(p.c.B);
+  const int head_blocks = (p.c.H_kv + kThreads / 32 - 1) / (kThreads / 32);
+  scan = p.cu_new != nullptr && (all - most) * head_blocks > 4 * 608;
+  return (scan ? most : all) * head_blocks;
+}
+
 template <int D, bool E4M3>
 bool launch(const AppendParams& p, cudaStream_t stream) {
   const int total = p.cu_new ? p.n_tokens : p.c.B * p.max_new;
@@ -438,19 +500,21 @@ bool launch(const AppendParams& p, cudaStream_t stream) {
   int log2_tokens = 0;
   while (log2_tokens < 3 && total >> log2_tokens > 152 * 16) ++log2_tokens;
   const int blocks = total > 0 ? (total + (1 << log2_tokens) - 1) >> log2_tokens : 1;  // new_lens needs one
-  int segs = 0, pages = 0;
-  if (p.c.summary && p.max_new > 0) {
-    const int P = 1 << p.c.log2_page;
-    segs = (p.max_new + P - 2) / P + 1;  // the most pages a run of max_new tokens can touch
-    const int64_t n = static_cast<int64_t>((p.c.H_kv + kThreads / 32 - 1) / (kThreads / 32)) * segs * p.c.B;
-    if (n + blocks > 0x7FFFFFFF) return false;
-    pages = static_cast<int>(n);
-  }
-  return launch_after(p.interleaved ? append_kernel<D, E4M3, true> : append_kernel<D, E4M3, false>,
-                      dim3(pages + blocks), kThreads, kSlots * 2 * kThreads * 16, stream, p, log2_tokens, pages, segs);
+  bool scan = false;
+  const int segs = append_segments(p);
+  const int pages = p.c.summary && p.max_new > 0 ? static_cast<int>(append_pages(p, scan)) : 0;
+  auto* kernel = p.interleaved ? (scan ? append_kernel<D, E4M3, true, true> : append_kernel<D, E4M3, true, false>)
+                               : (scan ? append_kernel<D, E4M3, false, true> : append_kernel<D, E4M3, false, false>);
+  return launch_after(kernel, dim3(pages + blocks), kThreads, kSlots * 2 * kThreads * 16, stream, p, log2_tokens, pages,
+                      segs);
 }
 
 }  // namespace
+
+int64_t append_page_blocks(const AppendParams& p) {
+  bool scan;
+  return p.c.summary && p.max_new > 0 ? append_pages(p, scan) : 0;
+}
 
 int launch_kv_append(const AppendParams& p, cudaStream_t stream) {
   const bool ok = p.c.d == 128 ? (p.c.e4m3 ? launch<128, true>(p, stream) : launch<128, false>(p, stream))

@@ -41,6 +41,8 @@ struct AppendParams {
   const float* rope;
   int32_t* new_lens;
 };
+// Blocks that go by page (with summaries); the rest of the grid is below 2^30.
+int64_t append_page_blocks(const AppendParams& p);
 int launch_kv_append(const AppendParams& p, cudaStream_t stream);
 
 struct DecodeParams {

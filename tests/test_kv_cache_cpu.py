@@ -139,7 +139,9 @@ def test_append_refusals(B):
     for bad in BAD_NEW:
         assert call(_cache(B), _seqs(B), _new(B, **bad)) == B.CM_ERR_INVALID_ARG, bad
     assert call(_cache(B), _seqs(B), _new(B, H_q=1 << 20)) == B.CM_ERR_UNSUPPORTED
-    assert call(_cache(B, page_size=16), _seqs(B), _new(B, n_tokens=1 << 21, max_new=1 << 21)) == B.CM_ERR_UNSUPPORTED
+    assert call(_cache(B, page_size=16), _seqs(B), _new(B, n_tokens=1 << 30, max_new=1 << 30)) == B.CM_ERR_UNSUPPORTED
+    assert call(_cache(B, page_size=16, summary=A16, summary_scale=A16, H_kv=1024, k_page_stride=1 << 21, v_page_stride=1 << 21),
+                _seqs(B, B=32767), _new(B, n_tokens=32000, max_new=32000)) == B.CM_ERR_UNSUPPORTED
     for args in ((None, _seqs(B), _new(B)), (_cache(B), None, _new(B)), (_cache(B), _seqs(B), None)):
         assert call(*args) == B.CM_ERR_INVALID_ARG
 

@@ -824,3 +824,37 @@ def test_binding_refusals(B):
                  (cache.k, cache.v, lens.float(), lens.float()), (cache.k, cache.v, None, None, torch.zeros(1, device="cuda"))):
         with pytest.raises(ValueError):
             B.KVCache(*args)
+
+
+@pytest.mark.parametrize("summaries", [False, True])
+def test_append_of_a_mixed_batch(B, summaries):
+    """700 sequences, most with one new token, some with none, a few with long prompts, packed: the same cache as
+    one sequence a call."""
+    gen = torch.Generator().manual_seed(58)
+    n, H, P, d, cap = 700, 9, 16, 64, 24
+    held = torch.randint(0, 60, (n,), generator=gen)
+    new = (torch.rand(n, generator=gen) < 0.9).long()
+    for b, m in ((0, 250), (1, 0), (300, 97), (511, 16), (512, 300), (699, 33)):
+        new[b] = m
+    table = torch.randperm(n * cap, generator=gen).to(torch.int32).view(n, cap).cuda()
+    lens, cu = held.to(torch.int32).cuda(), torch.cat([torch.zeros(1, dtype=torch.long), new.cumsum(0)]).to(torch.int32).cuda()
+    total = int(new.sum())
+    k, v = (torch.randn(total, H, d, generator=gen).to(torch.bfloat16).cuda() for _ in range(2))
+    rope = _rope(cap * P, 32, gen).cuda()
+    first = torch.randn(n * cap, H, P, d, device="cuda").to(torch.bfloat16)
+    caches = []
+    for _ in range(2):
+        more = {"summary": torch.zeros(n * cap, H, 2, d, dtype=torch.int8, device="cuda"),
+                "summary_scale": torch.zeros(n * cap, H, device="cuda")} if summaries else {}
+        caches.append(B.KVCache(first.clone(), first.clone(), **more))
+    new_lens = torch.zeros_like(lens)
+    B.cm_kv_append(caches[0], table, lens, k, v, rope=rope, cu_new=cu, max_new=300, new_lens=new_lens)
+    assert torch.equal(new_lens.cpu().long(), held + new)
+    at = cu.tolist()
+    for b in range(n):
+        t = slice(at[b], at[b + 1])
+        if at[b] < at[b + 1]:
+            B.cm_kv_append(caches[1], table[b:b + 1], lens[b:b + 1], k[t].transpose(0, 1)[None], v[t].transpose(0, 1)[None], rope=rope)
+    assert B.cm_kv_status(caches[0]) == B.CM_OK and B.cm_kv_status(caches[1]) == B.CM_OK
+    for name in ("k", "v") + (("summary", "summary_scale") if summaries else ()):
+        assert torch.equal(getattr(caches[0], name), getattr(caches[1], name)), name
