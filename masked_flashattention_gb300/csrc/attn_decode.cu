@@ -22,6 +22,12 @@
 // most tiles.  P is rounded to the values' 16-bit type for the second product; sums, maxima and O are fp32.
 // An e4m3 cache is widened to fp16 (exactly) between shared memory and the product; queries become
 // fp16 scaled by a power of two per head so that none overflows.
+//
+// Measured (8 key-value heads of 128, 4 query heads each, bf16): 64 sequences of up to 16384 keys, 343 us =
+// 6.7 TB/s, the copy bandwidth; one of 131071, 86 us = 6.2 TB/s; 200 of up to 333, 19 us.  What stands
+// above the bytes is the start, 4 us from the launch to the first tile on its way (length, place, page number: one
+// load behind another) and up to 4 more until the memory's address translations are warm, and the end, 4 to 5
+// us where rows are split (join, launch, join).  One CTA a head took 52 ms for the one of 131071.
 #include <cuda_fp16.h>
 #include <atomic>
 

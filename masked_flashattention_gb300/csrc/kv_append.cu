@@ -12,6 +12,9 @@
 //   pages   With summaries, the keys go by page instead: one warp a (page, head) that the call
 //           touches stores the new keys and takes the largest and smallest over all that the page
 //           then holds, so a summary never depends on how its tokens arrived and needs no atomics.
+// Measured: 42,000 new tokens of 9 sequences, 32 query and 8 key-value heads of 128, with summaries, 183 us =
+// 5.75 TB/s, 85 % of the copy bandwidth (428 us with one unit a warp of 16 rows in registers, 265 with
+// the heads' loads in registers, which held a quarter of the warps); one token of 256 sequences, e4m3, 10 us.
 //
 // Numerics: the rotation is fp32 with every product and sum rounded once (no fused
 // multiply-add), so that it equals the formula evaluated step by step; one rounding to bf16, and
@@ -482,9 +485,10 @@ int append_segments(const AppendParams& p) {
 }
 // Pages that blocks are launched for, and whether they are dealt out by a scan.  Packed tokens: every page but a
 // sequence's first and last takes a page's worth of them, so a batch of a few long prompts among many
-// single tokens has far fewer than `segs` for each sequence.  A block that finds nothing to do takes about
-// 1 us of one of 608 places, the scan's barriers about 0.5 us of each block that has work: it pays from a
-// few rounds of idle blocks on.
+// single tokens has far fewer than `segs` for each sequence: 17.8 us instead of 53.6 for 255 single tokens
+// and 2048 of one sequence (pages of 16).  A block that finds nothing to do takes about 1 us of one of 608
+// places, the scan's barriers about 0.5 us of each block that has work: it pays from a few rounds of idle
+// blocks on.
 int64_t append_pages(const AppendParams& p, bool& scan) {
   const int64_t all = static_cast<int64_t>(append_segments(p)) * p.c.B;
   const int64_t most = (p.n_tokens >> p.c.log2_page) + 2 * static_cast<int64_t>(p.c.B);
