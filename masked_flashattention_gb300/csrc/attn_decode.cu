@@ -230,7 +230,7 @@ __device__ __forceinline__ int unit_tiles(const DecodeArgs& a, int u, bool repor
   // one interval after another comes to the front (small code: instructions fetched for the first time
   // cost more than these)
 #pragma unroll 1
-  for (int i = 0; i < kMaxIntervals; ++i) {
+  for (int i = 0; i < a.p.NI; ++i) {
     int from = lo[0];
 #pragma unroll
     for (int k = 1; k < kMaxIntervals; ++k)
@@ -1132,13 +1132,14 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NB>::kThreads, 1)
   const int run = max((total + a.ctas - 1) / a.ctas, a.min_run);  // of a CTA
   int cta0 = min(static_cast<int64_t>(run) * blockIdx.x, static_cast<int64_t>(total));
   int cta1 = min(static_cast<int64_t>(cta0) + run, static_cast<int64_t>(total));
-  if (a.whole_rows) {  // from the first row that starts in the run to the end of the last
+  if (a.whole_rows) {  // ends go to the nearest end of a row
     int* bounds = warp_sum;  // the sums have been read
     if (warp < 2) {
       int at = warp ? cta1 : cta0;
       if (at < total) {
         const Place x = locate(at);
-        if (x.c) at += row_cost(x.tiles) - x.c;
+        const int cost = row_cost(x.tiles);
+        at += 2 * x.c > cost ? cost - x.c : -x.c;
       }
       if (lane == 0) bounds[warp] = at;
     }
