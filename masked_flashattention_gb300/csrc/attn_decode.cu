@@ -73,6 +73,10 @@ struct Cfg {
   static constexpr int kPiece = kHeads * kHeadPitch * 4 + 2 * kHeads * 4;  // O, m, l
   static constexpr int kFit = (static_cast<int>(kSmemMax) - 1024 - kPairs * kPiece) / (kPairs * kStage);
   static constexpr int kStages = kFit < 8 ? kFit : 8;
+  // Stages in flight where rows are long: 128 KB an SM.  With all that fits, some SMs get their data a third
+  // faster than others (one sequence of 131071: blocks were done after 60 to 87 us), and the slowest decide.
+  // Short rows are better off with every stage: the next rows' tiles are on their way during the ends of these.
+  static constexpr int kSteady = (128 << 10) / (kPairs * kStage) < kStages ? (128 << 10) / (kPairs * kStage) : kStages;
   static constexpr int kRing = kPairs * kStages * kStage;
   static constexpr int kOffPiece = kRing;
   static constexpr int kOffMeta = kOffPiece + kPairs * kPiece;
@@ -451,6 +455,7 @@ __device__ __forceinline__ int fetch(const DecodeArgs& a, const CUtensorMap* kma
   using C = Cfg<D, E4M3, NB>;
   const DecodeParams& p = a.p;
   const int log2_page = p.c.log2_page, P = 1 << log2_page;
+  const int depth = a.whole_rows ? C::kStages : C::kSteady;
   int issued = 0;
   const int begin = w.pos, end = w.end;
   Chunk next;
@@ -468,8 +473,9 @@ __device__ __forceinline__ int fetch(const DecodeArgs& a, const CUtensorMap* kma
     next_chunk<D>(a, w, next, lane);  // its loads are on their way while cur is fetched
     for (int j = 0; j < cur.n; ++j) {
       const int stage = issued % C::kStages;
-      const uint32_t full = bars + stage * 16, empty = full + 8;
-      if (issued >= C::kStages && !warp_wait(wait, empty, ((issued / C::kStages) & 1) ^ 1, 1)) {
+      const uint32_t full = bars + stage * 16;
+      const int before = issued - depth;  // that tile has to be done with
+      if (before >= 0 && !warp_wait(wait, bars + before % C::kStages * 16 + 8, (before / C::kStages) & 1, 1)) {
         ok = false;
         break;
       }
