@@ -23,11 +23,11 @@
 // An e4m3 cache is widened to fp16 (exactly) between shared memory and the product; queries become
 // fp16 scaled by a power of two per head so that none overflows.
 //
-// Measured (8 key-value heads of 128, 4 query heads each, bf16): 64 sequences of up to 16384 keys, 343 us =
-// 6.7 TB/s, the copy bandwidth; one of 131071, 86 us = 6.2 TB/s; 200 of up to 333, 19 us.  What stands
-// above the bytes is the start, 4 us from the launch to the first tile on its way (length, place, page number: one
-// load behind another) and up to 4 more until the memory's address translations are warm, and the end, 4 to 5
-// us where rows are split (join, launch, join).  One CTA a head took 52 ms for the one of 131071.
+// Measured (8 key-value heads of 128, 4 query heads each, bf16): 64 sequences of up to 16384 keys, 331 us =
+// 7.0 TB/s, 103 % of the copy bandwidth; one of 131071, 84 us = 6.4 TB/s; 200 of up to 333, 17.3 us.  What
+// stands above the bytes is the start, 4 us from the launch to the first tile on its way (length, place, page
+// number: one load behind another) and up to 4 more until the memory's address translations are warm, and the end,
+// 4 to 5 us where rows are split (join, launch, join).  One CTA a head took 52 ms for the one of 131071.
 #include <cuda_fp16.h>
 #include <atomic>
 
@@ -52,10 +52,9 @@ constexpr int kStarts = 4;  // the part begins where the row begins
 constexpr int kEnds = 8;    // the part ends where the row ends
 constexpr int kFlagBits = 4;  // above them: the CTAs that hold parts of the row
 
-// Shared memory: 32 keys of 128 bf16 channels, K and V, are 16 KB, and 4 pairs with 3 such stages keep
-// 100 KB or more of an SM's reads in flight, twice what the memory's latency asks for.  The smaller rows take
-// more instructions a byte, so 8 pairs share the ring's memory (one computing warp a scheduler
-// left an e4m3 cache at 47 % of the bandwidth).  Their 16 warps start with 128 registers a thread and
+// Shared memory: 32 keys of 128 bf16 channels, K and V, are 16 KB, and 4 pairs with 3 such stages are what fits.
+// The smaller rows take more instructions a byte, so 8 pairs share the ring's memory (one computing warp
+// a scheduler left an e4m3 cache at 47 % of the bandwidth).  Their 16 warps start with 128 registers a thread and
 // trade: 184 for a computing warp, 72 for a fetching one.
 template <int D, bool E4M3, int NB>
 struct Cfg {

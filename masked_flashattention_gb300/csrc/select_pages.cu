@@ -20,7 +20,7 @@
 // pages in that range are ranked against each other (a bisection over the score's bits where they are
 // many, as with equal scores), and scans over the block write the pages in order.
 //
-// Measured (d = 128, 8 key-value heads, groups of 4): one sequence of 2048 pages, 8.2 us; 32 of up to 1024, 18 us, of
+// Measured (d = 128, 8 key-value heads, groups of 4): one sequence of 2048 pages, 8.1 us; 32 of up to 1024, 18 us, of
 // which the scores are half (34 MB: 5 us at the copy bandwidth; rows of unequal length, one a block), the
 // choice 4.  As two kernels, scores by a warp a head with 16 to 64 pages, then the choice, they took
 // 8.7 and 19.7: rounding the queries for so few pages took more instructions than the products.
