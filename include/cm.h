@@ -255,7 +255,8 @@ CM_API int cm_attn_bwd_dq(const cm_descriptor* desc, const void* q, const void* 
  * the descriptor stay usable.  This is a diagnostic hook: a very small limit makes ordinary waits
  * expire, which tests the time-out path without a fault.  Not synchronised with launches in
  * flight on other host threads.  (The pages describe no failure handling; this is the library's
- * own.) */
+ * own.)  cm_attn_decode's waits are bounded by it too; it records CM_ERR_TIMEOUT in the cache's status
+ * word (cm_kv_status). */
 CM_API int cm_set_wait_limit_ns(unsigned long long ns);
 
 /* ---- backward without a workspace (no counterpart in the paper) ---------------------------- */

@@ -17,7 +17,9 @@
 // tensor-core shape is turned around so that few query heads waste little of it:
 //   S^T [32 keys x 8 heads] = K Q^T          A = K rows as they lie in shared memory (ldmatrix)
 //   O^T [d x 8 heads]      += V^T P^T        A = V transposed on the way (ldmatrix.trans)
-// with a running maximum and sum per head (one pass).  The maximum is only renewed when a score
+// (tcgen05 is the wrong tool for this one: its products start at 64 rows and take B from shared memory alone, so P would
+// go there and back for a pipe that is busy 13 % of the time.)
+// There is a running maximum and sum per head (one pass).  The maximum is only renewed when a score
 // passes it by 2^8 (all in log2 units), which bounds p by 256 and spares the cross-lane maximum on
 // most tiles.  P is rounded to the values' 16-bit type for the second product; sums, maxima and O are fp32.
 // An e4m3 cache is widened to fp16 (exactly) between shared memory and the product; queries become

@@ -458,6 +458,7 @@ SELECT = [
     (64, 64, "bf16", 4, 8, [640, 641], 10, 0, 10),
     (128, 128, "e4m3", 1, 3, [900, 128, 129], 1, 0, 1),
     (64, 16, "bf16", 1, 5, [9000], 300, 2, 3),
+    (128, 16, "e4m3", 1, 19, [9001, 7000], 100, 0, 1),  # several blocks a row, several rounds of heads
 ]
 
 
