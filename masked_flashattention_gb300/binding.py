@@ -63,7 +63,6 @@ class cm_kv_seqs(ctypes.Structure):
                 ("page_table", ctypes.c_void_p), ("lens", ctypes.c_void_p)]
 
 
-_Strides2 = ctypes.c_int64 * 2
 _Strides3 = ctypes.c_int64 * 3
 
 
@@ -511,7 +510,7 @@ class KVCache:
         self.c = cm_kv_cache(n, P, H, d, CM_KV_E4M3 if e4m3 else CM_KV_BF16, k_stride, v_stride,
                              k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale),
                              _ptr(summary), _ptr(summary_scale), self.status.data_ptr())
-        self._ref = ctypes.byref(self.c)
+        self._address = ctypes.addressof(self.c)
 
     @classmethod
     def alloc(cls, num_pages: int, H_kv: int, page_size: int, d: int, dtype=torch.bfloat16,
@@ -536,25 +535,53 @@ def _kv_tensor(t, name, dtype, shape, device: int):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on cuda:{device}")
 
 
-# These calls are a few microseconds of GPU work each, so their checks are written to be quick: one
-# device number instead of device objects, strides read once, one constructor for a whole struct.
+# These calls are a few microseconds of GPU work each, so they are written to be quick: one device number
+# instead of device objects, shapes and strides read once, structs packed in one go, and function
+# objects of their own that take them as bytes.
+_I32 = torch.int32
+_SEQS = struct.Struct("2i2P")      # cm_kv_seqs, field by field
+_NEW = struct.Struct("5P15q2P6i2P")  # cm_kv_new
+_TWO = struct.Struct("2q")
+assert _SEQS.size == ctypes.sizeof(cm_kv_seqs) and _NEW.size == ctypes.sizeof(cm_kv_new)
+_calls = None
+
+
+def _serving():
+    """(cm_kv_append, cm_attn_decode, cm_select_pages) with every pointer as an address or bytes."""
+    global _calls
+    if _calls is None:
+        L, vp, i32, sz = lib(), ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+
+        def call(name, *args):
+            return ctypes.CFUNCTYPE(i32, *args)((name, L))
+
+        _calls = (call("cm_kv_append", vp, vp, vp, vp),
+                  call("cm_attn_decode", vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, i32,
+                       ctypes.c_float, vp, sz, vp),
+                  call("cm_select_pages", vp, vp, vp, vp, i32, i32, i32, vp, vp, i32, vp, sz, vp))
+    return _calls
+
+
 def _kv_stream(cache: KVCache, stream) -> int:
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(cache.index)
     return _stream(stream)
 
 
-def _kv_seqs(cache: KVCache, page_table, lens) -> cm_kv_seqs:
-    dev = cache.index
+def _kv_seqs(cache: KVCache, page_table, lens):
+    """B and the packed cm_kv_seqs."""
+    dev, shape = cache.index, page_table.shape
     if dev != torch._C._cuda_getDevice():
         raise ValueError(f"the cache is on {cache.device}, which is not the current device")
-    if not (page_table.dim() == 2 and page_table.dtype is torch.int32
-            and page_table.get_device() == dev and page_table.is_contiguous()):
+    if not (len(shape) == 2 and page_table.dtype is _I32 and page_table.get_device() == dev
+            and page_table.is_contiguous()):
         raise ValueError("page_table must be a contiguous int32 tensor [B, max_pages] on "
                          f"{cache.device}")
-    B, n = page_table.shape
-    _kv_tensor(lens, "lens", torch.int32, (B,), dev)
-    return cm_kv_seqs(B, n, page_table.data_ptr(), lens.data_ptr())
+    B, n = shape
+    if not (lens.dtype is _I32 and lens.shape == (B,) and lens.get_device() == dev
+            and lens.is_contiguous()):
+        raise ValueError(f"lens must be a contiguous int32 tensor [{B}] on {cache.device}")
+    return B, _SEQS.pack(B, n, page_table.data_ptr(), lens.data_ptr())
 
 
 def _tokens(t, name, cache: KVCache, packed: bool):
@@ -572,8 +599,6 @@ def _tokens(t, name, cache: KVCache, packed: bool):
 
 
 _NONE3 = (0, 0, 0)
-_NEW = struct.Struct("5P15q2P6i2P")  # cm_kv_new, field by field
-assert _NEW.size == ctypes.sizeof(cm_kv_new)
 
 
 def _addr(t):
@@ -590,8 +615,8 @@ def cm_kv_append(cache: KVCache, page_table, lens, k, v, q=None, q_out=None, k_o
     max_new: the most tokens of any sequence (default: as many as the tensors hold).  rope: fp32
     [positions, rot_dim / 2, 2] of cosines and sines.  new_lens (int32 [B]) receives the new
     lengths."""
-    seqs = _kv_seqs(cache, page_table, lens)
-    B, dev, packed = seqs.B, cache.index, cu_new is not None
+    B, seqs = _kv_seqs(cache, page_table, lens)
+    dev, packed = cache.index, cu_new is not None
     shape, ks = _tokens(k, "k", cache, packed)
     v_shape, vs = _tokens(v, "v", cache, packed)
     if shape[1] != cache.H_kv or v_shape != shape or not (packed or shape[0] == B):
@@ -625,13 +650,13 @@ def cm_kv_append(cache: KVCache, page_table, lens, k, v, q=None, q_out=None, k_o
         rot_dim = 2 * half
     if new_lens is not None:
         _kv_tensor(new_lens, "new_lens", torch.int32, (B,), dev)
-    tok = cm_kv_new.from_buffer_copy(_NEW.pack(
+    tok = _NEW.pack(
         k.data_ptr(), v.data_ptr(), _addr(q), _addr(q_out), _addr(k_out), *ks, *vs, *qs, *qos, *kos,
         _addr(cu_new), _addr(n_new), n, n if max_new is None else max_new, H_q, rot_dim,
-        interleaved, rope_len, _addr(rope), _addr(new_lens)))
-    rc = lib().cm_kv_append(cache._ref, ctypes.byref(seqs), ctypes.byref(tok),
-                            _kv_stream(cache, stream))
-    _check(rc, "cm_kv_append")
+        interleaved, rope_len, _addr(rope), _addr(new_lens))
+    rc = _serving()[0](cache._address, seqs, tok, _kv_stream(cache, stream))
+    if rc != CM_OK:
+        raise CMError(rc, "cm_kv_append")
 
 
 def cm_attn_decode_workspace_size(B: int, H_q: int, H_kv: int, d: int) -> int:
@@ -647,7 +672,7 @@ def _one_token(t, name, cache: KVCache, B: int):
             and shape[0] == B and shape[2] == cache.d and s[2] == 1):
         raise ValueError(f"{name} must be a bf16 tensor [B, H_q, d] on {cache.device} with d = "
                          f"{cache.d} contiguous")
-    return _Strides2(s[0] if B > 1 else 0, s[1] if shape[1] > 1 else 0)
+    return _TWO.pack(s[0] if B > 1 else 0, s[1] if shape[1] > 1 else 0)
 
 
 def _workspace(w, cache: KVCache):
@@ -661,8 +686,8 @@ def cm_attn_decode(cache: KVCache, page_table, lens, q, o, lse, workspace: torch
     """Attention of the last of each sequence's lens[b] tokens over the cache: q, o bf16
     [B, H_q, d]; lse fp32 [B, H_q] or None.  desc: the mask, whose row lens[b] - 1 the token sees by;
     or sel (int32 [B, H_kv, n]) with nsel (int32 [B, H_kv]): the pages to attend to."""
-    seqs = _kv_seqs(cache, page_table, lens)
-    B, dev, H = seqs.B, cache.index, q.shape[1]
+    B, seqs = _kv_seqs(cache, page_table, lens)
+    dev, H = cache.index, q.shape[1]
     qs, os = _one_token(q, "q", cache, B), _one_token(o, "o", cache, B)
     if o.shape[1] != H:
         raise ValueError("o shape mismatch")
@@ -678,12 +703,12 @@ def cm_attn_decode(cache: KVCache, page_table, lens, q, o, lse, workspace: torch
     _workspace(workspace, cache)
     if desc is not None and desc.itab_f.get_device() != dev:
         raise ValueError(f"desc must be on {cache.device}")
-    rc = lib().cm_attn_decode(cache._ref, ctypes.byref(seqs),
-                              None if desc is None else ctypes.byref(desc.c), _ptr(sel),
-                              _ptr(nsel), sel_max, q.data_ptr(), qs, o.data_ptr(), os, _ptr(lse),
-                              H, cache.scale if scale is None else scale, workspace.data_ptr(),
-                              workspace.nbytes, _kv_stream(cache, stream))
-    _check(rc, "cm_attn_decode")
+    rc = _serving()[1](cache._address, seqs, None if desc is None else ctypes.addressof(desc.c),
+                       _ptr(sel), _ptr(nsel), sel_max, q.data_ptr(), qs, o.data_ptr(), os,
+                       _ptr(lse), H, cache.scale if scale is None else scale,
+                       workspace.data_ptr(), workspace.nbytes, _kv_stream(cache, stream))
+    if rc != CM_OK:
+        raise CMError(rc, "cm_attn_decode")
 
 
 def cm_select_pages_workspace_size(B: int, H_kv: int, max_pages: int) -> int:
@@ -699,8 +724,7 @@ def cm_select_pages(cache: KVCache, page_table, lens, q, sel, nsel, workspace: t
     scores for the new token's queries q (bf16 [B, H_q, d]), the first keep_first and last keep_last
     pages always among them: sel int32 [B, H_kv, n] in ascending order, -1 behind the last, and
     their number nsel int32 [B, H_kv]."""
-    seqs = _kv_seqs(cache, page_table, lens)
-    B = seqs.B
+    B, seqs = _kv_seqs(cache, page_table, lens)
     if cache.summary is None:
         raise ValueError("the cache has no page summaries")
     if not (sel.dim() == 3 and sel.shape[2] > 0):
@@ -709,16 +733,16 @@ def cm_select_pages(cache: KVCache, page_table, lens, q, sel, nsel, workspace: t
     _kv_tensor(nsel, "nsel", torch.int32, (B, cache.H_kv), cache.index)
     _workspace(workspace, cache)
     qs = _one_token(q, "q", cache, B)
-    _check(lib().cm_select_pages(cache._ref, ctypes.byref(seqs), q.data_ptr(), qs, q.shape[1],
-                                 keep_first, keep_last, sel.data_ptr(), nsel.data_ptr(),
-                                 sel.shape[2], workspace.data_ptr(), workspace.nbytes,
-                                 _kv_stream(cache, stream)),
-           "cm_select_pages")
+    rc = _serving()[2](cache._address, seqs, q.data_ptr(), qs, q.shape[1], keep_first, keep_last,
+                       sel.data_ptr(), nsel.data_ptr(), sel.shape[2], workspace.data_ptr(),
+                       workspace.nbytes, _kv_stream(cache, stream))
+    if rc != CM_OK:
+        raise CMError(rc, "cm_select_pages")
 
 
 def cm_kv_status(cache: KVCache, stream=None) -> int:
     """The first device error since the last call (CM_OK where there was none); zeroes it."""
-    return lib().cm_kv_status(cache._ref, _stream(stream))
+    return lib().cm_kv_status(ctypes.byref(cache.c), _stream(stream))
 
 
 def _used_on(stream, *tensors):
