@@ -21,7 +21,7 @@
 // go there and back for a pipe that is busy 13 % of the time.)
 // There is a running maximum and sum per head (one pass).  The maximum is only renewed when a score
 // passes it by 2^8 (all in log2 units), which bounds p by 256 and spares the cross-lane maximum on
-// most tiles.  P is rounded to the values' 16-bit type for the second product; sums, maxima and O are fp32.
+// most tiles; beside an e4m3 cache p is fp16 and taken 2^7 larger (kLift).  P is rounded to the values' 16-bit type for the second product; sums, maxima and O are fp32.
 // An e4m3 cache is widened to fp16 (exactly) between shared memory and the product; queries become
 // fp16 scaled by a power of two per head so that none overflows.
 //
@@ -45,6 +45,11 @@ constexpr int kMaxCtas = 320;
 constexpr int kMaxIntervals = 8;
 constexpr int kRowCost = 2;
 constexpr float kRenew = 8.f;       // log2 units a score may pass the running maximum by
+// Log2 units that the reference of fp16 weights lies below that maximum, so that weights reach up to
+// 2^(8 + 7) and what fp16 cannot hold is below 2^-32 of the largest: without them a million keys of 2^-25
+// each beside one large one lost 3 % of the sum.  bf16 weights have fp32's range.
+template <bool E4M3>
+constexpr float kLift = E4M3 ? 7.f : 0.f;
 constexpr size_t kSmemMax = 232448;
 
 // flags of a tile
@@ -701,7 +706,7 @@ __device__ __forceinline__ void compute_tile(State<D, E4M3, NB>& t, uint32_t k_a
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int x = 0; x < 4; ++x) pass |= s[i][n][x] > t.m[n][x & 1] + kRenew;
+      for (int x = 0; x < 4; ++x) pass |= s[i][n][x] > t.m[n][x & 1] + (kRenew + kLift<E4M3>);
   if (__any_sync(0xFFFFFFFFu, pass)) {
 #pragma unroll
     for (int n = 0; n < NB; ++n)
@@ -710,7 +715,7 @@ __device__ __forceinline__ void compute_tile(State<D, E4M3, NB>& t, uint32_t k_a
         float top = fmaxf(fmaxf(s[0][n][x], s[0][n][x + 2]), fmaxf(s[1][n][x], s[1][n][x + 2]));
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-        top = fmaxf(top, t.m[n][x]);
+        top = fmaxf(top - kLift<E4M3>, t.m[n][x]);
         const float fade = top == -INFINITY ? 1.f : ex2_approx(t.m[n][x] - top);
         t.m[n][x] = top;
         t.l[n][x] *= fade;

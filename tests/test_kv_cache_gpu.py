@@ -363,6 +363,36 @@ MASKS = {
 }
 
 
+@pytest.mark.parametrize("group", [1, 12])
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_many_small_weights_beside_a_large_one(B, kv, group):
+    """One key whose value is 0 and n - 1 of 2^-25.2 its weight whose values are 1: the small weights are
+    all of the output, and 2^-25.2 is less than half of fp16's smallest number.  Bounds: a weight is off by half of that
+    number (2^-25) times 2^-7 of the largest at most, o by n of those, the weights' 2^-14 and one rounding to bf16;
+    the log by its own (2^-20) and the sum's: additions of up to n / (4 warps x 8 lanes) terms."""
+    n, P, d = 1 << 19, 128, 64
+    k, v = (torch.zeros(n // P, 1, P, d, device="cuda").to(torch.bfloat16) for _ in range(2))
+    v += 1
+    k[0, 0, 5, 0] = 1
+    v[0, 0, 5] = 0
+    one = torch.ones(1, device="cuda")
+    scales = {}
+    if kv == "e4m3":
+        k, v = k.to(torch.float8_e4m3fn), v.to(torch.float8_e4m3fn)
+        scales = {"k_scale": one, "v_scale": one}
+    cache = B.KVCache(k, v, **scales)
+    table = torch.arange(n // P, dtype=torch.int32, device="cuda")[None]
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    q = torch.zeros(1, group, d, device="cuda", dtype=torch.bfloat16)
+    q[..., 0] = 1
+    o, lse = B.decode_attention(cache, table, lens, q, scale=25.2 * math.log(2))
+    assert B.cm_kv_status(cache) == B.CM_OK
+    rest = (n - 1) * 2.0 ** -25.2
+    want, wl = rest / (1 + rest), 25.2 * math.log(2) + math.log1p(rest)
+    assert ((o.double() - want).abs() <= (BF16_HALF + 2.0 ** -14) * want + n * 2.0 ** -32).all(), (o, want)
+    assert ((lse.double() - wl).abs() <= 2.0 ** -20 * (1 + wl) + n / 32 * 2 * F32_HALF * rest).all(), (lse, wl)
+
+
 @pytest.mark.parametrize("name", MASKS)
 @pytest.mark.parametrize("d,P,kv,H,group", [(128, 64, "bf16", 2, 4), (64, 16, "e4m3", 1, 9)])
 def test_decode_masked(B, name, d, P, kv, H, group):
