@@ -745,26 +745,37 @@ def cm_kv_status(cache: KVCache, stream=None) -> int:
     return lib().cm_kv_status(ctypes.byref(cache.c), _stream(stream))
 
 
-def _used_on(stream, *tensors):
-    """Tells the allocator of tensors made on the current stream that `stream` uses them."""
-    if stream is not None:
-        if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream))
-        for t in tensors:
-            t.record_stream(stream)
+def _for_stream(stream, make):
+    """make()'s tensors for work on `stream`: new ones from its memory, where nothing that the current
+    stream still does can write, and all kept from reuse until both streams have done with them."""
+    if stream is None:
+        return make()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    here = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        made = make()
+    for t in made:
+        t.record_stream(here)
+        t.record_stream(stream)
+    return made
 
 
 def decode_attention(cache: KVCache, page_table, lens, q, desc=None, sel=None, nsel=None,
                      scale=None, stream=None, workspace=None):
     """cm_attn_decode into new tensors: (o, lse)."""
     B, H, d = q.shape
-    o = torch.empty(B, H, d, dtype=q.dtype, device=q.device)
-    lse = torch.empty(B, H, dtype=torch.float32, device=q.device)
-    if workspace is None:
-        workspace = torch.empty(cm_attn_decode_workspace_size(B, H, cache.H_kv, d),
-                                dtype=torch.uint8, device=q.device)
+
+    def make():
+        w = workspace
+        if w is None:
+            w = torch.empty(cm_attn_decode_workspace_size(B, H, cache.H_kv, d), dtype=torch.uint8,
+                            device=q.device)
+        return (torch.empty(B, H, d, dtype=q.dtype, device=q.device),
+                torch.empty(B, H, dtype=torch.float32, device=q.device), w)
+
+    o, lse, workspace = _for_stream(stream, make)
     cm_attn_decode(cache, page_table, lens, q, o, lse, workspace, desc, sel, nsel, scale, stream)
-    _used_on(stream, o, lse, workspace)
     return o, lse
 
 
@@ -772,12 +783,15 @@ def select_pages(cache: KVCache, page_table, lens, q, n: int, keep_first: int = 
                  keep_last: int = 0, stream=None, workspace=None):
     """cm_select_pages of n pages into new tensors: (sel, nsel)."""
     B = q.shape[0]
-    sel = torch.empty(B, cache.H_kv, n, dtype=torch.int32, device=q.device)
-    nsel = torch.empty(B, cache.H_kv, dtype=torch.int32, device=q.device)
-    if workspace is None:
-        workspace = torch.empty(
-            cm_select_pages_workspace_size(B, cache.H_kv, page_table.shape[1]), dtype=torch.uint8,
-            device=q.device)
+
+    def make():
+        w = workspace
+        if w is None:
+            w = torch.empty(cm_select_pages_workspace_size(B, cache.H_kv, page_table.shape[1]),
+                            dtype=torch.uint8, device=q.device)
+        return (torch.empty(B, cache.H_kv, n, dtype=torch.int32, device=q.device),
+                torch.empty(B, cache.H_kv, dtype=torch.int32, device=q.device), w)
+
+    sel, nsel, workspace = _for_stream(stream, make)
     cm_select_pages(cache, page_table, lens, q, sel, nsel, workspace, keep_first, keep_last, stream)
-    _used_on(stream, sel, nsel, workspace)
     return sel, nsel

@@ -656,6 +656,37 @@ def test_two_streams_with_workspaces_of_their_own(B):
             assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
 
 
+def test_results_for_another_stream_keep_their_memory(B):
+    """Memory that the current stream has given back but still writes to does not serve a call on another
+    stream; nor does a later call there get memory whose contents the current stream still reads."""
+    gen = torch.Generator().manual_seed(44)
+    lens = [3000, 10, 700]
+    cache, table, n = _filled(B, lens, 2, 64, 128, "bf16", gen)
+    q = [torch.randn(3, 8, 128, generator=gen).to(torch.bfloat16).cuda() for _ in range(2)]
+    want = [B.decode_attention(cache, table, n, x) for x in q]
+    sizes = [B.cm_attn_decode_workspace_size(3, 8, 2, 128), 3 * 8 * 128 * 2, 3 * 8 * 4]
+    torch.cuda.synchronize()
+    here, side = torch.cuda.current_stream(), torch.cuda.Stream()
+    held = [torch.empty(b, dtype=torch.uint8, device="cuda") for b in sizes]
+    torch.cuda._sleep(50_000_000)
+    for t in held:
+        t.fill_(255)
+    del held, t
+    o, lse = B.decode_attention(cache, table, n, q[0], stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(o, want[0][0]) and torch.equal(lse, want[0][1])
+    o, lse = B.decode_attention(cache, table, n, q[0], stream=side)
+    here.wait_stream(side)
+    torch.cuda._sleep(50_000_000)
+    kept = o.clone(), lse.clone()
+    del o, lse
+    for _ in range(4):
+        B.decode_attention(cache, table, n, q[1], stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(kept[0], want[0][0]) and torch.equal(kept[1], want[0][1])
+    assert B.cm_kv_status(cache) == B.CM_OK
+
+
 def test_many_sequences_sharing_pages(B):
     """More sequences than a block has threads, most of them short or empty, with a common prefix in
     shared pages; the same through selected pages, one row of pages a sequence and head."""
