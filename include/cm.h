@@ -298,7 +298,10 @@ CM_API int cm_attn_bwd_noalloc(const cm_descriptor* desc, const void* q, const v
  *     CM_ERR_DEVICE_CHECK in the cache's status word and skips what they name, as each entry
  *     point says.
  *   - Keys past a sequence's length, and keys that a mask hides, are never used: whatever their
- *     memory holds (NaN and infinities too) does not reach an output. */
+ *     memory holds (NaN and infinities too) does not reach an output.
+ *   - An infinite value of a key that is used makes its channel of o infinite (NaN beside the other
+ *     infinity), and a NaN makes it NaN; the other channels do not change.  Weights are held in fp32: one
+ *     below 2^-110 of a row's largest may count as 0, and 0 times an infinity is NaN. */
 
 #define CM_KV_BF16 0
 #define CM_KV_E4M3 1

@@ -634,6 +634,11 @@ struct State {
   float o[NB][D / 16][4];
 };
 
+// What is left of a weight p beside its first 8 bits: never negative, and of a weight that is not 0 never 0, as
+// an infinite value would make NaN of either (inf - inf, 0 * inf) where p * inf is infinite.  The floor, fp32's
+// smallest normal number, is far below p's own last bit unless p is as small.
+__device__ __forceinline__ float left_over(float p, float cut) { return fmaxf(p - cut, fminf(p, 1.17549435e-38f)); }
+
 template <int D, bool E4M3, int NB>
 __device__ __forceinline__ void compute_tile(State<D, E4M3, NB>& t, uint32_t k_at, uint32_t v_at,
                                              uint32_t seen, int lane) {
@@ -727,8 +732,8 @@ __device__ __forceinline__ void compute_tile(State<D, E4M3, NB>& t, uint32_t k_a
       }
   }
   // P^T as the B operand [16 keys x 8 heads].  fp16 P (beside an e4m3 cache) keeps 11 bits; bf16 P would
-  // keep 8 and be off by as much as the rounded output, so its remainder goes through a second product
-  // with the same values.
+  // keep 8 and be off by as much as the rounded output, so it is cut there and its remainder goes through a
+  // second product with the same values.
   uint32_t pb[2][NB][2], rest[2][NB][2];
 #pragma unroll
   for (int n = 0; n < NB; ++n) {
@@ -748,9 +753,9 @@ __device__ __forceinline__ void compute_tile(State<D, E4M3, NB>& t, uint32_t k_a
           const __half2 f = __floats2half2_rn(e[2 * x], e[2 * x + 1]);
           w = *reinterpret_cast<const uint32_t*>(&f);
         } else {
-          w = pack_bf16x2(e[2 * x], e[2 * x + 1]);
-          rest[i][n][x] = movm_trans(pack_bf16x2(e[2 * x] - __uint_as_float(w << 16),
-                                                 e[2 * x + 1] - __uint_as_float(w & 0xFFFF0000u)));
+          w = __byte_perm(__float_as_uint(e[2 * x]), __float_as_uint(e[2 * x + 1]), 0x7632);  // upper halves
+          rest[i][n][x] = movm_trans(pack_bf16x2(left_over(e[2 * x], __uint_as_float(w << 16)),
+                                                 left_over(e[2 * x + 1], __uint_as_float(w & 0xFFFF0000u))));
         }
         pb[i][n][x] = movm_trans(w);
       }

@@ -1,0 +1,51 @@
+"""Paged key-value cache on the GPU: values, calls and interleavings at the edge of what is allowed,
+against the plain 64-bit forms (oracle/kv_cache.py)."""
+import math
+
+import pytest
+import torch
+
+from oracle import kv_cache as K
+from tests.test_kv_cache_gpu import BF16_HALF, B, F64, _check_decode, _filled, _host  # noqa: F401 (B is a fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+# ---- values ----------------------------------------------------------------------------------
+@pytest.mark.parametrize("d,P,H,group,lens", [(64, 16, 2, 3, [1, 2, 33, 700]), (128, 64, 1, 12, [1, 64, 9000]),
+                                              (128, 128, 1, 8, [40000])])
+def test_infinite_values(B, d, P, H, group, lens):
+    """A visible infinite value makes its channel infinite (both signs: NaN) and no other; scores are close
+    enough that no weight is below fp32's smallest."""
+    gen = torch.Generator().manual_seed(61)
+    cache, table, n = _filled(B, lens, H, P, d, "bf16", gen)
+    where = table.cpu()
+    for b, m in enumerate(lens):
+        def put(pos, channel, value):
+            cache.v[int(where[b, pos // P]), :, pos % P, channel] = value
+        put(0, 0, math.inf)
+        put(m - 1, 1, -math.inf)
+        put(m // 2, 2, math.inf)
+        put(0, 3, math.inf)
+        put(m - 1, 3, -math.inf)  # of one token, the same value
+        for pos in range(0, m, 7):
+            put(pos, d - 1, -math.inf)
+    q = torch.randn(len(lens), H * group, d, generator=gen).to(torch.bfloat16).cuda()
+    scale = 1 / math.sqrt(d)
+    o, lse = B.decode_attention(cache, table, n, q)
+    assert B.cm_kv_status(cache) == B.CM_OK
+    k, v, _, _ = _host(cache)
+    o, q = o.double().cpu(), q.cpu()
+    for b, m in enumerate(lens):
+        for g in range(H):
+            hs, pos = slice(g * group, (g + 1) * group), torch.arange(m)
+            kk, vv = K.rows(k, None, where[b], g, pos), K.rows(v, None, where[b], g, pos)
+            up, down = (vv == math.inf).any(0), (vv == -math.inf).any(0)
+            want, wl, size, mag = K.decode(q[b, hs], kk, torch.where(vv.isinf(), 0.0, vv), scale)
+            got, finite = o[b, hs], ~(up | down)
+            assert (got[:, up & ~down] == math.inf).all() and (got[:, down & ~up] == -math.inf).all(), (b, g)
+            assert got[:, up & down].isnan().all(), (b, g)
+            ds = (d + 8) * 2 * 2.0 ** -24 * size + 2.0 ** -20
+            bound = BF16_HALF * want.abs() + (BF16_HALF + 2 * ds + 2.0 ** -14) * mag
+            assert ((got - want).abs() <= bound)[:, finite].all(), (b, g)
+            assert ((lse[b, hs].double().cpu() - wl).abs() <= ds + 2.0 ** -20 * (1 + wl.abs())).all(), (b, g)
