@@ -301,7 +301,9 @@ CM_API int cm_attn_bwd_noalloc(const cm_descriptor* desc, const void* q, const v
  *     memory holds (NaN and infinities too) does not reach an output.
  *   - An infinite value of a key that is used makes its channel of o infinite (NaN beside the other
  *     infinity), and a NaN makes it NaN; the other channels do not change.  Weights are held in fp32: one
- *     below 2^-110 of a row's largest may count as 0, and 0 times an infinity is NaN. */
+ *     below 2^-110 of a row's largest may count as 0, and 0 times an infinity is NaN.  Weights of at
+ *     most 1 times values are summed before the division: beside a bf16 cache, where a row's keys times
+ *     the largest |v| pass 2^127, an output may overflow. */
 
 #define CM_KV_BF16 0
 #define CM_KV_E4M3 1

@@ -19,9 +19,10 @@
 //   O^T [d x 8 heads]      += V^T P^T        A = V transposed on the way (ldmatrix.trans)
 // (tcgen05 is the wrong tool for this one: its products start at 64 rows and take B from shared memory alone, so P would
 // go there and back for a pipe that is busy 13 % of the time.)
-// There is a running maximum and sum per head (one pass).  The maximum is only renewed when a score
-// passes it by 2^8 (all in log2 units), which bounds p by 256 and spares the cross-lane maximum on
-// most tiles; beside an e4m3 cache p is fp16 and taken 2^7 larger (kLift).  P is rounded to the values' 16-bit type for the second product; sums, maxima and O are fp32.
+// There is a running maximum and sum per head (one pass).  The reference that weights are taken by is
+// renewed only when a score passes it, and then put 2^8 above that maximum (all in log2 units), which
+// bounds p by 1 and spares the cross-lane maximum on most tiles; beside an e4m3 cache p is fp16 and taken
+// 2^15 larger (kLift).  P is rounded to the values' 16-bit type for the second product; sums, maxima and O are fp32.
 // An e4m3 cache is widened to fp16 (exactly) between shared memory and the product; queries become
 // fp16 scaled by a power of two per head so that none overflows.
 //
@@ -44,12 +45,13 @@ constexpr int kTileKeys = 32;
 constexpr int kMaxCtas = 320;
 constexpr int kMaxIntervals = 8;
 constexpr int kRowCost = 2;
-constexpr float kRenew = 8.f;       // log2 units a score may pass the running maximum by
-// Log2 units that the reference of fp16 weights lies below that maximum, so that weights reach up to
-// 2^(8 + 7) and what fp16 cannot hold is below 2^-32 of the largest: without them a million keys of 2^-25
-// each beside one large one lost 3 % of the sum.  bf16 weights have fp32's range.
+constexpr float kRenew = 8.f;       // log2 units a score may pass the maximum by that the reference was set from
+// Log2 units that the reference of the weights lies below that maximum.  bf16 weights have fp32's range: 8 above
+// it, no weight is beyond 1, and O stays within fp32 where the sum of |v| does (with weights up to 2^8,
+// values of 2^118 overflowed).  fp16 weights reach up to 2^(8 + 7), and what fp16 cannot hold is below 2^-32 of the
+// largest: with 2^8, a million keys of 2^-25 each beside one large one lost 3 % of the sum.
 template <bool E4M3>
-constexpr float kLift = E4M3 ? 7.f : 0.f;
+constexpr float kLift = E4M3 ? 7.f : -kRenew;
 constexpr size_t kSmemMax = 232448;
 
 // flags of a tile
@@ -704,7 +706,7 @@ __device__ __forceinline__ void compute_tile(State<D, E4M3, NB>& t, uint32_t k_a
         for (int x = 0; x < 4; ++x)
           s[i][n][x] = (bits >> (i * 16 + (x >> 1) * 8)) & 1u ? s[i][n][x] : -INFINITY;
   }
-  // running maximum in log2 units; renewed when a score passes it by kRenew
+  // the reference of the weights in log2 units; renewed when a score passes it by kRenew + kLift
   bool pass = false;
 #pragma unroll
   for (int n = 0; n < NB; ++n)

@@ -49,3 +49,27 @@ def test_infinite_values(B, d, P, H, group, lens):
             bound = BF16_HALF * want.abs() + (BF16_HALF + 2 * ds + 2.0 ** -14) * mag
             assert ((got - want).abs() <= bound)[:, finite].all(), (b, g)
             assert ((lse[b, hs].double().cpu() - wl).abs() <= ds + 2.0 ** -20 * (1 + wl.abs())).all(), (b, g)
+
+
+@pytest.mark.parametrize("group", [1, 12])
+def test_large_values(B, group):
+    """Values of 2^118 whose scores come 2^7.9 above those before them: sums of weights of at most 1 stay within fp32
+    (250 * 2^118 < 2^128), weights of 2^7.9 would not.  Weights are off by 2^-14 at most, o by one rounding more."""
+    P, d = 32, 64
+    lens = [256, 500]
+    cache = B.KVCache.alloc(24, 1, P, d)  # a page is a tile of the kernel
+    cache.k.zero_(), cache.v.zero_()
+    cache.k[1::2, :, :, 0] = 1
+    cache.v[1::2] = 2.0 ** 118
+    table = torch.stack([torch.arange(0, 16), torch.arange(8, 24)]).to(torch.int32).cuda()
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    q = torch.zeros(2, group, d, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1
+    o, lse = B.decode_attention(cache, table, n, q, scale=7.9 * math.log(2))
+    assert B.cm_kv_status(cache) == B.CM_OK
+    for b, m in enumerate(lens):
+        high = sum(1 for i in range(m) if (i // P) % 2)
+        weight = high * 2.0 ** 7.9
+        total = weight + m - high
+        assert ((o[b].double() * 2.0 ** -118 - weight / total).abs() <= (BF16_HALF + 2.0 ** -14) * weight / total).all(), b
+        assert (lse[b].double() - math.log(total)).abs().max() <= 2.0 ** -20 * (1 + math.log(total)), b
