@@ -24,7 +24,7 @@
 // bounds p by 1 and spares the cross-lane maximum on most tiles; beside an e4m3 cache p is fp16 and taken
 // 2^15 larger (kLift).  P is rounded to the values' 16-bit type for the second product; sums, maxima and O are fp32.
 // An e4m3 cache is widened to fp16 (exactly) between shared memory and the product; queries become
-// fp16 scaled by a power of two per head so that none overflows.
+// fp16 scaled by a power of two per head so that none overflows (scale_q).
 //
 // Measured (8 key-value heads of 128, 4 query heads each, bf16): 64 sequences of up to 16384 keys, 331 us =
 // 7.0 TB/s, 103 % of the copy bandwidth; one of 131071, 84 us = 6.4 TB/s; 200 of up to 333, 17.3 us.  What
@@ -581,7 +581,9 @@ __device__ __forceinline__ void read_q(const DecodeArgs& a, int row, int n, int 
 }
 
 // Factor of the scores (log2 units) of the lane's two columns; for an e4m3 cache the fragments become
-// fp16, scaled by a power of two per head to a largest value in [1, 2).
+// fp16, scaled by a power of two per head to a largest value in [2^14, 2^15): no more (65504) fits, and
+// what is smaller loses no bits down to 2^-31 of it.  (Powers of two are held to fp32's normal numbers: a head
+// whose largest value is below 2^-112 stays below 2^14.)
 template <int D, bool E4M3, int NB>
 __device__ __forceinline__ void scale_q(const DecodeArgs& a, int row, int lane, uint32_t (&q)[NB][D / 16][2],
                                         float (&scale)[NB][2]) {
@@ -601,7 +603,7 @@ __device__ __forceinline__ void scale_q(const DecodeArgs& a, int row, int lane, 
         }
       top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-      const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -100), 100);
+      const int e = max(min(static_cast<int>(__float_as_uint(top) >> 23) - 127, 127) - 14, -126);
       const float inv = pow2_bits(-e);
 #pragma unroll
       for (int s = 0; s < D / 16; ++s)

@@ -73,3 +73,28 @@ def test_large_values(B, group):
         total = weight + m - high
         assert ((o[b].double() * 2.0 ** -118 - weight / total).abs() <= (BF16_HALF + 2.0 ** -14) * weight / total).all(), b
         assert (lse[b].double() - math.log(total)).abs().max() <= 2.0 ** -20 * (1 + math.log(total)), b
+
+
+def test_queries_of_any_size_beside_an_e4m3_cache(B):
+    """Queries up to 2^120 (the keys' scale brings the scores back), and queries whose channels are 2^-20 of the
+    head's largest while the keys are 0 in that one: scores as in the other tests."""
+    gen = torch.Generator().manual_seed(63)
+    lens, H, P, d = [50, 700], 2, 16, 64
+    cache, table, n = _filled(B, lens, H, P, d, "e4m3", gen)
+    v = cache.v
+    k = (torch.randn(cache.num_pages, H, P, d, generator=gen) * 2.0 ** -4).to(v.dtype).cuda()
+    tiny = torch.full((H,), 2.0 ** -106, device="cuda")
+    big = B.KVCache(k, v, tiny, cache.v_scale)
+    q = (torch.randn(2, H * 3, d, generator=gen) * 2.0 ** 118).to(torch.bfloat16).cuda()
+    scale = 2.0 ** -10
+    o, lse = B.decode_attention(big, table, n, q, scale=scale)
+    assert o.isfinite().all() and B.cm_kv_status(big) == B.CM_OK
+    _check_decode(big, table, lens, q, o, lse, scale, lambda b, g: torch.arange(lens[b]))
+    k.view(torch.uint8)[..., 0] = 0
+    one = torch.ones(H, device="cuda")
+    small = B.KVCache(k, v, one, cache.v_scale)
+    q = (torch.randn(2, H * 3, d, generator=gen) * 2.0 ** -20).to(torch.bfloat16).cuda()
+    q[..., 0] = 1
+    scale = 2.0 ** 21
+    o, lse = B.decode_attention(small, table, n, q, scale=scale)
+    _check_decode(small, table, lens, q, o, lse, scale, lambda b, g: torch.arange(lens[b]))
