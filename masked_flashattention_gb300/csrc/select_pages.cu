@@ -90,7 +90,8 @@ __device__ __forceinline__ void quantise(const SelectParams& p, const __nv_bfloa
   }
 }
 
-// Summaries of 16 pages as a lane holds them: 16-byte pieces of pages lane / 4 and 8 further.
+// Summaries of 16 pages as a lane holds them: 16-byte pieces of pages lane / 4 and 8 further.  Loaded from L2 (ld.cg)
+// rather than as read-only data: the append before may still be writing them when this kernel's blocks start.
 template <int D>
 struct Summaries {
   static constexpr int kLoads = 2 * D / 64;
@@ -102,11 +103,11 @@ struct Summaries {
     for (int i = 0; i < 2; ++i) {
       const int page = __shfl_sync(0xFFFFFFFFu, number, half * 16 + i * 8 + r);
       const int64_t at = static_cast<int64_t>(page) * p.c.H_kv + g;
-      scale[i] = page < 0 ? -1.f : __ldg(p.c.summary_scale + at);
+      scale[i] = page < 0 ? -1.f : __ldcg(p.c.summary_scale + at);
 #pragma unroll
       for (int j = 0; j < kLoads; ++j)
         y[i][j] = page < 0 ? make_uint4(0, 0, 0, 0)
-                           : __ldg(reinterpret_cast<const uint4*>(p.c.summary + at * 2 * D + j * 64 + t * 16));
+                           : __ldcg(reinterpret_cast<const uint4*>(p.c.summary + at * 2 * D + j * 64 + t * 16));
     }
   }
 };

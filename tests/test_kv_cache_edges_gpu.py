@@ -98,3 +98,36 @@ def test_queries_of_any_size_beside_an_e4m3_cache(B):
     scale = 2.0 ** 21
     o, lse = B.decode_attention(small, table, n, q, scale=scale)
     _check_decode(small, table, lens, q, o, lse, scale, lambda b, g: torch.arange(lens[b]))
+
+
+# ---- calls that overlap ------------------------------------------------------------------------
+def test_selection_sees_the_summaries_of_the_append_before_it(B):
+    """Appends and selections in turn, without a wait between them: each selection goes by what the append just
+    before it wrote.  A step writes row 0 of one page anew, whose summary then is that token's."""
+    gen = torch.Generator().manual_seed(64)
+    Bn, H, P, d, per, n, steps = 40, 4, 16, 128, 8, 3, 80
+    cache = B.KVCache.alloc(Bn * per, H, P, d, summaries=True)
+    table = torch.randperm(Bn * per, generator=gen).to(torch.int32).view(Bn, per).cuda()
+    full = torch.full((Bn,), per * P, dtype=torch.int32, device="cuda")
+    zeros = torch.zeros(Bn, H, per * P, d, dtype=torch.bfloat16, device="cuda")
+    B.cm_kv_append(cache, table, torch.zeros_like(full), zeros, zeros)
+    place = torch.randint(0, per, (steps, Bn), generator=gen)
+    power = torch.randint(-6, 7, (steps, Bn, H), generator=gen)  # scores are d times these powers of two
+    tokens = torch.exp2(power.float()).to(torch.bfloat16).cuda()[..., None, None].expand(steps, Bn, H, 1, d).contiguous()
+    lens = (place * P).to(torch.int32).cuda()
+    q = torch.ones(Bn, H * 2, d, dtype=torch.bfloat16, device="cuda")
+    work = torch.empty(B.cm_select_pages_workspace_size(Bn, H, per), dtype=torch.uint8, device="cuda")
+    sel = torch.empty(steps, Bn, H, n, dtype=torch.int32, device="cuda")
+    nsel = torch.empty(steps, Bn, H, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    for t in range(steps):
+        B.cm_kv_append(cache, table, lens[t], tokens[t], tokens[t])
+        B.cm_select_pages(cache, table, full, q, sel[t], nsel[t], work)
+    assert B.cm_kv_status(cache) == B.CM_OK
+    assert (nsel == n).all()
+    sel, value = sel.cpu(), torch.zeros(Bn, H, per, dtype=F64)
+    for t in range(steps):
+        value[torch.arange(Bn), :, place[t]] = torch.exp2(power[t].double())
+        for b in range(Bn):
+            for h in range(H):
+                assert sel[t, b, h].tolist() == K.pick(value[b, h].tolist(), n, 0, 0), (t, b, h)
