@@ -131,3 +131,50 @@ def test_selection_sees_the_summaries_of_the_append_before_it(B):
         for b in range(Bn):
             for h in range(H):
                 assert sel[t, b, h].tolist() == K.pick(value[b, h].tolist(), n, 0, 0), (t, b, h)
+
+
+_FIRST_CALLS = """
+import threading, torch
+from masked_flashattention_gb300 import binding as B
+P, d, n = 64, 128, 300
+gen = torch.Generator().manual_seed(5)
+sets = []
+for _ in range(4):
+    cache = B.KVCache.alloc(5, 2, P, d)
+    cache.k.copy_(torch.randn(5, 2, P, d, generator=gen)), cache.v.copy_(torch.randn(5, 2, P, d, generator=gen))
+    q = torch.randn(1, 8, d, generator=gen).to(torch.bfloat16).cuda()
+    work = torch.empty(B.cm_attn_decode_workspace_size(1, 8, 2, d), dtype=torch.uint8, device="cuda")
+    sets.append((cache, q, torch.zeros_like(q), work, torch.cuda.Stream()))
+table = torch.arange(5, dtype=torch.int32, device="cuda")[None]
+lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+B._serving()
+torch.cuda.synchronize()
+gate, errors = threading.Barrier(4), []
+def first(cache, q, o, work, stream):
+    try:
+        torch.cuda.set_device(0)
+        gate.wait()
+        B.cm_attn_decode(cache, table, lens, q, o, None, work, stream=stream)
+    except Exception as e:
+        errors.append(repr(e))
+threads = [threading.Thread(target=first, args=s) for s in sets]
+[t.start() for t in threads], [t.join() for t in threads]
+torch.cuda.synchronize()
+assert not errors, errors
+for cache, q, o, work, _ in sets:
+    again = torch.zeros_like(o)
+    B.cm_attn_decode(cache, table, lens, q, again, None, work)
+    assert torch.equal(o, again) and o.any() and B.cm_kv_status(cache) == 0
+print("first calls ok")
+"""
+
+
+def test_first_calls_of_several_threads():
+    """The first calls of a process may come from several host threads at once."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    for _ in range(3):
+        r = subprocess.run([sys.executable, "-c", _FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=300)
+        assert r.returncode == 0 and "first calls ok" in r.stdout, r.stderr
