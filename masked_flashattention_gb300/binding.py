@@ -750,8 +750,8 @@ def _for_stream(stream, make):
     stream still does can write, and all kept from reuse until both streams have done with them."""
     if stream is None:
         return make()
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream))
+    if not hasattr(stream, "cuda_stream"):  # ExternalStream(0) would be a new stream of torch's own
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
     here = torch.cuda.current_stream()
     with torch.cuda.stream(stream):
         made = make()

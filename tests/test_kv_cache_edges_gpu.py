@@ -178,3 +178,39 @@ def test_first_calls_of_several_threads():
     for _ in range(3):
         r = subprocess.run([sys.executable, "-c", _FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=300)
         assert r.returncode == 0 and "first calls ok" in r.stdout, r.stderr
+
+
+def test_handle_0_is_the_default_stream(B):
+    """Memory for work on stream handle 0 is the default stream's, from whatever stream the call comes."""
+    with torch.cuda.stream(torch.cuda.Stream()):
+        def make():
+            assert torch.cuda.current_stream() == torch.cuda.default_stream()
+            return (torch.empty(8, device="cuda"),)
+        B._for_stream(0, make)
+        B._for_stream(torch.cuda.default_stream(), make)
+
+
+def test_results_for_handle_0_from_another_stream(B):
+    """decode_attention and select_pages on stream handle 0, called where another stream is current and has
+    memory of the same sizes that it still writes to."""
+    gen = torch.Generator().manual_seed(66)
+    lens, H, P, d, n = [3000, 10, 700], 2, 64, 128, 5
+    cache, table, m = _filled(B, lens, H, P, d, "bf16", gen)
+    s = torch.randint(-127, 128, (cache.num_pages, H, 2, d), generator=gen, dtype=torch.int8).cuda()
+    cache = B.KVCache(cache.k, cache.v, summary=s, summary_scale=torch.ones(cache.num_pages, H, device="cuda"))
+    q = torch.randn(3, 8, d, generator=gen).to(torch.bfloat16).cuda()
+    want, chosen = B.decode_attention(cache, table, m, q), B.select_pages(cache, table, m, q, n)
+    sizes = [B.cm_attn_decode_workspace_size(3, 8, H, d), B.cm_select_pages_workspace_size(3, H, table.shape[1]),
+             3 * 8 * d * 2, 3 * 8 * 4, 3 * H * n * 4, 3 * H * 4]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        held = [torch.empty(b, dtype=torch.uint8, device="cuda") for b in sizes]
+        torch.cuda._sleep(50_000_000)
+        for t in held:
+            t.fill_(255)
+        del held, t
+        got = B.decode_attention(cache, table, m, q, stream=0), B.select_pages(cache, table, m, q, n, stream=0)
+        torch.cuda.synchronize()
+    for a, b in zip((*got[0], *got[1]), (*want, *chosen)):
+        assert torch.equal(a, b)
+    assert B.cm_kv_status(cache) == B.CM_OK
