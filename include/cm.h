@@ -340,8 +340,9 @@ typedef struct cm_kv_cache {
 
 /* The sequences of a call: page_table device int32 [B][max_pages], lens device int32 [B].
  * Entries of the table past a sequence's tokens may hold anything.  B at most 32767; max_pages *
- * page_size at most 2^27; for cm_attn_decode, the keys a table (or a selection) has room for, times
- * B * H_q, below 2^39. */
+ * page_size at most 2^27; for cm_attn_decode, with n the keys a table (or a selection) has room for and
+ * one row for up to 16 query heads of a key-value head, rows * (ceil(n / 32) + 2) below 2^31 - 320, where
+ * rows = B * H_kv * ceil(H_q / H_kv / 16). */
 typedef struct cm_kv_seqs {
   int32_t B, max_pages;
   const int32_t* page_table;

@@ -1172,7 +1172,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NB>::kThreads, 1)
   }
   const int share = (cta1 - cta0 + C::kPairs - 1) / C::kPairs;  // of a warp
   const int pair = warp & (C::kPairs - 1);
-  const int at = min(cta0 + pair * share, cta1), until = min(at + share, cta1);
+  const int at = min(cta0 + pair * share, cta1), until = min(share, cta1 - at) + at;
   Place place{0, 0, 0, 0, 0};
   if (at < until) place = locate(at);
   __syncthreads();
@@ -1320,7 +1320,7 @@ static int64_t most_tiles(const DecodeParams& p) {
 bool decode_fits(const DecodeParams& p) {
   const int group = p.H_q / p.c.H_kv, heads = heads_of(group);
   const int64_t rows = static_cast<int64_t>(p.c.B) * p.c.H_kv * ((group + heads - 1) / heads);
-  return rows * (most_tiles(p) + kRowCost) < (1LL << 31);
+  return rows * (most_tiles(p) + kRowCost) < (1LL << 31) - kMaxCtas;  // the kernel adds less than its grid to the sum
 }
 
 int launch_attn_decode(const DecodeParams& p, uint64_t wait_ns, cudaStream_t stream) {

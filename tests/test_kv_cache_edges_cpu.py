@@ -2,6 +2,11 @@
 import os
 import subprocess
 
+import pytest
+import torch
+
+from tests.test_kv_cache_cpu import A16, B, _cache, _decode, _seqs  # noqa: F401 (B is a fixture)
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 _SLOW_LOOKUP = r"""
@@ -26,6 +31,7 @@ int main() {
 }
 """
 
+
 def test_the_encoder_is_found_by_every_thread(tmp_path):
     """Threads that ask for the tensor maps' encoder while the first still looks it up get it too."""
     src, exe = tmp_path / "lookup.cpp", tmp_path / "lookup"
@@ -35,3 +41,17 @@ def test_the_encoder_is_found_by_every_thread(tmp_path):
                        capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
     assert subprocess.run([str(exe)], capture_output=True, text=True, timeout=60).stdout.strip() == "1111"
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the pointers are made up: nothing may be queued")
+def test_limit_of_a_decode_call(B):  # noqa: F811
+    """Rows of tiles are counted in 31 bits, with room for the rounding of their division among up to 320 blocks:
+    331 x 151 rows of one head with 42,966 places each are 2^31 - 2, one too many by that; with 42,959 they fit."""
+    def call(pages, group=1, **more):
+        c = _cache(B, num_pages=16, page_size=32, H_kv=151, k_page_stride=151 * 32 * 128, v_page_stride=151 * 32 * 128)
+        return _decode(B, cache=c, seqs=_seqs(B, B=331, max_pages=pages), H_q=151 * group, **more)
+    assert call(42964) == B.CM_ERR_UNSUPPORTED
+    assert call(42957) == B.CM_ERR_CUDA  # goes on to the launch
+    assert call(42957, group=16) == B.CM_ERR_CUDA
+    assert call(42957, group=17) == B.CM_ERR_UNSUPPORTED  # two rows of 16
+    assert call(42964, sel=A16, nsel=A16, sel_max=8192) == B.CM_ERR_CUDA  # what is selected counts
