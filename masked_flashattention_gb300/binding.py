@@ -568,11 +568,15 @@ def _kv_stream(cache: KVCache, stream) -> int:
     return _stream(stream)
 
 
+def _on_current_device(cache: KVCache):
+    if cache.index != torch._C._cuda_getDevice():
+        raise ValueError(f"the cache is on {cache.device}, which is not the current device")
+
+
 def _kv_seqs(cache: KVCache, page_table, lens):
     """B and the packed cm_kv_seqs."""
     dev, shape = cache.index, page_table.shape
-    if dev != torch._C._cuda_getDevice():
-        raise ValueError(f"the cache is on {cache.device}, which is not the current device")
+    _on_current_device(cache)
     if not (len(shape) == 2 and page_table.dtype is _I32 and page_table.get_device() == dev
             and page_table.is_contiguous()):
         raise ValueError("page_table must be a contiguous int32 tensor [B, max_pages] on "
@@ -742,7 +746,8 @@ def cm_select_pages(cache: KVCache, page_table, lens, q, sel, nsel, workspace: t
 
 def cm_kv_status(cache: KVCache, stream=None) -> int:
     """The first device error since the last call (CM_OK where there was none); zeroes it."""
-    return lib().cm_kv_status(ctypes.byref(cache.c), _stream(stream))
+    _on_current_device(cache)  # another device's stream would not wait for the work that is asked about
+    return lib().cm_kv_status(ctypes.byref(cache.c), _kv_stream(cache, stream))
 
 
 def _for_stream(stream, make):

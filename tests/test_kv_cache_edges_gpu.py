@@ -214,3 +214,13 @@ def test_results_for_handle_0_from_another_stream(B):
     for a, b in zip((*got[0], *got[1]), (*want, *chosen)):
         assert torch.equal(a, b)
     assert B.cm_kv_status(cache) == B.CM_OK
+
+
+def test_status_of_a_cache_on_another_device(B):
+    """Like the other calls, cm_kv_status wants the cache's device to be the current one: another device's stream
+    would not wait for the work that it asks about."""
+    cache = B.KVCache.alloc(2, 1, 16, 64)
+    assert B.cm_kv_status(cache) == B.CM_OK
+    cache.index += 1
+    with pytest.raises(ValueError):
+        B.cm_kv_status(cache)
