@@ -224,3 +224,41 @@ def test_status_of_a_cache_on_another_device(B):
     cache.index += 1
     with pytest.raises(ValueError):
         B.cm_kv_status(cache)
+
+
+def test_the_loop_of_the_readme(B):
+    """The README's generation loop as it stands there: prompt, then tokens, each one further."""
+    import os
+    import re
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    blocks = re.findall(r"```python\n(.*?)```", open(os.path.join(root, "README.md")).read(), re.S)
+    code, = (x for x in blocks if "KVCache.alloc" in x)
+    gen = torch.Generator().manual_seed(69)
+    Bn, H, Hq, T, d, S, num_pages, steps = 2, 2, 4, 37, 64, 256, 8, 30
+    draw = lambda h, t: torch.randn(Bn, h, t, d, generator=gen).to(torch.bfloat16).cuda()  # noqa: E731
+    prompt = [draw(H, T), draw(H, T), draw(Hq, T)]
+    tokens = [(draw(H, 1), draw(H, 1), draw(Hq, 1)) for _ in range(steps)]
+    angle = torch.rand(S, d // 2, generator=gen, dtype=F64) * 50
+    spec = B.cm_compile_spec("region all : j <= i")
+    desc = B.Descriptor(spec, spec, Bn, S)
+    B.cm_build_descriptor(spec, spec, torch.tensor([[0, S]] * Bn, dtype=torch.int32, device="cuda"),
+                          torch.ones(Bn, dtype=torch.int32, device="cuda"), desc)
+    names = {"torch": torch, "cm": B, "num_pages": num_pages, "H_kv": H, "d": d, "B": Bn, "desc": desc,
+             "page_table": torch.arange(num_pages, dtype=torch.int32, device="cuda").view(Bn, -1).contiguous(),
+             "rope": torch.stack([angle.cos(), angle.sin()], 2).float().cuda(), "tokens": [tuple(x.clone() for x in t) for t in tokens],
+             "k": prompt[0], "v": prompt[1], "q": prompt[2], "q_rot": torch.empty_like(prompt[2]), "k_rot": torch.empty_like(prompt[0])}
+    names["lens"], names["after"] = (torch.zeros(Bn, dtype=torch.int32, device="cuda") for _ in range(2))
+    exec(code, names)
+    cache = names["cache"]
+    assert names["after"].tolist() == [T + steps] * Bn and B.cm_kv_status(cache) == B.CM_OK
+    rows = torch.arange(T + steps)
+    k, v, _, _ = _host(cache)
+    for b in range(Bn):
+        for g in range(H):
+            want = torch.cat([prompt[1][b, g], *(t[1][b, g] for t in tokens)]).cpu().to(F64)
+            assert torch.equal(K.rows(v, None, names["page_table"][b].cpu(), g, rows), want)
+    # the last step attends to all of it (64 pages are more than there are, so the selection is every page)
+    last = tokens[-1][2].cpu()
+    q = torch.stack([K.rotate(last[b, :, 0], names["rope"][T + steps - 1, :, 0].cpu(),
+                              names["rope"][T + steps - 1, :, 1].cpu(), False)[0] for b in range(Bn)]).to(torch.bfloat16)
+    _check_decode(cache, names["page_table"], [T + steps] * Bn, q, names["o"], names["lse"], 1 / math.sqrt(d), lambda b, g: rows)
