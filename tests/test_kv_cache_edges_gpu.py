@@ -262,3 +262,109 @@ def test_the_loop_of_the_readme(B):
     q = torch.stack([K.rotate(last[b, :, 0], names["rope"][T + steps - 1, :, 0].cpu(),
                               names["rope"][T + steps - 1, :, 1].cpu(), False)[0] for b in range(Bn)]).to(torch.bfloat16)
     _check_decode(cache, names["page_table"], [T + steps] * Bn, q, names["o"], names["lse"], 1 / math.sqrt(d), lambda b, g: rows)
+
+
+# ---- how far outputs may be off ------------------------------------------------------------------
+def _sharp_bound(kv, n, want, mag, size, d):
+    """The scores' error and the output's rounding as in _check_decode, and in place of a rounding of every weight
+    to bf16 what the kernel rounds: a weight beside bf16 values is two bf16 numbers, the first cut (the rest is below
+    2^-7 of it), the second rounded (half a step: 2^-8 of that); beside e4m3 values it is one fp16 number (2^-11).  Two
+    exp2 of 2^-22 each.  The second product adds 16 terms and the sum so far up to 4 times a tile of 32 keys, and may cut
+    each term at 2^-23 of the largest."""
+    ds = (d + 8) * 2 * 2.0 ** -24 * size + 2.0 ** -20
+    weight = 2.0 ** -15 if kv == "bf16" else 2.0 ** -11
+    return BF16_HALF * want.abs() + (1 + BF16_HALF) * (weight + 2 * ds + 2.0 ** -21 + 4 * ((n + 31) // 32) * 17 * 2.0 ** -23) * mag
+
+
+def _close_scores(heads, d):
+    """Two keys whose weights differ by up to 6 %, with values 1 and -1: what is left of the values is less than
+    their weights' rounding to 8 bits."""
+    k = torch.zeros(2, d)
+    k[0, 0], k[1, 0] = 1, 0.9375
+    v = torch.ones(2, d)
+    v[1] = -1
+    q = torch.zeros(heads, d)
+    q[:, 0] = torch.arange(heads) / heads + 1 / 128
+    return q.to(torch.bfloat16), k, v
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("group", [8, 16])
+def test_cancelling_values(B, kv, group):
+    """Beside bf16 values, weights rounded to bf16 alone would be outside the bound (shown on the plain form first)."""
+    d, P = 64, 16
+    q, k, v = _close_scores(group, d)
+    dtype = torch.bfloat16 if kv == "bf16" else torch.float8_e4m3fn
+    pools = [torch.zeros(1, 1, P, d) for _ in range(2)]
+    pools[0][0, 0, :2], pools[1][0, 0, :2] = k, v
+    pools = [x.to(dtype).cuda() for x in pools]
+    one = torch.ones(1, device="cuda")
+    scales = {"k_scale": one, "v_scale": one} if kv == "e4m3" else {}
+    cache = B.KVCache(*pools, **scales)
+    want, wl, size, mag = K.decode(q, k.to(F64), v.to(F64), 1.0)
+    bound = _sharp_bound(kv, 2, want, mag, size, d)
+    s = q.to(F64) @ k.to(F64).T
+    p = torch.exp(s - s.amax(1, keepdim=True))
+    rounded = p.to(torch.bfloat16).to(F64) @ v.to(F64) / p.sum(1, keepdim=True)
+    assert kv == "e4m3" or ((rounded - want).abs() > bound).any()
+    table, n = torch.zeros(1, 1, dtype=torch.int32, device="cuda"), torch.tensor([2], dtype=torch.int32, device="cuda")
+    o, lse = B.decode_attention(cache, table, n, q.cuda()[None], scale=1.0)
+    err = (o[0].double().cpu() - want).abs()
+    assert (err <= bound).all(), (err / bound).max()
+    assert ((lse[0].double().cpu() - wl).abs() <= 2.0 ** -19 * (1 + wl.abs())).all()
+
+
+@pytest.mark.parametrize("d,P,kv,H,group", [(128, 64, "bf16", 2, 4), (64, 16, "bf16", 1, 16), (128, 16, "e4m3", 2, 3),
+                                            (64, 32, "e4m3", 1, 12)])
+def test_decode_is_off_by_its_own_rounding(B, d, P, kv, H, group):
+    """Values of magnitude 1 and random signs, so that the outputs are small beside the weighted magnitudes."""
+    gen = torch.Generator().manual_seed(70)
+    lens = [3, 17, 33, 100, 300]
+    cache, table, n = _filled(B, lens, H, P, d, kv, gen)
+    sign = torch.randint(0, 2, cache.v.shape, generator=gen).float() * 2 - 1
+    v = sign.to(cache.v.dtype).cuda()
+    scales = {} if kv == "bf16" else {"k_scale": cache.k_scale, "v_scale": torch.ones(H, device="cuda")}
+    cache = B.KVCache(cache.k, v, **scales)
+    q = torch.randn(len(lens), H * group, d, generator=gen).to(torch.bfloat16).cuda()
+    o, lse = B.decode_attention(cache, table, n, q)
+    assert B.cm_kv_status(cache) == B.CM_OK
+    k, v, ks, vs = _host(cache)
+    where, worst = table.cpu(), 0.0
+    for b, m in enumerate(lens):
+        for g in range(H):
+            kk, vv = (K.rows(x, s, where[b], g, torch.arange(m)) for x, s in ((k, ks), (v, vs)))
+            hs = slice(g * group, (g + 1) * group)
+            want, _, size, mag = K.decode(q[b, hs].cpu(), kk, vv, 1 / math.sqrt(d))
+            err = (o[b, hs].double().cpu() - want).abs() / _sharp_bound(kv, m, want, mag, size, d)
+            worst = max(worst, err.max().item())
+    assert worst <= 1, worst
+
+
+def test_tokens_after_a_prompt_are_off_by_their_own_rounding(B):
+    """A prompt and the tokens after it under one mask, token by token, against the 64-bit form of the rows."""
+    from masked_flashattention_gb300 import specs
+    from oracle import masks as M
+    gen = torch.Generator().manual_seed(71)
+    H, S, d, P, T, wid = 2, 256, 64, 32, 150, 5
+    cuts = [0, 20, 100, 190, S]
+    f, b = B.cm_compile_spec(specs.FWD[wid]), B.cm_compile_spec(specs.BWD[wid])
+    desc = B.Descriptor(f, b, 1, S)
+    B.cm_build_descriptor(f, b, torch.tensor([cuts], dtype=torch.int32, device="cuda"),
+                          torch.tensor([4], dtype=torch.int32, device="cuda"), desc)
+    mask = torch.from_numpy(M.dense_mask(wid, torch.tensor(cuts).numpy(), 4, S))
+    q, k, v = (torch.randn(1, H, S, d, generator=gen).to(torch.bfloat16).cuda() for _ in range(3))
+    cache = B.KVCache.alloc(S // P, H, P, d)
+    table = torch.randperm(S // P, generator=gen).to(torch.int32).view(1, -1).cuda()
+    lens, after = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    B.cm_kv_append(cache, table, lens, k[:, :, :T], v[:, :, :T], new_lens=after)
+    for i in range(T, S):
+        lens, after = after, lens
+        B.cm_kv_append(cache, table, lens, k[:, :, i:i + 1], v[:, :, i:i + 1], new_lens=after)
+        o, lse = B.decode_attention(cache, table, after, q[:, :, i], desc=desc)
+        see = mask[i].nonzero()[:, 0]
+        for h in range(H):
+            want, wl, size, mag = K.decode(q[0, h, i:i + 1].cpu(), k[0, h].double().cpu()[see], v[0, h].double().cpu()[see],
+                                           1 / math.sqrt(d))
+            assert ((o[0, h:h + 1].double().cpu() - want).abs() <= _sharp_bound("bf16", i + 1, want, mag, size, d)).all(), (i, h)
+            assert (lse[0, h].double().cpu() - wl).abs().item() <= (d + 8) * 2.0 ** -23 * size + 2.0 ** -18 * (1 + wl.abs().item())
+    assert B.cm_kv_status(cache) == B.CM_OK and B.cm_get_status(desc) == B.CM_OK
