@@ -398,17 +398,20 @@ CM_API int cm_attn_decode_workspace_size(int B, int H_q, int H_kv, int d, size_t
  * o[b][h] = softmax_j(scale * q[b][h] . k[j]) v[j] over the visible j < lens[b], of key-value head
  * h / (H_q / H_kv).  q, o: bf16 [B][H_q][d] with strides in elements for {sequence, head}, multiples
  * of 8; lse: fp32 [B][H_q] in natural log, or NULL.  H_q is a multiple of H_kv.  (Beside an e4m3 cache,
- * channels of q below 2^-31 of their head's largest lose bits.)
+ * channels of q below 2^-31 of their head's largest lose bits.)  o may be q with the same strides; otherwise
+ * outputs overlap nothing else.
  *   desc  NULL: every token is visible.  Else a descriptor of B samples with S >= lens[b] in the
  *         CM_FORM_VISIBLE form: the token sees what row lens[b] - 1 of the forward half says, cut
  *         at lens[b].  One built for the prompt's MaskSpec with room for the tokens to come (the
  *         last segment ending at S) serves the prompt and every token after it.
  *   sel   NULL, or device int32 [B][H_kv][sel_max] with nsel device int32 [B][H_kv]: only the pages
- *         sel[b][g][0 .. nsel[b][g]-1] (places in the sequence's table, ascending) are attended to.
- *         Not together with desc.
- * A row with no visible key gets o = 0 and lse = -inf.  So does a sequence whose length is below 0,
- * beyond the table or beyond desc->S (with CM_ERR_DEVICE_CHECK); a page outside the pool, or a
- * selected page that is out of order or past the sequence, is skipped (same).
+ *         sel[b][g][0 .. nsel[b][g]-1] (places in the sequence's table, ascending; nsel is held to
+ *         [0, sel_max]) are attended to.  Not together with desc.
+ * A row with no visible key, or whose visible keys all score -inf, gets o = 0 and lse = -inf, and
+ * so does a sequence whose length is below 0, beyond the table or beyond
+ * desc->S (with CM_ERR_DEVICE_CHECK); a page outside the pool, or a selected page that is not above the
+ * entry before it or is past the sequence, is skipped (same).  A visible key
+ * whose score is NaN or +inf makes its head's o and lse NaN.
  * The sums of a row are split over the keys in a way that depends on all the batch's lengths; the
  * same call gives the same bits every time. */
 CM_API int cm_attn_decode(const cm_kv_cache* cache, const cm_kv_seqs* seqs,

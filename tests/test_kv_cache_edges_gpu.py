@@ -368,3 +368,77 @@ def test_tokens_after_a_prompt_are_off_by_their_own_rounding(B):
             assert ((o[0, h:h + 1].double().cpu() - want).abs() <= _sharp_bound("bf16", i + 1, want, mag, size, d)).all(), (i, h)
             assert (lse[0, h].double().cpu() - wl).abs().item() <= (d + 8) * 2.0 ** -23 * size + 2.0 ** -18 * (1 + wl.abs().item())
     assert B.cm_kv_status(cache) == B.CM_OK and B.cm_get_status(desc) == B.CM_OK
+
+
+@pytest.mark.parametrize("lens", [[300, 0, 77], [20000, 5, 0]])
+def test_outputs_in_place_of_the_queries(B, lens):
+    """o may be q: a row's queries have been read by all that need them before its output is written."""
+    gen = torch.Generator().manual_seed(72)
+    cache, table, n = _filled(B, lens, 2, 64, 128, "bf16", gen)
+    q = torch.randn(3, 2 * 20, 128, generator=gen).to(torch.bfloat16).cuda()
+    want, wl = B.decode_attention(cache, table, n, q)
+    work = torch.empty(B.cm_attn_decode_workspace_size(3, 40, 2, 128), dtype=torch.uint8, device="cuda")
+    lse = torch.empty_like(wl)
+    B.cm_attn_decode(cache, table, n, q, q, lse, work)
+    assert torch.equal(q, want) and torch.equal(lse, wl) and B.cm_kv_status(cache) == B.CM_OK
+
+
+_FIRST_CAPTURE = """
+import torch
+from masked_flashattention_gb300 import binding as B
+P, d, n = 64, 128, 300
+gen = torch.Generator().manual_seed(6)
+caches = [B.KVCache.alloc(6, 2, P, d, summaries=True) for _ in range(2)]
+draw = lambda h, t: torch.randn(1, h, t, d, generator=gen).to(torch.bfloat16).cuda()
+k, v, q = draw(2, n), draw(2, n), draw(8, 1)
+table = torch.arange(6, dtype=torch.int32, device="cuda")[None]
+lens, after = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+torch.cuda.synchronize()
+def step(cache):
+    B.cm_kv_append(cache, table, lens, k, v, new_lens=after)
+    sel, nsel = B.select_pages(cache, table, after, q[:, :, 0], 3, 1, 1)
+    return [sel, *B.decode_attention(cache, table, after, q[:, :, 0], sel=sel, nsel=nsel),
+            *B.decode_attention(cache, table, after, q[:, :, 0])]
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = step(caches[0])
+graph.replay()
+want = step(caches[1])
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, want)) and got[1].any()
+assert B.cm_kv_status(caches[0]) == 0 and B.cm_kv_status(caches[1]) == 0
+print("first capture ok")
+"""
+
+
+def test_first_calls_of_a_process_in_a_capture():
+    """Nothing has to be called before a step is captured."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _FIRST_CAPTURE], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "first capture ok" in r.stdout, r.stderr
+
+
+@pytest.mark.parametrize("group", [2, 10])
+def test_infinite_keys(B, group):
+    """A key of -inf against a positive channel has no weight; against a negative one it makes that head NaN; where
+    every key is such a key, the row is empty."""
+    gen = torch.Generator().manual_seed(73)
+    lens, P, d = [40, 40, 3], 16, 64
+    cache, table, n = _filled(B, lens, 1, P, d, "bf16", gen)
+    where = table.cpu()
+    cache.k[int(where[0, 1]), 0, 5, 7] = -math.inf  # position 21 of sequence 0
+    cache.k[int(where[2, 0]), 0, :3, 7] = -math.inf
+    q = torch.randn(3, group, d, generator=gen).to(torch.bfloat16).cuda()
+    q[..., 7] = 1
+    q[0, 1, 7] = -1
+    o, lse = B.decode_attention(cache, table, n, q)
+    assert B.cm_kv_status(cache) == B.CM_OK
+    assert o[0, 1].isnan().all() and lse[0, 1].isnan()
+    assert not o[2].any() and (lse[2] == -math.inf).all()
+    keep = [h for h in range(group) if h != 1]
+    q0, o0, l0 = q[:, keep].contiguous(), o[:, keep].contiguous(), lse[:, keep].contiguous()
+    seen = [torch.tensor([p for p in range(40) if p != 21]), torch.arange(40), torch.arange(0)]
+    _check_decode(cache, table, lens, q0, o0, l0, 1 / 8, lambda b, g: seen[b])
