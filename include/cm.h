@@ -353,7 +353,8 @@ typedef struct cm_kv_seqs {
  * elements for {sequence, head, token}, each a multiple of 8.
  *   k, v    H_kv heads; q (may be NULL) H_q heads, rotated into q_out; k_out (may be NULL) receives
  *           the rotated keys.  q_out may be q, and k_out k, with the same strides; otherwise
- *           outputs overlap nothing else.
+ *           outputs overlap nothing else, nor themselves (an output's strides are at least d
+ *           along every axis of more than one entry; inputs may be expanded, strides of 0).
  *   cu_new  packed tokens: device int32 [B + 1], ascending, sequence b's are tokens cu_new[b] .. cu_new[b+1]-1
  *           of n_tokens (the sequence strides are not used).  NULL: padded tokens, sequence b's
  *           are tokens 0 .. n_new[b]-1 of n_tokens; n_new (device int32 [B]) NULL: all n_tokens.
@@ -399,7 +400,7 @@ CM_API int cm_attn_decode_workspace_size(int B, int H_q, int H_kv, int d, size_t
  * h / (H_q / H_kv).  q, o: bf16 [B][H_q][d] with strides in elements for {sequence, head}, multiples
  * of 8; lse: fp32 [B][H_q] in natural log, or NULL.  H_q is a multiple of H_kv.  (Beside an e4m3 cache,
  * channels of q below 2^-31 of their head's largest lose bits.)  o may be q with the same strides; otherwise
- * outputs overlap nothing else.
+ * outputs overlap nothing else, nor themselves (o_stride at least d).
  *   desc  NULL: every token is visible.  Else a descriptor of B samples with S >= lens[b] in the
  *         CM_FORM_VISIBLE form: the token sees what row lens[b] - 1 of the forward half says, cut
  *         at lens[b].  One built for the prompt's MaskSpec with room for the tokens to come (the

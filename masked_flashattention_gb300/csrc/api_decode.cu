@@ -59,6 +59,13 @@ bool good_strides(const int64_t* s, int n) {
   return true;
 }
 
+// Whether an output's rows of d elements lie apart along every axis that has more than one entry.
+bool rows_apart(const int64_t* s, const int64_t* entries, int n, int d) {
+  for (int i = 0; i < n; ++i)
+    if (entries[i] > 1 && s[i] < d) return false;
+  return true;
+}
+
 bool same_strides(const int64_t* a, const int64_t* b) {
   return a[0] == b[0] && a[1] == b[1] && a[2] == b[2];
 }
@@ -118,6 +125,14 @@ CM_API int cm_kv_append(const cm_kv_cache* cache, const cm_kv_seqs* seqs, const 
     if (!good_ptr(t->k_out) || !good_strides(t->k_out_stride, 3)) return CM_ERR_INVALID_ARG;
     if (t->k_out == t->k && !same_strides(t->k_stride, t->k_out_stride)) return CM_ERR_INVALID_ARG;
   }
+  if (!none) {
+    const int64_t seqs_apart = t->cu_new ? 1 : seqs->B;
+    const int64_t q_rows[3] = {seqs_apart, t->H_q, t->n_tokens};
+    const int64_t k_rows[3] = {seqs_apart, cache->H_kv, t->n_tokens};
+    if ((t->q_out && !rows_apart(t->q_out_stride, q_rows, 3, cache->d)) ||
+        (t->k_out && !rows_apart(t->k_out_stride, k_rows, 3, cache->d)))
+      return CM_ERR_INVALID_ARG;
+  }
   if (t->n_tokens < 0 || t->max_new < 0 || t->max_new > t->n_tokens) return CM_ERR_INVALID_ARG;
   if (t->cu_new ? (t->n_new || !good_ints(t->cu_new)) : (t->n_new && !good_ints(t->n_new)))
     return CM_ERR_INVALID_ARG;
@@ -176,6 +191,8 @@ CM_API int cm_attn_decode(const cm_kv_cache* cache, const cm_kv_seqs* seqs,
   if (!good_ptr(q) || !good_ptr(o) || !q_stride || !o_stride || !good_strides(q_stride, 2) ||
       !good_strides(o_stride, 2) || (lse && !aligned(lse, 4)) || !std::isfinite(scale))
     return CM_ERR_INVALID_ARG;
+  const int64_t o_rows[2] = {seqs->B, H_q};
+  if (!rows_apart(o_stride, o_rows, 2, cache->d)) return CM_ERR_INVALID_ARG;
   if ((sel != nullptr) != (nsel != nullptr) || (sel && desc)) return CM_ERR_INVALID_ARG;
   if (sel && (!good_ints(sel) || !good_ints(nsel) || sel_max < 1)) return CM_ERR_INVALID_ARG;
   if (sel && sel_max > 8192) return CM_ERR_UNSUPPORTED;

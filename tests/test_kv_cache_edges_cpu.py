@@ -5,7 +5,7 @@ import subprocess
 import pytest
 import torch
 
-from tests.test_kv_cache_cpu import A16, B, _cache, _decode, _seqs  # noqa: F401 (B is a fixture)
+from tests.test_kv_cache_cpu import A16, B, _cache, _decode, _new, _seqs  # noqa: F401 (B is a fixture)
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -55,3 +55,29 @@ def test_limit_of_a_decode_call(B):  # noqa: F811
     assert call(42957, group=16) == B.CM_ERR_CUDA
     assert call(42957, group=17) == B.CM_ERR_UNSUPPORTED  # two rows of 16
     assert call(42964, sel=A16, nsel=A16, sel_max=8192) == B.CM_ERR_CUDA  # what is selected counts
+
+
+def test_outputs_that_overlap_themselves(B):  # noqa: F811
+    """Heads, tokens or sequences of an output in the same memory (an expanded tensor) are refused; inputs may be."""
+    for name in ("q_out", "k_out"):
+        for s in ((1024, 0, 128), (0, 512, 128), (1024, 512, 64), (1024, 8, 128)):
+            t = _new(B, **{name: 2 * A16, name + "_stride": s})
+            assert B.lib().cm_kv_append(_cache(B), _seqs(B), t, None) == B.CM_ERR_INVALID_ARG, (name, s)
+    t = _new(B, cu_new=A16, q_out=2 * A16, q_out_stride=(0, 512, 0))
+    assert B.lib().cm_kv_append(_cache(B), _seqs(B), t, None) == B.CM_ERR_INVALID_ARG
+    for s in ((0, 128), (512, 0), (512, 64)):
+        assert _decode(B, os=s) == B.CM_ERR_INVALID_ARG, s
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the pointers are made up: nothing may be queued")
+def test_inputs_that_are_expanded_and_axes_of_one_entry(B):  # noqa: F811
+    """What goes on to the launch: inputs with strides of 0, and outputs whose axis of one entry has any."""
+    t = _new(B, k_stride=(0, 0, 0), v_stride=(0, 0, 0), q_stride=(0, 0, 0), q_out=2 * A16)
+    assert B.lib().cm_kv_append(_cache(B), _seqs(B), t, None) == B.CM_ERR_CUDA
+    t = _new(B, n_tokens=1, max_new=1, H_q=1, q_out=2 * A16, q_out_stride=(1024, 0, 0))
+    assert B.lib().cm_kv_append(_cache(B), _seqs(B), t, None) == B.CM_ERR_CUDA
+    t = _new(B, cu_new=A16, q_out=2 * A16, q_out_stride=(0, 512, 128))
+    assert B.lib().cm_kv_append(_cache(B), _seqs(B), t, None) == B.CM_ERR_CUDA
+    one = _cache(B, H_kv=1)
+    assert _decode(B, cache=one, seqs=_seqs(B, B=1), H_q=1, qs=(0, 0), os=(0, 0)) == B.CM_ERR_CUDA
+    assert _decode(B, qs=(0, 0)) == B.CM_ERR_CUDA
