@@ -1172,7 +1172,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NB>::kThreads, 1)
   }
   const int share = (cta1 - cta0 + C::kPairs - 1) / C::kPairs;  // of a warp
   const int pair = warp & (C::kPairs - 1);
-  const int at = min(cta0 + pair * share, cta1), until = min(share, cta1 - at) + at;
+  const int at = min(cta0 + pair * share, cta1);
+  const int until = min(static_cast<uint32_t>(at) + share, static_cast<uint32_t>(cta1));  // the sum may pass 2^31
   Place place{0, 0, 0, 0, 0};
   if (at < until) place = locate(at);
   __syncthreads();
