@@ -421,6 +421,18 @@ CM_API int cm_attn_decode(const cm_kv_cache* cache, const cm_kv_seqs* seqs,
                           const int64_t o_stride[2], float* lse, int H_q, float scale,
                           void* workspace, size_t workspace_bytes, void* stream);
 
+/* The same under a sliding window with a few first tokens that stay visible (sinks): the token at
+ * position p = lens[b] - 1 sees the positions j < sinks and p - window < j <= p (window >= 1, sinks >= 0).
+ * Arguments, results and errors as for cm_attn_decode, without a descriptor's limit on the length.  The
+ * page table's entries of pages that hold no visible key are not read, so those pages may be anybody's.  (With n of
+ * cm_kv_seqs' limit at most the keys that sinks and window can cover.)  For prompts and training the same
+ * mask is a MaskSpec, "region i < W + A : j <= i" then "region all : j < A || (j > i - W && j <= i)" for a
+ * window W and A sinks. */
+CM_API int cm_attn_decode_window(const cm_kv_cache* cache, const cm_kv_seqs* seqs, int window,
+                                 int sinks, const void* q, const int64_t q_stride[2], void* o,
+                                 const int64_t o_stride[2], float* lse, int H_q, float scale,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
 /* Workspace bytes of cm_select_pages (rules as for cm_attn_decode's). */
 CM_API int cm_select_pages_workspace_size(int B, int H_kv, int max_pages, size_t* bytes);
 

@@ -124,6 +124,8 @@ def lib() -> ctypes.CDLL:
         L.cm_attn_decode_workspace_size.argtypes = [i32, i32, i32, i32, size_p]
         L.cm_attn_decode.argtypes = [cache_p, seqs_p, ctypes.POINTER(cm_descriptor), vp, vp, i32,
                                      vp, i64_p, vp, i64_p, vp, i32, ctypes.c_float, vp, sz, vp]
+        L.cm_attn_decode_window.argtypes = [cache_p, seqs_p, i32, i32, vp, i64_p, vp, i64_p, vp, i32,
+                                            ctypes.c_float, vp, sz, vp]
         L.cm_select_pages_workspace_size.argtypes = [i32, i32, i32, size_p]
         L.cm_select_pages.argtypes = [cache_p, seqs_p, vp, i64_p, i32, i32, i32, vp, vp, i32,
                                       vp, sz, vp]
@@ -547,7 +549,8 @@ _calls = None
 
 
 def _serving():
-    """(cm_kv_append, cm_attn_decode, cm_select_pages) with every pointer as an address or bytes."""
+    """(cm_kv_append, cm_attn_decode, cm_select_pages, cm_attn_decode_window) with every pointer as an
+    address or bytes."""
     global _calls
     if _calls is None:
         L, vp, i32, sz = lib(), ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
@@ -558,7 +561,9 @@ def _serving():
         _calls = (call("cm_kv_append", vp, vp, vp, vp),
                   call("cm_attn_decode", vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, i32,
                        ctypes.c_float, vp, sz, vp),
-                  call("cm_select_pages", vp, vp, vp, vp, i32, i32, i32, vp, vp, i32, vp, sz, vp))
+                  call("cm_select_pages", vp, vp, vp, vp, i32, i32, i32, vp, vp, i32, vp, sz, vp),
+                  call("cm_attn_decode_window", vp, vp, i32, i32, vp, vp, vp, vp, vp, i32,
+                       ctypes.c_float, vp, sz, vp))
     return _calls
 
 
@@ -686,10 +691,13 @@ def _workspace(w, cache: KVCache):
 
 def cm_attn_decode(cache: KVCache, page_table, lens, q, o, lse, workspace: torch.Tensor,
                    desc: Descriptor | None = None, sel=None, nsel=None,
-                   scale: float | None = None, stream=None) -> None:
+                   scale: float | None = None, stream=None, window: int | None = None,
+                   sinks: int = 0) -> None:
     """Attention of the last of each sequence's lens[b] tokens over the cache: q, o bf16
     [B, H_q, d]; lse fp32 [B, H_q] or None.  desc: the mask, whose row lens[b] - 1 the token sees by;
-    or sel (int32 [B, H_kv, n]) with nsel (int32 [B, H_kv]): the pages to attend to."""
+    or sel (int32 [B, H_kv, n]) with nsel (int32 [B, H_kv]): the pages to attend to; or window, with
+    sinks: the token sees the last `window` tokens, itself among them, and the first `sinks`
+    (cm_attn_decode_window)."""
     B, seqs = _kv_seqs(cache, page_table, lens)
     dev, H = cache.index, q.shape[1]
     qs, os = _one_token(q, "q", cache, B), _one_token(o, "o", cache, B)
@@ -707,10 +715,24 @@ def cm_attn_decode(cache: KVCache, page_table, lens, q, o, lse, workspace: torch
     _workspace(workspace, cache)
     if desc is not None and desc.itab_f.get_device() != dev:
         raise ValueError(f"desc must be on {cache.device}")
+    scale = cache.scale if scale is None else scale
+    if window is not None:
+        if desc is not None or sel is not None:
+            raise ValueError("a window comes without desc and without sel")
+        if window >= 1 << 31 or sinks >= 1 << 31:  # ctypes would take them modulo 2^32
+            raise ValueError("window and sinks must be below 2^31")
+        rc = _serving()[3](cache._address, seqs, window, sinks, q.data_ptr(), qs, o.data_ptr(), os,
+                           _ptr(lse), H, scale, workspace.data_ptr(), workspace.nbytes,
+                           _kv_stream(cache, stream))
+        if rc != CM_OK:
+            raise CMError(rc, "cm_attn_decode_window")
+        return
+    if sinks:
+        raise ValueError("sinks come with a window")
     rc = _serving()[1](cache._address, seqs, None if desc is None else ctypes.addressof(desc.c),
                        _ptr(sel), _ptr(nsel), sel_max, q.data_ptr(), qs, o.data_ptr(), os,
-                       _ptr(lse), H, cache.scale if scale is None else scale,
-                       workspace.data_ptr(), workspace.nbytes, _kv_stream(cache, stream))
+                       _ptr(lse), H, scale, workspace.data_ptr(), workspace.nbytes,
+                       _kv_stream(cache, stream))
     if rc != CM_OK:
         raise CMError(rc, "cm_attn_decode")
 
@@ -767,7 +789,7 @@ def _for_stream(stream, make):
 
 
 def decode_attention(cache: KVCache, page_table, lens, q, desc=None, sel=None, nsel=None,
-                     scale=None, stream=None, workspace=None):
+                     scale=None, stream=None, workspace=None, window=None, sinks=0):
     """cm_attn_decode into new tensors: (o, lse)."""
     B, H, d = q.shape
 
@@ -780,7 +802,8 @@ def decode_attention(cache: KVCache, page_table, lens, q, desc=None, sel=None, n
                 torch.empty(B, H, dtype=torch.float32, device=q.device), w)
 
     o, lse, workspace = _for_stream(stream, make)
-    cm_attn_decode(cache, page_table, lens, q, o, lse, workspace, desc, sel, nsel, scale, stream)
+    cm_attn_decode(cache, page_table, lens, q, o, lse, workspace, desc, sel, nsel, scale, stream, window,
+                   sinks)
     return o, lse
 
 

@@ -101,6 +101,46 @@ int check_heads(int H_q, int H_kv) {
   return H_q > kMaxHeads ? CM_ERR_UNSUPPORTED : CM_OK;
 }
 
+// What the two attention entry points share: their tensors checked, and put into p.
+int check_decode(const cm_kv_cache* cache, const cm_kv_seqs* seqs, const void* q, const int64_t* q_stride, void* o,
+                 const int64_t* o_stride, float* lse, int H_q, float scale, void* workspace,
+                 size_t workspace_bytes, cm::DecodeParams& p) {
+  int rc = check_both(cache, seqs);
+  if (rc != CM_OK) return rc;
+  rc = check_heads(H_q, cache->H_kv);
+  if (rc != CM_OK) return rc;
+  if (!good_ptr(q) || !good_ptr(o) || !q_stride || !o_stride || !good_strides(q_stride, 2) ||
+      !good_strides(o_stride, 2) || (lse && !aligned(lse, 4)) || !std::isfinite(scale))
+    return CM_ERR_INVALID_ARG;
+  const int64_t o_rows[2] = {seqs->B, H_q};
+  if (!rows_apart(o_stride, o_rows, 2, cache->d)) return CM_ERR_INVALID_ARG;
+  size_t need = 0;
+  rc = cm_attn_decode_workspace_size(seqs->B, H_q, cache->H_kv, cache->d, &need);
+  if (rc != CM_OK) return rc;
+  if (!good_ptr(workspace) || workspace_bytes < need) return CM_ERR_INVALID_ARG;
+  p.c = view(cache, seqs);
+  p.itab = nullptr;
+  p.NI = 1;
+  p.S = p.window = p.sinks = p.sel_max = 0;
+  p.sel = p.nsel = nullptr;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.qs = {q_stride[0], q_stride[1], 0};
+  p.os = {o_stride[0], o_stride[1], 0};
+  p.lse = lse;
+  p.H_q = H_q;
+  p.scale = scale;
+  p.workspace = workspace;
+  return CM_OK;
+}
+
+int launch_decode(const cm::DecodeParams& p, void* stream) {
+  if (!cm::decode_fits(p)) return CM_ERR_UNSUPPORTED;
+  return cm::launch_attn_decode(p, cm::wait_limit_ns(), static_cast<cudaStream_t>(stream)) == 0
+             ? CM_OK
+             : CM_ERR_CUDA;
+}
+
 }  // namespace
 
 extern "C" {
@@ -184,15 +224,9 @@ CM_API int cm_attn_decode(const cm_kv_cache* cache, const cm_kv_seqs* seqs,
                           int sel_max, const void* q, const int64_t q_stride[2], void* o,
                           const int64_t o_stride[2], float* lse, int H_q, float scale,
                           void* workspace, size_t workspace_bytes, void* stream) {
-  int rc = check_both(cache, seqs);
+  cm::DecodeParams p;
+  const int rc = check_decode(cache, seqs, q, q_stride, o, o_stride, lse, H_q, scale, workspace, workspace_bytes, p);
   if (rc != CM_OK) return rc;
-  rc = check_heads(H_q, cache->H_kv);
-  if (rc != CM_OK) return rc;
-  if (!good_ptr(q) || !good_ptr(o) || !q_stride || !o_stride || !good_strides(q_stride, 2) ||
-      !good_strides(o_stride, 2) || (lse && !aligned(lse, 4)) || !std::isfinite(scale))
-    return CM_ERR_INVALID_ARG;
-  const int64_t o_rows[2] = {seqs->B, H_q};
-  if (!rows_apart(o_stride, o_rows, 2, cache->d)) return CM_ERR_INVALID_ARG;
   if ((sel != nullptr) != (nsel != nullptr) || (sel && desc)) return CM_ERR_INVALID_ARG;
   if (sel && (!good_ints(sel) || !good_ints(nsel) || sel_max < 1)) return CM_ERR_INVALID_ARG;
   if (sel && sel_max > 8192) return CM_ERR_UNSUPPORTED;
@@ -201,31 +235,28 @@ CM_API int cm_attn_decode(const cm_kv_cache* cache, const cm_kv_seqs* seqs,
         !aligned(desc->itab_f, 16))
       return CM_ERR_INVALID_ARG;
     if (desc->form != CM_FORM_VISIBLE) return CM_ERR_UNSUPPORTED;
+    p.itab = desc->itab_f;
+    p.NI = desc->ni_f;
+    p.S = desc->S;
   }
-  size_t need = 0;
-  rc = cm_attn_decode_workspace_size(seqs->B, H_q, cache->H_kv, cache->d, &need);
-  if (rc != CM_OK) return rc;
-  if (!good_ptr(workspace) || workspace_bytes < need) return CM_ERR_INVALID_ARG;
-  cm::DecodeParams p;
-  p.c = view(cache, seqs);
-  p.itab = desc ? desc->itab_f : nullptr;
-  p.NI = desc ? desc->ni_f : 1;
-  p.S = desc ? desc->S : 0;
   p.sel = sel;
   p.nsel = nsel;
   p.sel_max = sel ? sel_max : 0;
-  p.q = static_cast<const __nv_bfloat16*>(q);
-  p.o = static_cast<__nv_bfloat16*>(o);
-  p.qs = {q_stride[0], q_stride[1], 0};
-  p.os = {o_stride[0], o_stride[1], 0};
-  p.lse = lse;
-  p.H_q = H_q;
-  p.scale = scale;
-  p.workspace = workspace;
-  if (!cm::decode_fits(p)) return CM_ERR_UNSUPPORTED;
-  return cm::launch_attn_decode(p, cm::wait_limit_ns(), static_cast<cudaStream_t>(stream)) == 0
-             ? CM_OK
-             : CM_ERR_CUDA;
+  return launch_decode(p, stream);
+}
+
+CM_API int cm_attn_decode_window(const cm_kv_cache* cache, const cm_kv_seqs* seqs, int window,
+                                 int sinks, const void* q, const int64_t q_stride[2], void* o,
+                                 const int64_t o_stride[2], float* lse, int H_q, float scale,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+  cm::DecodeParams p;
+  const int rc = check_decode(cache, seqs, q, q_stride, o, o_stride, lse, H_q, scale, workspace, workspace_bytes, p);
+  if (rc != CM_OK) return rc;
+  if (window < 1 || sinks < 0) return CM_ERR_INVALID_ARG;
+  p.window = window;
+  p.sinks = sinks;
+  p.NI = 2;
+  return launch_decode(p, stream);
 }
 
 CM_API int cm_select_pages_workspace_size(int B, int H_kv, int max_pages, size_t* bytes) {

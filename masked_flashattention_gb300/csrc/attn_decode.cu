@@ -207,6 +207,8 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int3
 // key-value head of a sequence.  Intervals [st, en) of keys become tile ranges; a tile that several touch
 // belongs to the first in the order of the ranges' starts, so with `before` that order, interval i
 // owns the tiles [max(a_i, max of b_j before i), b_i).
+// Whether a unit's visible keys are intervals (of the mask or of the window), not all below its length.
+__device__ __forceinline__ bool masked(const DecodeParams& p) { return p.itab != nullptr || p.window != 0; }
 __device__ __forceinline__ int checked_length(const DecodeArgs& a, int b, int len, bool report) {
   const DecodeParams& p = a.p;
   const bool good = len >= 0 &&
@@ -215,7 +217,16 @@ __device__ __forceinline__ int checked_length(const DecodeArgs& a, int b, int le
   if (!good && report) set_status(p.c.status, kDevBadMeta, b);
   return good ? len : 0;
 }
+// First key of a sequence's window; 0 where the sinks reach it (one interval then, so that its tiles count as full).
+__device__ __forceinline__ int window_start(const DecodeParams& p, int len) {
+  const int start = max(len - p.window, 0);
+  return p.sinks >= start ? 0 : start;
+}
 __device__ __forceinline__ int2 unit_interval(const DecodeArgs& a, int b, int n, int len) {
+  if (a.p.window) {
+    const int start = window_start(a.p, len);
+    return n == 0 ? make_int2(0, start ? a.p.sinks : 0) : n == 1 ? make_int2(start, len) : make_int2(0, 0);
+  }
   if (a.p.itab == nullptr) return make_int2(0, n == 0 ? len : 0);
   if (n >= a.p.NI || len == 0) return make_int2(0, 0);
   const int2 iv = reinterpret_cast<const int2*>(
@@ -232,7 +243,12 @@ __device__ __forceinline__ int unit_tiles(const DecodeArgs& a, int u, bool repor
     const int n = len ? min(max(chosen, 0), a.p.sel_max) : 0;
     return a.p.c.log2_page == 4 ? (n + 1) / 2 : n << (a.p.c.log2_page - 5);
   }
-  if (a.p.itab == nullptr) return (len + kTileKeys - 1) / kTileKeys;
+  if (!masked(a.p)) return (len + kTileKeys - 1) / kTileKeys;
+  if (a.p.window) {
+    const int start = window_start(a.p, len), end = (len + kTileKeys - 1) / kTileKeys;
+    const int early = start ? (a.p.sinks + kTileKeys - 1) / kTileKeys : 0;
+    return early + max(end - max(start / kTileKeys, early), 0);
+  }
   int lo[kMaxIntervals], hi[kMaxIntervals], total = 0;
 #pragma unroll
   for (int n = 0; n < kMaxIntervals; ++n) {
@@ -276,7 +292,7 @@ __device__ __forceinline__ Plan make_plan(const DecodeArgs& a, int u, int len, i
   w.len = len;
   w.tiles = tiles;
   w.st = w.en = w.from = w.cnt = w.off = 0;
-  if (a.p.itab == nullptr) return w;  // its tiles in order, every key below the length
+  if (!masked(a.p)) return w;  // its tiles in order, every key below the length
   const int2 iv = lane < kMaxIntervals ? unit_interval(a, w.b, lane, w.len) : make_int2(0, 0);
   w.st = iv.x;
   w.en = iv.y;
@@ -384,7 +400,7 @@ __device__ __forceinline__ void next_chunk(const DecodeArgs& a, Walk& w, Chunk& 
     }
   } else {
     int tile = c;
-    if (p.itab) {
+    if (masked(p)) {
 #pragma unroll 1
       for (int j = 0; j < p.NI; ++j) {
         const int from = __shfl_sync(0xFFFFFFFFu, w.plan.from, j);
@@ -398,12 +414,17 @@ __device__ __forceinline__ void next_chunk(const DecodeArgs& a, Walk& w, Chunk& 
       k.key1 = k.key0 + 16;
       place0 = k.key0 >> log2_page;
       if (log2_page == 4 && place0 + 1 < pages) place1 = place0 + 1;
+      if (log2_page == 4 && p.window) {  // a page that lies behind the window is no longer the sequence's
+        const int start = window_start(p, w.plan.len);
+        if (k.key0 >= p.sinks && k.key1 <= start) place0 = -1;
+        if (k.key1 >= p.sinks && k.key1 + 16 <= start) place1 = -1;
+      }
     }
   }
   // visible keys are [st, en) of the intervals; without intervals, [0, len)
   const bool two = log2_page == 4;
   const int end0 = k.key0 + (two ? 16 : kTileKeys);
-  if (p.itab) {
+  if (masked(p)) {
 #pragma unroll 1
     for (int j = 0; j < p.NI; ++j) {
       const int st = __shfl_sync(0xFFFFFFFFu, w.plan.st, j), en = __shfl_sync(0xFFFFFFFFu, w.plan.en, j);
@@ -494,7 +515,7 @@ __device__ __forceinline__ int fetch(const DecodeArgs& a, const CUtensorMap* kma
         const bool second = log2_page == 4 && lane >= 16;
         const int key = second ? key1 + lane - 16 : key0 + lane;
         bool in = key < plan.len;
-        if (p.itab) {
+        if (masked(p)) {
           in = false;
 #pragma unroll 1
           for (int n = 0; n < p.NI; ++n) {
@@ -1314,8 +1335,16 @@ size_t decode_workspace_bytes(int, int H_q, int H_kv, int d) {
   return kMaxCtas * 16 + static_cast<size_t>(kMaxCtas) * 2 * heads_of(H_q / H_kv) * (d + 2) * 4;
 }
 
-static int64_t most_tiles(const DecodeParams& p) {
+static int64_t table_tiles(const DecodeParams& p) {
   return ((static_cast<int64_t>(p.sel ? p.sel_max : p.c.max_pages) << p.c.log2_page) + kTileKeys - 1) / kTileKeys;
+}
+
+static int64_t most_tiles(const DecodeParams& p) {
+  const int64_t room = table_tiles(p);
+  if (!p.window) return room;
+  // a window that starts inside a tile takes one more
+  const int64_t seen = (int64_t{p.sinks} + kTileKeys - 1) / kTileKeys + (int64_t{p.window} + kTileKeys - 1) / kTileKeys + 1;
+  return seen < room ? seen : room;
 }
 
 bool decode_fits(const DecodeParams& p) {

@@ -77,3 +77,16 @@ region seg_idx(i) % 2 == 0 : j >= i && j < seg_end_at(seg_idx(i) + 1)
 region seg_idx(i) % 2 == 1 : j == i
 """,
 }
+
+
+def sliding_window(window: int, sinks: int = 0) -> tuple[str, str]:
+    """(forward, backward) MaskSpec of a causal sliding window with a few first tokens that stay visible: row i
+    sees j < sinks and i - window < j <= i, the mask that cm_attn_decode_window applies to a generated token."""
+    if window < 1 or sinks < 0:
+        raise ValueError("window must be positive and sinks not negative")
+    if sinks == 0:
+        return (f"region all : j > i - {window} && j <= i", f"region all : j >= i && j < i + {window}")
+    return (f"region i < {window + sinks} : j <= i\n"
+            f"region all : j < {sinks} || (j > i - {window} && j <= i)",
+            f"region i < {sinks} : j >= i\n"
+            f"region all : j >= i && j < i + {window}")
