@@ -458,6 +458,57 @@ CM_API int cm_select_pages(const cm_kv_cache* cache, const cm_kv_seqs* seqs, con
  * or a copy itself failed). */
 CM_API int cm_kv_status(const cm_kv_cache* cache, void* stream);
 
+/* The pages of a pool and the page tables that are made of them, on the device: cm_kv_reserve takes pages
+ * for the tokens to come out of a list of free ones, cm_kv_release puts them back.  A step of a serving
+ * loop is reserve, append (cm_kv_append with n_new = granted), attention, release; nothing of it is read on the
+ * host, so it can be captured into one graph.
+ *   num_pages, page_size, B, max_pages  as in cm_kv_cache and cm_kv_seqs (same limits)
+ *   window, sinks  window 0: sequences keep all their pages until they end.  Else pages that hold no token
+ *                  which a token to come sees under cm_attn_decode_window(window, sinks) are given back.
+ *   page_table     device int32 [B][max_pages], as in cm_kv_seqs
+ *   free_pages     device int32 [num_pages]: the numbers of the free pages, as many as the state says
+ *   status         device int32: 0, or the first device error (cm_kv_pages_status)
+ * State, device int32 [B + 1][2], 8-byte aligned: for sequence b the pages {lo, hi} that it owns, which are the entries
+ * [0, f) and [max(lo, f), hi) of its row below hi, with f = ceil(sinks / page_size); in row B {free pages, 0}.  Both
+ * calls read `state` and write all of `new_state` (other memory); the next call goes on from there.  A new pool starts
+ * with all pages in free_pages, {0, 0} for every sequence and {num_pages, 0}. */
+typedef struct cm_kv_pages {
+  int32_t num_pages, page_size, B, max_pages, window, sinks;
+  int32_t* page_table;
+  int32_t* free_pages;
+  int32_t* status;
+} cm_kv_pages;
+
+/* Pages for the tokens that each sequence is about to append behind its lens[b], counted as in cm_kv_new
+ * (cu_new, n_new, n_tokens, max_new): its row gets the pages it lacks, from the end of the list, in
+ * the order of the sequences.  From the first sequence on for which too few are left, sequences that need a page get none.
+ *   granted  device int32 [B] (may be NULL; not lens, not n_new): the tokens that may be appended, all of a
+ *            sequence's or 0.
+ *   slots    device int64, [n_tokens] for packed tokens, [B][n_tokens] for padded ones (may be NULL): each new token's
+ *            place in the pool, page * page_size + row; -1 where none was granted.  Places of no token are left alone.
+ * A sequence whose length, token count or state is out of range (as in cm_kv_append; lo * page_size <= lens[b] <= hi *
+ * page_size, hi <= max_pages), and every sequence behind one at which cu_new falls, gets nothing, keeps its state and its slots are
+ * not written; a number in the list or the table
+ * that names no page becomes -1 in the row, and -1 in slots.  Both record CM_ERR_DEVICE_CHECK.  Entries of a row below hi are not changed, and
+ * entries of the list not at all. */
+CM_API int cm_kv_reserve(const cm_kv_pages* pages, const int32_t* state, int32_t* new_state,
+                         const int32_t* lens, const int32_t* cu_new, const int32_t* n_new, int n_tokens,
+                         int max_new, int32_t* granted, int64_t* slots, void* stream);
+
+/* Pages back into the list, behind its end, in the order of the sequences and of their rows: all that a sequence with
+ * done[b] != 0 owns (done: device int32 [B], may be NULL), and under a window, of the others, those that lie wholly
+ * before the position lens[b] - window but not among the first f.  The rows keep their entries, which
+ * are no longer the sequence's: a call that reads them reads what the page's new owner put there (attention under the same window does not).
+ * After its end a row of the table is ready for another sequence with lens[b] = 0.
+ * A sequence whose state is out of range keeps it and gives nothing back; a number that names no page goes into the list as it is
+ * (cm_kv_reserve will not hand it out), and pages beyond num_pages in the list are dropped; these record
+ * CM_ERR_DEVICE_CHECK. */
+CM_API int cm_kv_release(const cm_kv_pages* pages, const int32_t* state, int32_t* new_state,
+                         const int32_t* lens, const int32_t* done, void* stream);
+
+/* cm_kv_status of the pool's status word. */
+CM_API int cm_kv_pages_status(const cm_kv_pages* pages, void* stream);
+
 /* ---- status --------------------------------------------------------------------------------- */
 
 /* Wait for `stream`, then read desc->status: CM_OK, CM_ERR_TIMEOUT, CM_ERR_DEVICE_CHECK or

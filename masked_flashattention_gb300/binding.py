@@ -63,6 +63,13 @@ class cm_kv_seqs(ctypes.Structure):
                 ("page_table", ctypes.c_void_p), ("lens", ctypes.c_void_p)]
 
 
+class cm_kv_pages(ctypes.Structure):
+    _fields_ = [("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("B", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("window", ctypes.c_int32), ("sinks", ctypes.c_int32),
+                ("page_table", ctypes.c_void_p), ("free_pages", ctypes.c_void_p),
+                ("status", ctypes.c_void_p)]
+
+
 _Strides3 = ctypes.c_int64 * 3
 
 
@@ -130,6 +137,10 @@ def lib() -> ctypes.CDLL:
         L.cm_select_pages.argtypes = [cache_p, seqs_p, vp, i64_p, i32, i32, i32, vp, vp, i32,
                                       vp, sz, vp]
         L.cm_kv_status.argtypes = [cache_p, vp]
+        pages_p = ctypes.POINTER(cm_kv_pages)
+        L.cm_kv_reserve.argtypes = [pages_p, vp, vp, vp, vp, vp, i32, i32, vp, vp, vp]
+        L.cm_kv_release.argtypes = [pages_p, vp, vp, vp, vp, vp]
+        L.cm_kv_pages_status.argtypes = [pages_p, vp]
         L.cm_error_string.argtypes = [i32]
         L.cm_error_string.restype = ctypes.c_char_p
         _lib = L
@@ -549,8 +560,8 @@ _calls = None
 
 
 def _serving():
-    """(cm_kv_append, cm_attn_decode, cm_select_pages, cm_attn_decode_window) with every pointer as an
-    address or bytes."""
+    """(cm_kv_append, cm_attn_decode, cm_select_pages, cm_attn_decode_window, cm_kv_reserve, cm_kv_release)
+    with every pointer as an address or bytes."""
     global _calls
     if _calls is None:
         L, vp, i32, sz = lib(), ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
@@ -563,19 +574,22 @@ def _serving():
                        ctypes.c_float, vp, sz, vp),
                   call("cm_select_pages", vp, vp, vp, vp, i32, i32, i32, vp, vp, i32, vp, sz, vp),
                   call("cm_attn_decode_window", vp, vp, i32, i32, vp, vp, vp, vp, vp, i32,
-                       ctypes.c_float, vp, sz, vp))
+                       ctypes.c_float, vp, sz, vp),
+                  call("cm_kv_reserve", vp, vp, vp, vp, vp, vp, i32, i32, vp, vp, vp),
+                  call("cm_kv_release", vp, vp, vp, vp, vp, vp))
     return _calls
 
 
-def _kv_stream(cache: KVCache, stream) -> int:
+def _kv_stream(cache, stream) -> int:
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(cache.index)
     return _stream(stream)
 
 
-def _on_current_device(cache: KVCache):
+def _on_current_device(cache):
     if cache.index != torch._C._cuda_getDevice():
-        raise ValueError(f"the cache is on {cache.device}, which is not the current device")
+        what = "pool" if isinstance(cache, KVPages) else "cache"
+        raise ValueError(f"the {what} is on {cache.device}, which is not the current device")
 
 
 def _kv_seqs(cache: KVCache, page_table, lens):
@@ -772,6 +786,98 @@ def cm_kv_status(cache: KVCache, stream=None) -> int:
     return lib().cm_kv_status(ctypes.byref(cache.c), _kv_stream(cache, stream))
 
 
+class KVPages:
+    """The pages of a pool and their tables (cm_kv_pages) over the caller's tensors: page_table int32
+    [B, max_pages], free_pages int32 [num_pages].  window (None or 0: none) and sinks as in cm_attn_decode.  state and
+    spare, int32 [B + 1, 2], are what reserve_pages and release_pages go on from and write to; alloc makes
+    them, the low-level calls take their own."""
+
+    def __init__(self, page_table: torch.Tensor, free_pages: torch.Tensor, page_size: int,
+                 window: int | None = None, sinks: int = 0, state=None):
+        if not (page_table.is_cuda and page_table.dim() == 2 and free_pages.dim() == 1):
+            raise ValueError("page_table must be a CUDA tensor [B, max_pages], free_pages [num_pages]")
+        self.device, self.index = page_table.device, page_table.get_device()
+        self.B, self.max_pages = page_table.shape
+        _kv_tensor(page_table, "page_table", _I32, page_table.shape, self.index)
+        _kv_tensor(free_pages, "free_pages", _I32, free_pages.shape, self.index)
+        window = 0 if window is None else window
+        if not (0 <= window < 1 << 31 and 0 <= sinks < 1 << 31):
+            raise ValueError("window and sinks must be at least 0 and below 2^31")
+        self.page_table, self.free_pages = page_table, free_pages
+        self.page_size, self.window, self.sinks = page_size, window, sinks
+        self.num_pages = free_pages.shape[0]
+        self.state = self.spare = None
+        if state is not None:
+            _kv_tensor(state, "state", _I32, (self.B + 1, 2), self.index)
+            self.state, self.spare = state, torch.empty_like(state)
+        self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self.c = cm_kv_pages(self.num_pages, page_size, self.B, self.max_pages, window, sinks,
+                             page_table.data_ptr(), free_pages.data_ptr(), self.status.data_ptr())
+        self._address = ctypes.addressof(self.c)
+
+    @classmethod
+    def alloc(cls, num_pages: int, B: int, max_pages: int, page_size: int, window: int | None = None,
+              sinks: int = 0, device="cuda") -> "KVPages":
+        """A pool whose pages are all free, and tables (-1 throughout) of B sequences that own none."""
+        state = torch.zeros(B + 1, 2, dtype=torch.int32, device=device)
+        state[B, 0] = num_pages
+        return cls(torch.full((B, max_pages), -1, dtype=torch.int32, device=device),
+                   torch.arange(num_pages, dtype=torch.int32, device=device), page_size, window, sinks, state)
+
+
+def _pages_state(pages: KVPages, state, new_state, lens):
+    _on_current_device(pages)
+    dev, shape = pages.index, (pages.B + 1, 2)
+    _kv_tensor(state, "state", _I32, shape, dev)
+    _kv_tensor(new_state, "new_state", _I32, shape, dev)
+    _kv_tensor(lens, "lens", _I32, (pages.B,), dev)
+
+
+def cm_kv_reserve(pages: KVPages, state, new_state, lens, n_tokens: int, max_new: int | None = None,
+                  cu_new=None, n_new=None, granted=None, slots=None, stream=None) -> None:
+    """Pages out of the pool for the tokens that each sequence is about to append behind its lens[b]: packed ones
+    (cu_new int32 [B + 1]; n_tokens of all sequences) or padded ones (n_new int32 [B] of n_tokens each, all of
+    them where it is not given).  max_new: the most tokens of any sequence (default n_tokens).  granted
+    (int32 [B]): the tokens that may be appended, all of a sequence's or 0.  slots (int64 [n_tokens], padded [B,
+    n_tokens]): page * page_size + row of every token, -1 where none was granted.  state and new_state: int32
+    [B + 1, 2]."""
+    _pages_state(pages, state, new_state, lens)
+    dev, B = pages.index, pages.B
+    if cu_new is not None:
+        _kv_tensor(cu_new, "cu_new", _I32, (B + 1,), dev)
+    if n_new is not None:
+        _kv_tensor(n_new, "n_new", _I32, (B,), dev)
+    if granted is not None:
+        _kv_tensor(granted, "granted", _I32, (B,), dev)
+    if slots is not None:
+        _kv_tensor(slots, "slots", torch.int64, (B, n_tokens) if cu_new is None else (n_tokens,), dev)
+    if not (0 <= n_tokens < 1 << 31 and (max_new is None or 0 <= max_new < 1 << 31)):
+        raise ValueError("n_tokens and max_new must be at least 0 and below 2^31")
+    rc = _serving()[4](pages._address, state.data_ptr(), new_state.data_ptr(), lens.data_ptr(), _ptr(cu_new),
+                       _ptr(n_new), n_tokens, n_tokens if max_new is None else max_new, _ptr(granted),
+                       _ptr(slots) if n_tokens else None, _kv_stream(pages, stream))
+    if rc != CM_OK:
+        raise CMError(rc, "cm_kv_reserve")
+
+
+def cm_kv_release(pages: KVPages, state, new_state, lens, done=None, stream=None) -> None:
+    """Pages back into the pool: all of the sequences with done[b] != 0 (int32 [B]), and of the others those that
+    lie behind the pool's window.  state and new_state: int32 [B + 1, 2]."""
+    _pages_state(pages, state, new_state, lens)
+    if done is not None:
+        _kv_tensor(done, "done", _I32, (pages.B,), pages.index)
+    rc = _serving()[5](pages._address, state.data_ptr(), new_state.data_ptr(), lens.data_ptr(), _ptr(done),
+                       _kv_stream(pages, stream))
+    if rc != CM_OK:
+        raise CMError(rc, "cm_kv_release")
+
+
+def cm_kv_pages_status(pages: KVPages, stream=None) -> int:
+    """The first device error since the last call (CM_OK where there was none); zeroes it."""
+    _on_current_device(pages)
+    return lib().cm_kv_pages_status(ctypes.byref(pages.c), _kv_stream(pages, stream))
+
+
 def _for_stream(stream, make):
     """make()'s tensors for work on `stream`: new ones from its memory, where nothing that the current
     stream still does can write, and all kept from reuse until both streams have done with them."""
@@ -823,3 +929,35 @@ def select_pages(cache: KVCache, page_table, lens, q, n: int, keep_first: int = 
     sel, nsel, workspace = _for_stream(stream, make)
     cm_select_pages(cache, page_table, lens, q, sel, nsel, workspace, keep_first, keep_last, stream)
     return sel, nsel
+
+
+def _turn(pages: KVPages) -> None:
+    pages.state, pages.spare = pages.spare, pages.state
+
+
+def reserve_pages(pages: KVPages, lens, n_tokens: int, max_new: int | None = None, cu_new=None, n_new=None,
+                  slots: bool = False, stream=None):
+    """cm_kv_reserve from the pool's own state, with results in new tensors: granted, or (granted, slots).  The state turns
+    to the other of its two buffers; a captured graph should hold as many reserve_pages as release_pages, so
+    that every replay goes on where the one before ended."""
+    if pages.state is None:
+        raise ValueError("the pool was made without a state")
+    shape = (pages.B, n_tokens) if cu_new is None else (n_tokens,)
+
+    def make():
+        made = (torch.empty(pages.B, dtype=torch.int32, device=pages.device),)
+        return made + ((torch.full(shape, -1, dtype=torch.int64, device=pages.device),) if slots else ())
+
+    made = _for_stream(stream, make)
+    cm_kv_reserve(pages, pages.state, pages.spare, lens, n_tokens, max_new, cu_new, n_new, made[0],
+                  made[1] if slots else None, stream)
+    _turn(pages)
+    return made if slots else made[0]
+
+
+def release_pages(pages: KVPages, lens, done=None, stream=None) -> None:
+    """cm_kv_release from the pool's own state (see reserve_pages)."""
+    if pages.state is None:
+        raise ValueError("the pool was made without a state")
+    cm_kv_release(pages, pages.state, pages.spare, lens, done, stream)
+    _turn(pages)

@@ -18,7 +18,7 @@ LIB = os.path.join(HERE, "libcm.so")
 
 SOURCES = ["compiler.cpp", "codegen.cpp", "preprocess.cu", "attn_fwd.cu", "attn_bwd.cu", "attn_dq.cu", "api.cu",
            "attn_bwd_noalloc.cu", "kv_append.cu", "attn_decode.cu", "select_pages.cu",
-           "api_decode.cu"]
+           "kv_pages.cu", "api_decode.cu"]
 HEADERS = ["program.h", "kernels.h", "ptx.cuh", "tma_host.h", "descriptor_core.cuh", "mask.cuh",
            "kv_cache.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

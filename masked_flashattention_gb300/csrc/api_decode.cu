@@ -70,6 +70,8 @@ bool same_strides(const int64_t* a, const int64_t* b) {
   return a[0] == b[0] && a[1] == b[1] && a[2] == b[2];
 }
 
+int log2_page(int page_size) { return page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7; }
+
 cm::KvView view(const cm_kv_cache* c, const cm_kv_seqs* s) {
   cm::KvView v;
   const int item = c->dtype == CM_KV_E4M3 ? 1 : 2;
@@ -85,7 +87,7 @@ cm::KvView view(const cm_kv_cache* c, const cm_kv_seqs* s) {
   v.table = s->page_table;
   v.lens = s->lens;
   v.num_pages = c->num_pages;
-  v.log2_page = c->page_size == 16 ? 4 : c->page_size == 32 ? 5 : c->page_size == 64 ? 6 : 7;
+  v.log2_page = log2_page(c->page_size);
   v.H_kv = c->H_kv;
   v.d = c->d;
   v.e4m3 = c->dtype == CM_KV_E4M3;
@@ -99,6 +101,47 @@ cm::Strides strides3(const int64_t* s) { return {s[0], s[1], s[2]}; }
 int check_heads(int H_q, int H_kv) {
   if (H_q < 1 || H_q % H_kv != 0) return CM_ERR_INVALID_ARG;
   return H_q > kMaxHeads ? CM_ERR_UNSUPPORTED : CM_OK;
+}
+
+int check_pages(const cm_kv_pages* g, const int32_t* state, const int32_t* new_state, const int32_t* lens,
+                cm::PagesParams& p) {
+  if (!g || g->num_pages < 1 || g->B < 1 || g->max_pages < 1 || g->window < 0 || g->sinks < 0)
+    return CM_ERR_INVALID_ARG;
+  if (g->page_size != 16 && g->page_size != 32 && g->page_size != 64 && g->page_size != 128)
+    return CM_ERR_UNSUPPORTED;
+  if (g->B > kMaxB || static_cast<int64_t>(g->max_pages) * g->page_size > (1LL << 27))
+    return CM_ERR_UNSUPPORTED;
+  if (!good_ints(g->page_table) || !good_ints(g->free_pages) || !good_ints(g->status) || !good_ints(lens))
+    return CM_ERR_INVALID_ARG;
+  if (!state || !new_state || state == new_state || !aligned(state, 8) || !aligned(new_state, 8))
+    return CM_ERR_INVALID_ARG;
+  p = {};
+  p.page_table = g->page_table;
+  p.free_pages = g->free_pages;
+  p.status = g->status;
+  p.state = reinterpret_cast<const int2*>(state);
+  p.new_state = reinterpret_cast<int2*>(const_cast<int32_t*>(new_state));
+  p.lens = lens;
+  p.num_pages = g->num_pages;
+  p.log2_page = log2_page(g->page_size);
+  p.B = g->B;
+  p.max_pages = g->max_pages;
+  p.window = g->window;
+  p.sinks = g->sinks;
+  return CM_OK;
+}
+
+// Waits for the stream, then reads a status word and zeroes it.
+int read_status(int32_t* status, void* stream) {
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int32_t v = 0;
+  if (cudaMemcpyAsync(&v, status, 4, cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+      cudaStreamSynchronize(st) != cudaSuccess)
+    return CM_ERR_CUDA;
+  if (v == 0) return CM_OK;
+  if (cudaMemsetAsync(status, 0, 4, st) != cudaSuccess || cudaStreamSynchronize(st) != cudaSuccess)
+    return CM_ERR_CUDA;
+  return (v >> 16) == cm::kDevTimeout ? CM_ERR_TIMEOUT : CM_ERR_DEVICE_CHECK;
 }
 
 // What the two attention entry points share: their tensors checked, and put into p.
@@ -300,16 +343,43 @@ CM_API int cm_select_pages(const cm_kv_cache* cache, const cm_kv_seqs* seqs, con
 
 CM_API int cm_kv_status(const cm_kv_cache* cache, void* stream) {
   if (!cache || !good_ints(cache->status)) return CM_ERR_INVALID_ARG;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  int32_t v = 0;
-  if (cudaMemcpyAsync(&v, cache->status, 4, cudaMemcpyDeviceToHost, st) != cudaSuccess ||
-      cudaStreamSynchronize(st) != cudaSuccess)
-    return CM_ERR_CUDA;
-  if (v == 0) return CM_OK;
-  if (cudaMemsetAsync(cache->status, 0, 4, st) != cudaSuccess ||
-      cudaStreamSynchronize(st) != cudaSuccess)
-    return CM_ERR_CUDA;
-  return (v >> 16) == cm::kDevTimeout ? CM_ERR_TIMEOUT : CM_ERR_DEVICE_CHECK;
+  return read_status(cache->status, stream);
+}
+
+CM_API int cm_kv_reserve(const cm_kv_pages* pages, const int32_t* state, int32_t* new_state,
+                         const int32_t* lens, const int32_t* cu_new, const int32_t* n_new, int n_tokens,
+                         int max_new, int32_t* granted, int64_t* slots, void* stream) {
+  cm::PagesParams p;
+  const int rc = check_pages(pages, state, new_state, lens, p);
+  if (rc != CM_OK) return rc;
+  if (n_tokens < 0 || max_new < 0 || max_new > n_tokens) return CM_ERR_INVALID_ARG;
+  if (cu_new ? (n_new || !good_ints(cu_new)) : (n_new && !good_ints(n_new))) return CM_ERR_INVALID_ARG;
+  if (!cu_new && !n_new && max_new != n_tokens) return CM_ERR_INVALID_ARG;
+  if ((granted && !good_ints(granted)) || (slots && !aligned(slots, 8))) return CM_ERR_INVALID_ARG;
+  if (granted == lens || (granted && granted == n_new)) return CM_ERR_INVALID_ARG;
+  if ((cu_new ? n_tokens : static_cast<int64_t>(p.B) * max_new) > (1LL << 30)) return CM_ERR_UNSUPPORTED;
+  p.cu_new = cu_new;
+  p.n_new = n_new;
+  p.n_tokens = n_tokens;
+  p.max_new = max_new;
+  p.granted = granted;
+  p.slots = slots;
+  return cm::launch_kv_reserve(p, static_cast<cudaStream_t>(stream)) == 0 ? CM_OK : CM_ERR_CUDA;
+}
+
+CM_API int cm_kv_release(const cm_kv_pages* pages, const int32_t* state, int32_t* new_state,
+                         const int32_t* lens, const int32_t* done, void* stream) {
+  cm::PagesParams p;
+  const int rc = check_pages(pages, state, new_state, lens, p);
+  if (rc != CM_OK) return rc;
+  if (done && !good_ints(done)) return CM_ERR_INVALID_ARG;
+  p.done = done;
+  return cm::launch_kv_release(p, static_cast<cudaStream_t>(stream)) == 0 ? CM_OK : CM_ERR_CUDA;
+}
+
+CM_API int cm_kv_pages_status(const cm_kv_pages* pages, void* stream) {
+  if (!pages || !good_ints(pages->status)) return CM_ERR_INVALID_ARG;
+  return read_status(pages->status, stream);
 }
 
 }  // extern "C"

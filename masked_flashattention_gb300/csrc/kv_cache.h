@@ -79,6 +79,24 @@ struct SelectParams {
 __host__ __device__ constexpr int score_pitch(int max_pages) { return (max_pages + 3) & ~3; }
 int launch_select_pages(const SelectParams& p, cudaStream_t stream);
 
+// A pool's pages and their tables (cm_kv_pages), and one call's arguments.
+struct PagesParams {
+  int32_t* page_table;     // [B][max_pages]
+  int32_t* free_pages;     // [num_pages]
+  int32_t* status;
+  const int2* state;       // [B + 1]: own pages {lo, hi} of a sequence; {free pages, 0}
+  int2* new_state;
+  const int32_t* lens;     // [B]
+  const int32_t *cu_new, *n_new;
+  const int32_t* done;     // [B] or nullptr
+  int32_t* granted;        // [B] or nullptr
+  int64_t* slots;          // [n_tokens] or [B][n_tokens], or nullptr
+  int num_pages, log2_page, B, max_pages, window, sinks;
+  int n_tokens, max_new;
+};
+int launch_kv_reserve(const PagesParams& p, cudaStream_t stream);
+int launch_kv_release(const PagesParams& p, cudaStream_t stream);
+
 // Launches that follow one another in a serving step (append, scores, selection, attention, joining)
 // are a few microseconds each: every kernel lets the next one's blocks start early and waits for
 // the one before it to complete, memory included, before it reads or writes anything in memory.
