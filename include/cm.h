@@ -307,6 +307,8 @@ CM_API int cm_attn_bwd_noalloc(const cm_descriptor* desc, const void* q, const v
 
 #define CM_KV_BF16 0
 #define CM_KV_E4M3 1
+#define CM_KV_E4M3_BLOCK 2
+#define CM_KV_INT8_BLOCK 3
 
 /* The cache.  All pointers are device memory of the caller, 16-byte aligned but the scales, the
  * summary scales and the status word (4 bytes).
@@ -314,7 +316,11 @@ CM_API int cm_attn_bwd_noalloc(const cm_descriptor* desc, const void* q, const v
  *                positive fp32 scale per head (value = stored * scale).  Pages may lie apart:
  *                page n starts at n * k_page_stride (v_page_stride) elements, a multiple of 16
  *                bytes and at least H_kv * page_size * d.
- *   k_scale, v_scale  fp32 [H_kv]; e4m3 only, NULL for bf16.
+ *                CM_KV_E4M3_BLOCK and CM_KV_INT8_BLOCK: e4m3, or whole numbers in 8 bits, with a scale for each
+ *                block of 16 consecutive tokens (those of a page from a multiple of 16 on) and head.
+ *   k_scale, v_scale  fp32 [H_kv] for CM_KV_E4M3, fp32 [num_pages][H_kv][page_size / 16] for the block types
+ *                (written by cm_kv_append: positive powers of two within 2^-32 .. 2^32; any other number there counts as
+ *                the power of two that its exponent says, held to that range), NULL for bf16.
  *   summary      int8 [num_pages][H_kv][2][d] and summary_scale fp32 [num_pages][H_kv], both or
  *                neither (NULL): per page, head and channel the largest key, then the smallest,
  *                over the tokens the page holds, in units of summary_scale.  With a = the largest
@@ -383,6 +389,13 @@ typedef struct cm_kv_new {
  * and rounded to bf16, its key and value stored in the cache (e4m3: the bf16 value divided by the
  * head's scale, rounded to nearest, held to +-448), and the summaries of the pages it touches
  * are made anew from all the tokens these then hold.  lens is read only.
+ * Block types: with a the largest magnitude of a call's new keys (values) in a block (NaN passed over), 2^e is the
+ * smallest power of two with a <= 448 * 2^e (e4m3) or a <= 127 * 2^e (int8), e held to [-32, 32].  A block without
+ * earlier tokens (none at a position below lens[b]) gets it as its scale; one that has some gets the larger of it and its
+ * own, and where that is larger its earlier tokens become round(stored * old / new).  New tokens are stored as
+ * round(x / scale), held to +-448 or +-127; halves go to even; a NaN is kept by e4m3 and becomes 0 in int8.  So what
+ * a block holds depends on how many calls its tokens came in, by these roundings alone.  No calibration goes before, and an outlier
+ * costs 16 tokens of one head their precision.
  * A sequence whose length or token count is out of range (lens[b] < 0, more than max_new tokens,
  * tokens outside n_tokens, positions past the table or rope_len) appends nothing (new_lens[b] =
  * lens[b]), and tokens of a page outside the pool are left out (their q_out and k_out are written);

@@ -477,11 +477,14 @@ def attention_backward(desc: Descriptor, q, k, v, o, lse, d_o, scale=None, strea
 # ------------------------------------------------------------------------------------------------
 CM_KV_BF16 = 0
 CM_KV_E4M3 = 1
+CM_KV_E4M3_BLOCK = 2
+CM_KV_INT8_BLOCK = 3
+KV_BLOCK = 16  # tokens that share a scale in a block type
 
 
 def _pool(t: torch.Tensor, name: str):
-    if not (t.is_cuda and t.dim() == 4 and t.dtype in (torch.bfloat16, torch.float8_e4m3fn)):
-        raise ValueError(f"{name} must be a bf16 or float8_e4m3fn CUDA tensor "
+    if not (t.is_cuda and t.dim() == 4 and t.dtype in (torch.bfloat16, torch.float8_e4m3fn, torch.int8)):
+        raise ValueError(f"{name} must be a bf16, float8_e4m3fn or int8 CUDA tensor "
                          "[num_pages, H_kv, page_size, d]")
     n, H, P, d = t.shape
     if t[:1].is_contiguous() and (n == 1 or t.stride(0) >= H * P * d):
@@ -491,8 +494,9 @@ def _pool(t: torch.Tensor, name: str):
 
 class KVCache:
     """A paged key-value cache over the caller's tensors (cm_kv_cache): k, v
-    [num_pages, H_kv, page_size, d], bf16 or float8_e4m3fn; e4m3 takes k_scale and v_scale, fp32
-    [H_kv].  Pages may lie apart (a view such as kv[:, 0] of a [num_pages, 2, H_kv, page_size, d]
+    [num_pages, H_kv, page_size, d], bf16, float8_e4m3fn or int8; the 8-bit types take k_scale and v_scale,
+    fp32 [num_pages, H_kv, page_size / 16] (a power of two for each block of 16 tokens and head, which
+    cm_kv_append chooses), or for e4m3 fp32 [H_kv] (fixed by the caller).  Pages may lie apart (a view such as kv[:, 0] of a [num_pages, 2, H_kv, page_size, d]
     tensor).  summary (int8 [num_pages, H_kv, 2, d]) with summary_scale (fp32 [num_pages, H_kv])
     holds the page summaries that cm_select_pages reads."""
 
@@ -504,12 +508,15 @@ class KVCache:
             raise ValueError("v must have the shape, type and device of k")
         n, H, P, d = shape
         self.device, self.index = k.device, k.get_device()
-        e4m3 = k.dtype == torch.float8_e4m3fn
+        bits8 = k.dtype != torch.bfloat16
+        blocks = k.dtype == torch.int8 or (bits8 and k_scale is not None and k_scale.dim() == 3)
         for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-            if (t is not None) != e4m3:
-                raise ValueError("an e4m3 cache takes k_scale and v_scale, a bf16 cache neither")
-            if e4m3:
-                _kv_tensor(t, name, torch.float32, (H,), self.index)
+            if (t is not None) != bits8:
+                raise ValueError("an 8-bit cache takes k_scale and v_scale, a bf16 cache neither")
+            if bits8:
+                _kv_tensor(t, name, torch.float32, (n, H, P // KV_BLOCK) if blocks else (H,), self.index)
+        dtype = (CM_KV_BF16 if not bits8 else CM_KV_E4M3 if not blocks
+                 else CM_KV_INT8_BLOCK if k.dtype == torch.int8 else CM_KV_E4M3_BLOCK)
         if (summary is None) != (summary_scale is None):
             raise ValueError("summary and summary_scale come together")
         if summary is not None:
@@ -520,17 +527,23 @@ class KVCache:
         self.num_pages, self.H_kv, self.page_size, self.d = n, H, P, d
         self.scale = 1.0 / math.sqrt(d)  # of scores, where a call names none
         self.status = torch.zeros(1, dtype=torch.int32, device=k.device)
-        self.c = cm_kv_cache(n, P, H, d, CM_KV_E4M3 if e4m3 else CM_KV_BF16, k_stride, v_stride,
+        self.c = cm_kv_cache(n, P, H, d, dtype, k_stride, v_stride,
                              k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale),
                              _ptr(summary), _ptr(summary_scale), self.status.data_ptr())
         self._address = ctypes.addressof(self.c)
 
     @classmethod
     def alloc(cls, num_pages: int, H_kv: int, page_size: int, d: int, dtype=torch.bfloat16,
-              device="cuda", k_scale=None, v_scale=None, summaries: bool = False) -> "KVCache":
-        """A cache in new memory (not initialised: what no token was written to is never used)."""
+              device="cuda", k_scale=None, v_scale=None, summaries: bool = False,
+              block_scales: bool = False) -> "KVCache":
+        """A cache in new memory (not initialised: what no token was written to is never used).  int8, and e4m3 with
+        block_scales, come with scales of their own."""
         k, v = (torch.empty(num_pages, H_kv, page_size, d, dtype=dtype, device=device)
                 for _ in range(2))
+        if block_scales or dtype == torch.int8:
+            if k_scale is not None or v_scale is not None:
+                raise ValueError("block scales are the cache's own")
+            k_scale, v_scale = (torch.empty(num_pages, H_kv, page_size // KV_BLOCK, device=device) for _ in range(2))
         more = {}
         if summaries:
             more = {"summary": torch.empty(num_pages, H_kv, 2, d, dtype=torch.int8, device=device),

@@ -18,21 +18,21 @@ bool good_ints(const void* p) { return p && aligned(p, 4); }
 
 int check_cache(const cm_kv_cache* c) {
   if (!c || c->num_pages < 1 || c->H_kv < 1) return CM_ERR_INVALID_ARG;
-  if (c->dtype != CM_KV_BF16 && c->dtype != CM_KV_E4M3) return CM_ERR_INVALID_ARG;
+  if (c->dtype < CM_KV_BF16 || c->dtype > CM_KV_INT8_BLOCK) return CM_ERR_INVALID_ARG;
   if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
     return CM_ERR_UNSUPPORTED;
   if ((c->d != 64 && c->d != 128) || c->H_kv > 1024) return CM_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(c->num_pages) * c->H_kv >= (1LL << 40) / c->page_size)
     return CM_ERR_UNSUPPORTED;
   if (!good_ptr(c->k) || !good_ptr(c->v) || !good_ints(c->status)) return CM_ERR_INVALID_ARG;
-  const int item = c->dtype == CM_KV_E4M3 ? 1 : 2;
+  const int item = c->dtype == CM_KV_BF16 ? 2 : 1;
   const int64_t page = static_cast<int64_t>(c->H_kv) * c->page_size * c->d;
   for (const int64_t s : {c->k_page_stride, c->v_page_stride}) {
     if (s < page || (s * item) % 16 != 0) return CM_ERR_INVALID_ARG;
     if (s >= (1LL << 38)) return CM_ERR_UNSUPPORTED;  // strides of a tensor map end at 2^40 bytes
   }
-  if (c->dtype == CM_KV_E4M3 ? !(good_ints(c->k_scale) && good_ints(c->v_scale))
-                             : (c->k_scale || c->v_scale))
+  if (c->dtype == CM_KV_BF16 ? (c->k_scale || c->v_scale)
+                             : !(good_ints(c->k_scale) && good_ints(c->v_scale)))
     return CM_ERR_INVALID_ARG;
   if ((c->summary != nullptr) != (c->summary_scale != nullptr)) return CM_ERR_INVALID_ARG;
   if (c->summary && (!good_ptr(c->summary) || !good_ints(c->summary_scale)))
@@ -74,7 +74,7 @@ int log2_page(int page_size) { return page_size == 16 ? 4 : page_size == 32 ? 5 
 
 cm::KvView view(const cm_kv_cache* c, const cm_kv_seqs* s) {
   cm::KvView v;
-  const int item = c->dtype == CM_KV_E4M3 ? 1 : 2;
+  const int item = c->dtype == CM_KV_BF16 ? 2 : 1;
   v.k = static_cast<char*>(c->k);
   v.v = static_cast<char*>(c->v);
   v.k_page_bytes = c->k_page_stride * item;
@@ -90,7 +90,7 @@ cm::KvView view(const cm_kv_cache* c, const cm_kv_seqs* s) {
   v.log2_page = log2_page(c->page_size);
   v.H_kv = c->H_kv;
   v.d = c->d;
-  v.e4m3 = c->dtype == CM_KV_E4M3;
+  v.kind = c->dtype;
   v.B = s->B;
   v.max_pages = s->max_pages;
   return v;

@@ -50,8 +50,8 @@ constexpr float kRenew = 8.f;       // log2 units a score may pass the maximum b
 // it, no weight is beyond 1, and O stays within fp32 where the sum of |v| does (with weights up to 2^8,
 // values of 2^118 overflowed).  fp16 weights reach up to 2^(8 + 7), and what fp16 cannot hold is below 2^-32 of the
 // largest: with 2^8, a million keys of 2^-25 each beside one large one lost 3 % of the sum.
-template <bool E4M3>
-constexpr float kLift = E4M3 ? 7.f : -kRenew;
+template <int KIND>
+constexpr float kLift = KIND != kBf16 ? 7.f : -kRenew;
 constexpr size_t kSmemMax = 232448;
 
 // flags of a tile
@@ -65,9 +65,9 @@ constexpr int kFlagBits = 4;  // above them: the CTAs that hold parts of the row
 // The smaller rows take more instructions a byte, so 8 pairs share the ring's memory (one computing warp
 // a scheduler left an e4m3 cache at 47 % of the bandwidth).  Their 16 warps start with 128 registers a thread and
 // trade: 184 for a computing warp, 72 for a fetching one.
-template <int D, bool E4M3, int NB>
+template <int D, int KIND, int NB>
 struct Cfg {
-  static constexpr int kItem = E4M3 ? 1 : 2;
+  static constexpr int kItem = KIND == kBf16 ? 2 : 1;
   static constexpr int kRowBytes = D * kItem;
   static constexpr int kPairs = kRowBytes == 256 ? 4 : 8;  // warp pairs of a CTA
   static constexpr int kThreads = 64 * kPairs;
@@ -91,7 +91,9 @@ struct Cfg {
   static constexpr int kOffBars = kOffMeta + kPairs * kStages * 16;
   static constexpr int kOffHead = kOffBars + kPairs * kStages * 16;   // int4 per piece
   static constexpr int kOffMisc = kOffHead + 2 * kPairs * 16;         // starts, counts, abort flag
+  static constexpr int kOffExps = kOffMisc + 64;                      // a word a stage: exponents of its blocks' scales
   static constexpr int kSmem = kOffMisc + 256;
+  static_assert(KIND < kE4m3Block || kPairs * kStages * 4 <= 256 - 64, "the exponents lie behind the abort flag");
   static_assert(kStages >= 2 && kSmem <= static_cast<int>(kSmemMax), "shared memory");
   static_assert(kOffPiece % 16 == 0 && kPiece % 16 == 0 && kOffMeta % 16 == 0, "alignment");
   static_assert(kPairs * kPiece >= (3 * kThreads + kThreads / 32) * 4, "the search borrows the pieces' memory");
@@ -182,16 +184,24 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// two e4m3 (the low or the high half of x) as fp16x2, exact
-__device__ __forceinline__ uint32_t widen_lo(uint32_t x) {
-  uint32_t y;
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(y) : "r"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t widen_hi(uint32_t x) {
-  uint32_t y;
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(y) : "r"(x));
-  return y;
+// Two of the four 8-bit numbers of x as fp16x2, exact: bytes 0 and 1, or 2 and 3; ODD: bytes 0 and 2, or 1 and 3.
+// A whole number n is the fp16 1024 + (n + 128), whose bits are 0x6400 + (n + 128), less 1152.
+template <int KIND, bool ODD = false>
+__device__ __forceinline__ void widen(uint32_t x, uint32_t& lo, uint32_t& hi) {
+  if constexpr (KIND == kInt8Block) {
+    x ^= 0x80808080u;
+    const __half2 less = __half2half2(__ushort_as_half(0x6480));
+    const uint32_t a = __byte_perm(x, 0x64646464u, ODD ? 0x4240 : 0x4140);
+    const uint32_t b = __byte_perm(x, 0x64646464u, ODD ? 0x4341 : 0x4342);
+    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&a), less), z = __hsub2(*reinterpret_cast<const __half2*>(&b), less);
+    lo = *reinterpret_cast<const uint32_t*>(&y);
+    hi = *reinterpret_cast<const uint32_t*>(&z);
+  } else {
+    if constexpr (ODD) x = __byte_perm(x, 0, 0x3120);
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(x));
+  }
 }
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int32_t x, int32_t y,
                                             int32_t z, uint32_t bar) {
@@ -323,6 +333,7 @@ struct Chunk {
   int h;                 // key-value head
   int page0, page1;      // pages of the tile (page1: second half of a tile of two 16-key pages); -1: none
   int key0, key1;        // first keys of these
+  uint32_t k0, k1, v0, v1;  // scales of their two blocks of 16 keys, as they lie in memory
   bool full;             // every key of the tile is visible
   bool whole;            // the chunk is a whole row
 };
@@ -334,7 +345,21 @@ struct Walk {
   Plan plan;
 };
 
-template <int D>
+// Scales of the chunk's tiles, for its key-value head: asked for once the page numbers are there, and not looked at
+// before the chunk is fetched.
+__device__ __forceinline__ void load_scales(const DecodeParams& p, Chunk& k) {
+  const int log2_page = p.c.log2_page, per = log2_page - 4, block = (k.key0 & ((1 << log2_page) - 1)) >> 4;
+  const bool two = log2_page == 4;
+  const int64_t at0 = ((static_cast<int64_t>(k.page0) * p.c.H_kv + k.h) << per) + block;
+  const int64_t at1 = two ? static_cast<int64_t>(k.page1) * p.c.H_kv + k.h : at0 + 1;
+  const bool in0 = k.page0 >= 0, in1 = two ? k.page1 >= 0 : in0;
+  k.k0 = in0 ? __float_as_uint(p.c.k_scale[at0]) : 0u;
+  k.v0 = in0 ? __float_as_uint(p.c.v_scale[at0]) : 0u;
+  k.k1 = in1 ? __float_as_uint(p.c.k_scale[at1]) : 0u;
+  k.v1 = in1 ? __float_as_uint(p.c.v_scale[at1]) : 0u;
+}
+
+template <int D, int KIND>
 __device__ __forceinline__ void next_chunk(const DecodeArgs& a, Walk& w, Chunk& k, int lane) {
   if (w.c >= w.plan.tiles) {  // next row
     w.pos += kRowCost - (w.c - w.plan.tiles);
@@ -346,6 +371,7 @@ __device__ __forceinline__ void next_chunk(const DecodeArgs& a, Walk& w, Chunk& 
         k.h = row_index(a, k.row).h;
         k.n = w.c = w.plan.tiles;
         w.pos += k.n;
+        if constexpr (KIND >= kE4m3Block) load_scales(a.p, k);
         return;
       }
     } else if (w.pos < w.end) {  // next unit that has tiles: there is one, or the run would have ended
@@ -444,6 +470,7 @@ __device__ __forceinline__ void next_chunk(const DecodeArgs& a, Walk& w, Chunk& 
     if (static_cast<unsigned>(k.page1) >= static_cast<unsigned>(p.c.num_pages)) k.page1 = -1;
     k.full = false;
   }
+  if constexpr (KIND >= kE4m3Block) load_scales(p, k);
   w.c += k.n;
   w.pos += k.n;
 }
@@ -473,15 +500,23 @@ __device__ __forceinline__ bool warp_wait(const WaitCtl& w, uint32_t bar, uint32
   return __all_sync(0xFFFFFFFFu, got);
 }
 
+// Exponents of a tile's block scales (keys' two, then values' two), a byte each.
+__device__ __forceinline__ uint32_t pack_exponents(uint32_t k0, uint32_t k1, uint32_t v0, uint32_t v1) {
+  const uint32_t a = __byte_perm(block_exponent(k0), block_exponent(k1), 0x0040);
+  const uint32_t b = __byte_perm(block_exponent(v0), block_exponent(v1), 0x0040);
+  return __byte_perm(a, b, 0x5410);
+}
+__device__ __forceinline__ int exponent_at(uint32_t word, int i) { return static_cast<int8_t>(word >> (8 * i)); }
+
 // ---- fetching warp ------------------------------------------------------------------------------
 // Returns the tiles fetched; `rest` is the first of them whose copy the computing warp need not have
 // waited for, were it to give up.
-template <int D, bool E4M3, int NB>
+template <int D, int KIND, int NB>
 __device__ __forceinline__ int fetch(const DecodeArgs& a, const CUtensorMap* kmap,
                                      const CUtensorMap* vmap, Walk w, uint32_t ring,
-                                     uint32_t meta, uint32_t bars, int run, const WaitCtl& wait,
+                                     uint32_t meta, uint32_t bars, uint32_t exps, int run, const WaitCtl& wait,
                                      int lane, int& rest) {
-  using C = Cfg<D, E4M3, NB>;
+  using C = Cfg<D, KIND, NB>;
   const DecodeParams& p = a.p;
   const int log2_page = p.c.log2_page, P = 1 << log2_page;
   const int depth = a.whole_rows ? C::kStages : C::kSteady;
@@ -489,7 +524,7 @@ __device__ __forceinline__ int fetch(const DecodeArgs& a, const CUtensorMap* kma
   const int begin = w.pos, end = w.end;
   Chunk next;
   next.whole = false;
-  next_chunk<D>(a, w, next, lane);
+  next_chunk<D, KIND>(a, w, next, lane);
   bool ok = true;
   while (next.n > 0 && ok) {
     const Chunk cur = next;
@@ -499,7 +534,7 @@ __device__ __forceinline__ int fetch(const DecodeArgs& a, const CUtensorMap* kma
     const int parts = row_begin < begin || row_begin + plan.tiles > end
                           ? (row_begin + plan.tiles - 1) / run - row_begin / run + 1
                           : 1;
-    next_chunk<D>(a, w, next, lane);  // its loads are on their way while cur is fetched
+    next_chunk<D, KIND>(a, w, next, lane);  // its loads are on their way while cur is fetched
     for (int j = 0; j < cur.n; ++j) {
       const int stage = issued % C::kStages;
       const uint32_t full = bars + stage * 16;
@@ -525,8 +560,14 @@ __device__ __forceinline__ int fetch(const DecodeArgs& a, const CUtensorMap* kma
         }
         seen = __ballot_sync(0xFFFFFFFFu, in && (second ? page1 : page0) >= 0);
       }
+      uint32_t scales = 0;
+      if constexpr (KIND >= kE4m3Block) {
+        const uint32_t mine = pack_exponents(cur.k0, cur.k1, cur.v0, cur.v1);
+        scales = __shfl_sync(0xFFFFFFFFu, mine, j);
+      }
       if (lane == 0) {
         const int c = cur.c0 + j;
+        if constexpr (KIND >= kE4m3Block) asm volatile("st.shared.b32 [%0], %1;" ::"r"(exps + stage * 4), "r"(scales) : "memory");
         int flags = 0;
         if (c == 0) flags |= kFirst | kStarts;
         if (at + j == begin) flags |= kFirst;
@@ -580,7 +621,7 @@ __device__ __forceinline__ int fetch(const DecodeArgs& a, const CUtensorMap* kma
 // Query fragments of a row: B operand [16 channels x 8 heads] of each step, thread (head lane / 4,
 // channels by lane % 4).  bf16 steps take channels 2t, 2t+1 and 2t+8, 2t+9; e4m3 steps take
 // 4t .. 4t+3, the order in which a lane gets the keys' bytes.
-template <int D, bool E4M3>
+template <int D, int KIND>
 __device__ __forceinline__ void read_q(const DecodeArgs& a, int row, int n, int lane, uint32_t (&q)[D / 16][2]) {
   const DecodeParams& p = a.p;
   const auto [b, h, chunk] = row_index(a, row);
@@ -589,7 +630,7 @@ __device__ __forceinline__ void read_q(const DecodeArgs& a, int row, int n, int 
   const __nv_bfloat16* src = p.q + b * p.qs.seq + static_cast<int64_t>(h * a.group + (in ? i : 0)) * p.qs.head;
 #pragma unroll
   for (int s = 0; s < D / 16; ++s) {
-    if constexpr (E4M3) {
+    if constexpr (KIND != kBf16) {
       const uint2 w = in ? *reinterpret_cast<const uint2*>(src + s * 16 + (lane & 3) * 4) : make_uint2(0, 0);
       q[s][0] = w.x;
       q[s][1] = w.y;
@@ -605,13 +646,13 @@ __device__ __forceinline__ void read_q(const DecodeArgs& a, int row, int n, int 
 // fp16, scaled by a power of two per head to a largest value in [2^14, 2^15): no more (65504) fits, and
 // what is smaller loses no bits down to 2^-31 of it.  (Powers of two are held to fp32's normal numbers: a head
 // whose largest value is below 2^-112 stays below 2^14.)
-template <int D, bool E4M3, int NB>
+template <int D, int KIND, int NB>
 __device__ __forceinline__ void scale_q(const DecodeArgs& a, int row, int lane, uint32_t (&q)[NB][D / 16][2],
                                         float (&scale)[NB][2]) {
-  const float base = a.p.scale * 1.4426950408889634f * (E4M3 ? a.p.c.k_scale[row_index(a, row).h] : 1.f);
+  const float base = a.p.scale * 1.4426950408889634f * (KIND == kE4m3 ? a.p.c.k_scale[row_index(a, row).h] : 1.f);
 #pragma unroll
   for (int n = 0; n < NB; ++n) {
-    if constexpr (!E4M3) {
+    if constexpr (KIND == kBf16) {
       scale[n][0] = scale[n][1] = base;
     } else {
       float top = 0.f;
@@ -642,16 +683,16 @@ __device__ __forceinline__ void scale_q(const DecodeArgs& a, int row, int lane, 
 }
 
 // Address of the 16-byte piece `c` of key `r` in a matrix of the ring (TMA's swizzle).
-template <int D, bool E4M3>
+template <int D, int KIND>
 __device__ __forceinline__ uint32_t piece_at(uint32_t matrix, int r, int c) {
-  if constexpr (E4M3 && D == 64) {  // 64-byte rows
+  if constexpr (KIND != kBf16 && D == 64) {  // 64-byte rows
     return matrix + r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
   } else {
     return matrix + (c >> 3) * (kTileKeys * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
   }
 }
 
-template <int D, bool E4M3, int NB>
+template <int D, int KIND, int NB>
 struct State {
   uint32_t q[NB][D / 16][2];
   float scale[NB][2];
@@ -664,9 +705,10 @@ struct State {
 // smallest normal number, is far below p's own last bit unless p is as small.
 __device__ __forceinline__ float left_over(float p, float cut) { return fmaxf(p - cut, fminf(p, 1.17549435e-38f)); }
 
-template <int D, bool E4M3, int NB>
-__device__ __forceinline__ void compute_tile(State<D, E4M3, NB>& t, uint32_t k_at, uint32_t v_at,
-                                             uint32_t seen, int lane) {
+template <int D, int KIND, int NB>
+__device__ __forceinline__ void compute_tile(State<D, KIND, NB>& t, uint32_t k_at, uint32_t v_at,
+                                             uint32_t seen, uint32_t exps, int lane) {
+  constexpr bool k8 = KIND != kBf16, kBlocks = KIND >= kE4m3Block;
   // One or two warps a scheduler: latencies are hidden within the warp, by loading ahead of the
   // products and by two sets of sums each.
   float s[2][NB][4], s2[2][NB][4];
@@ -677,7 +719,7 @@ __device__ __forceinline__ void compute_tile(State<D, E4M3, NB>& t, uint32_t k_a
 #pragma unroll
       for (int x = 0; x < 4; ++x) s[i][n][x] = s2[i][n][x] = 0.f;
   // S^T = K Q^T: matrices of ldmatrix are (keys 0-7, 8-15) x (pieces 2j, 2j+1)
-  constexpr int kSteps = D * (E4M3 ? 1 : 2) / 32, kGroup = kSteps < 4 ? kSteps : 4;
+  constexpr int kSteps = D * (k8 ? 1 : 2) / 32, kGroup = kSteps < 4 ? kSteps : 4;
   const int row = lane & 15, col = lane >> 4;
 #pragma unroll
   for (int j0 = 0; j0 < kSteps; j0 += kGroup) {
@@ -685,20 +727,21 @@ __device__ __forceinline__ void compute_tile(State<D, E4M3, NB>& t, uint32_t k_a
 #pragma unroll
     for (int j = 0; j < kGroup; ++j)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) ldsm4(w[j][i], piece_at<D, E4M3>(k_at, i * 16 + row, 2 * (j0 + j) + col));
+      for (int i = 0; i < 2; ++i) ldsm4(w[j][i], piece_at<D, KIND>(k_at, i * 16 + row, 2 * (j0 + j) + col));
 #pragma unroll
     for (int j = 0; j < kGroup; ++j)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        if constexpr (!E4M3) {
+        if constexpr (!k8) {
 #pragma unroll
           for (int n = 0; n < NB; ++n)
             mma16816<false>(j & 1 ? s2[i][n] : s[i][n], w[j][i], t.q[n][j0 + j][0], t.q[n][j0 + j][1]);
         } else {
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const uint32_t f[4] = {widen_lo(w[j][i][2 * x]), widen_lo(w[j][i][2 * x + 1]), widen_hi(w[j][i][2 * x]),
-                                   widen_hi(w[j][i][2 * x + 1])};
+            uint32_t f[4];
+            widen<KIND>(w[j][i][2 * x], f[0], f[2]);
+            widen<KIND>(w[j][i][2 * x + 1], f[1], f[3]);
 #pragma unroll
             for (int n = 0; n < NB; ++n)
               mma16816<true>(x ? s2[i][n] : s[i][n], f, t.q[n][2 * (j0 + j) + x][0], t.q[n][2 * (j0 + j) + x][1]);
@@ -707,17 +750,25 @@ __device__ __forceinline__ void compute_tile(State<D, E4M3, NB>& t, uint32_t k_a
       }
   }
   // values of the first 16 keys, for the second product
-  constexpr int kValues = E4M3 ? D / 32 : D / 16;
-  const int key = E4M3 ? row : (lane & 7) + ((lane >> 4) << 3), piece = E4M3 ? col : (lane >> 3) & 1;
+  constexpr int kValues = k8 ? D / 32 : D / 16;
+  const int key = k8 ? row : (lane & 7) + ((lane >> 4) << 3), piece = k8 ? col : (lane >> 3) & 1;
   uint32_t v[kValues][4];
 #pragma unroll
-  for (int j = 0; j < kValues; ++j) ldsm4t(v[j], piece_at<D, E4M3>(v_at, key, 2 * j + piece));
+  for (int j = 0; j < kValues; ++j) ldsm4t(v[j], piece_at<D, KIND>(v_at, key, 2 * j + piece));
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int n = 0; n < NB; ++n)
 #pragma unroll
-      for (int x = 0; x < 4; ++x) s[i][n][x] = (s[i][n][x] + s2[i][n][x]) * t.scale[n][x & 1];
+      for (int x = 0; x < 4; ++x) {
+        // with block scales, a key's score gets the log of its value's scale: weights are then those of the stored
+        // numbers, and none is beyond what the reference allows
+        if constexpr (kBlocks)
+          s[i][n][x] = fmaf((s[i][n][x] + s2[i][n][x]) * pow2_bits(exponent_at(exps, i)), t.scale[n][x & 1],
+                            static_cast<float>(exponent_at(exps, 2 + i)));
+        else
+          s[i][n][x] = (s[i][n][x] + s2[i][n][x]) * t.scale[n][x & 1];
+      }
   const bool whole = seen == 0xFFFFFFFFu;
   if (!whole) {  // keys of the lane: lane / 4 and 8 further, of both halves
     const uint32_t bits = seen >> (lane >> 2);
@@ -736,7 +787,7 @@ __device__ __forceinline__ void compute_tile(State<D, E4M3, NB>& t, uint32_t k_a
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int x = 0; x < 4; ++x) pass |= s[i][n][x] > t.m[n][x & 1] + (kRenew + kLift<E4M3>);
+      for (int x = 0; x < 4; ++x) pass |= s[i][n][x] > t.m[n][x & 1] + (kRenew + kLift<KIND>);
   if (__any_sync(0xFFFFFFFFu, pass)) {
 #pragma unroll
     for (int n = 0; n < NB; ++n)
@@ -745,7 +796,7 @@ __device__ __forceinline__ void compute_tile(State<D, E4M3, NB>& t, uint32_t k_a
         float top = fmaxf(fmaxf(s[0][n][x], s[0][n][x + 2]), fmaxf(s[1][n][x], s[1][n][x + 2]));
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-        top = fmaxf(top - kLift<E4M3>, t.m[n][x]);
+        top = fmaxf(top - kLift<KIND>, t.m[n][x]);
         const float fade = top == -INFINITY ? 1.f : ex2_approx(t.m[n][x] - top);
         t.m[n][x] = top;
         t.l[n][x] *= fade;
@@ -769,12 +820,13 @@ __device__ __forceinline__ void compute_tile(State<D, E4M3, NB>& t, uint32_t k_a
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         e[x] = ex2_approx(s[i][n][x] - (x & 1 ? m1 : m0));
-        t.l[n][x & 1] += e[x];
+        if constexpr (kBlocks) t.l[n][x & 1] = fmaf(e[x], pow2_bits(-exponent_at(exps, 2 + i)), t.l[n][x & 1]);
+        else t.l[n][x & 1] += e[x];
       }
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         uint32_t w;
-        if constexpr (E4M3) {
+        if constexpr (k8) {
           const __half2 f = __floats2half2_rn(e[2 * x], e[2 * x + 1]);
           w = *reinterpret_cast<const uint32_t*>(&f);
         } else {
@@ -803,8 +855,8 @@ __device__ __forceinline__ void compute_tile(State<D, E4M3, NB>& t, uint32_t k_a
 #pragma unroll
     for (int j = 0; j < kValues; ++j) {
       uint32_t w[4] = {v[j][0], v[j][1], v[j][2], v[j][3]};
-      if (i == 0) ldsm4t(v[j], piece_at<D, E4M3>(v_at, 16 + key, 2 * j + piece));
-      if constexpr (!E4M3) {
+      if (i == 0) ldsm4t(v[j], piece_at<D, KIND>(v_at, 16 + key, 2 * j + piece));
+      if constexpr (!k8) {
         if (!whole) {
           w[0] &= keep[0];
           w[1] &= keep[0];
@@ -819,8 +871,9 @@ __device__ __forceinline__ void compute_tile(State<D, E4M3, NB>& t, uint32_t k_a
       } else {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const uint32_t u0 = __byte_perm(w[2 * x], 0, 0x3120), u1 = __byte_perm(w[2 * x + 1], 0, 0x3120);
-          uint32_t f[4] = {widen_lo(u0), widen_hi(u0), widen_lo(u1), widen_hi(u1)};
+          uint32_t f[4];
+          widen<KIND, true>(w[2 * x], f[0], f[1]);
+          widen<KIND, true>(w[2 * x + 1], f[2], f[3]);
           if (!whole) {
             f[0] &= keep[0];
             f[1] &= keep[0];
@@ -836,9 +889,9 @@ __device__ __forceinline__ void compute_tile(State<D, E4M3, NB>& t, uint32_t k_a
 }
 
 // Channel of accumulator x (0 or 2: rows lane / 4 and 8 further) of tile j.
-template <bool E4M3>
+template <int KIND>
 __device__ __forceinline__ int channel_of(int j, int x, int lane) {
-  return E4M3 ? j * 16 + (lane >> 2) * 2 + (x >> 1) : j * 16 + (lane >> 2) + (x >> 1) * 8;
+  return KIND != kBf16 ? j * 16 + (lane >> 2) * 2 + (x >> 1) : j * 16 + (lane >> 2) + (x >> 1) * 8;
 }
 
 struct RowAt {
@@ -856,9 +909,9 @@ __device__ __forceinline__ RowAt row_at(const DecodeArgs& a, int row) {
           p.lse ? p.lse + static_cast<int64_t>(b) * p.H_q + head : nullptr,
           min(8 * NB, a.group - chunk * 8 * NB), h};
 }
-template <bool E4M3>
+template <int KIND>
 __device__ __forceinline__ float value_scale(const DecodeArgs& a, int h) {
-  return E4M3 ? __ldg(a.p.c.v_scale + h) : 1.f;
+  return KIND == kE4m3 ? __ldg(a.p.c.v_scale + h) : 1.f;
 }
 
 // 1 / l, 0 for a row that saw nothing (l = 0 and O = 0: the output is 0)
@@ -867,17 +920,17 @@ __device__ __forceinline__ float natural_lse(float m, float l) {
   return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
-template <int D, bool E4M3, int NB>
+template <int D, int KIND, int NB>
 __device__ __forceinline__ void compute(const DecodeArgs& a, char* smem, uint32_t ring, uint32_t meta,
-                                        uint32_t bars, int pair, int first_row, const WaitCtl& wait, int lane) {
-  using C = Cfg<D, E4M3, NB>;
-  State<D, E4M3, NB> t;
+                                        uint32_t bars, uint32_t exps, int pair, int first_row, const WaitCtl& wait, int lane) {
+  using C = Cfg<D, KIND, NB>;
+  State<D, KIND, NB> t;
   // the next row's queries, on their way while the last tile of a row is computed (the first row's, while
   // its first tile comes); 16 heads' would take the registers of the accumulators
   constexpr bool kAhead = NB == 1;
   uint32_t ahead[kAhead ? D / 16 : 1][2];
   int ahead_row = first_row;
-  if constexpr (kAhead) read_q<D, E4M3>(a, first_row, 0, lane, ahead);
+  if constexpr (kAhead) read_q<D, KIND>(a, first_row, 0, lane, ahead);
   int4* heads = reinterpret_cast<int4*>(smem + C::kOffHead) + 2 * pair;
   bool starts = false;
   for (int done = 0;; ++done) {
@@ -897,13 +950,13 @@ __device__ __forceinline__ void compute(const DecodeArgs& a, char* smem, uint32_
             t.q[0][i][1] = ahead[i][1];
           }
         } else {
-          read_q<D, E4M3>(a, row, 0, lane, t.q[0]);
+          read_q<D, KIND>(a, row, 0, lane, t.q[0]);
         }
       } else {
 #pragma unroll
-        for (int n = 0; n < NB; ++n) read_q<D, E4M3>(a, row, n, lane, t.q[n]);
+        for (int n = 0; n < NB; ++n) read_q<D, KIND>(a, row, n, lane, t.q[n]);
       }
-      scale_q<D, E4M3, NB>(a, row, lane, t.q, t.scale);
+      scale_q<D, KIND, NB>(a, row, lane, t.q, t.scale);
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
         t.m[n][0] = t.m[n][1] = -INFINITY;
@@ -916,10 +969,12 @@ __device__ __forceinline__ void compute(const DecodeArgs& a, char* smem, uint32_
     }
     if constexpr (kAhead) {
       ahead_row = flags & kLast ? static_cast<int>(x.w) : -1;
-      if (ahead_row >= 0) read_q<D, E4M3>(a, ahead_row, 0, lane, ahead);
+      if (ahead_row >= 0) read_q<D, KIND>(a, ahead_row, 0, lane, ahead);
     }
     const uint32_t k_at = ring + stage * C::kStage;
-    compute_tile<D, E4M3, NB>(t, k_at, k_at + C::kMatrix, x.y, lane);
+    uint32_t e = 0;
+    if constexpr (KIND >= kE4m3Block) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(e) : "r"(exps + stage * 4));
+    compute_tile<D, KIND, NB>(t, k_at, k_at + C::kMatrix, x.y, e, lane);
     __syncwarp();
     if (lane == 0) mbar_arrive(full + 8);
     if (!(flags & kLast)) continue;
@@ -933,15 +988,15 @@ __device__ __forceinline__ void compute(const DecodeArgs& a, char* smem, uint32_
         for (int d = 4; d < 32; d <<= 1) t.l[n][i] += __shfl_xor_sync(0xFFFFFFFFu, t.l[n][i], d);
     if (starts && (flags & kEnds)) {  // the whole row
       const RowAt r = row_at<NB>(a, row);
-      const float v_scale = value_scale<E4M3>(a, r.h);
+      const float v_scale = value_scale<KIND>(a, r.h);
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
         const float i0 = inverse(t.l[n][0]) * v_scale, i1 = inverse(t.l[n][1]) * v_scale;
         const int h0 = n * 8 + (lane & 3) * 2;
-        if constexpr (E4M3) {
+        if constexpr (KIND != kBf16) {
 #pragma unroll
           for (int j = 0; j < D / 16; ++j) {
-            const int c = channel_of<true>(j, 0, lane);
+            const int c = channel_of<KIND>(j, 0, lane);
             if (h0 < r.heads)
               *reinterpret_cast<uint32_t*>(r.o + h0 * a.p.os.head + c) = pack_bf16x2(t.o[n][j][0] * i0, t.o[n][j][2] * i0);
             if (h0 + 1 < r.heads)
@@ -977,7 +1032,7 @@ __device__ __forceinline__ void compute(const DecodeArgs& a, char* smem, uint32_
       for (int j = 0; j < D / 16; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          f[(h0 + (i & 1)) * C::kHeadPitch + channel_of<E4M3>(j, i, lane)] = t.o[n][j][i];
+          f[(h0 + (i & 1)) * C::kHeadPitch + channel_of<KIND>(j, i, lane)] = t.o[n][j][i];
       if (lane < 4) {
         float* ml = f + C::kHeads * C::kHeadPitch;
 #pragma unroll
@@ -994,9 +1049,9 @@ __device__ __forceinline__ void compute(const DecodeArgs& a, char* smem, uint32_
 
 // Joins the CTA's parts, row by row: 16 threads a head, D / 16 channels a thread.  Parts lie in the order of
 // the keys; the first of a row says whether the row starts in this CTA, the last whether it ends here.
-template <int D, bool E4M3, int NB>
+template <int D, int KIND, int NB>
 __device__ __forceinline__ void join_warps(const DecodeArgs& a, char* smem, int tid) {
-  using C = Cfg<D, E4M3, NB>;
+  using C = Cfg<D, KIND, NB>;
   constexpr int N = D / 16;
   const int lane = tid & 31, c0 = (tid & 15) * 4;  // channels c0 .. c0+3 of each 64
   const int4 mine = lane < 2 * C::kPairs ? reinterpret_cast<const int4*>(smem + C::kOffHead)[lane] : make_int4(0, 0, 0, 0);
@@ -1051,7 +1106,7 @@ __device__ __forceinline__ void join_warps(const DecodeArgs& a, char* smem, int 
         }
       }
       if (starts && ends) {
-        const float inv = inverse(l) * value_scale<E4M3>(a, r.h);
+        const float inv = inverse(l) * value_scale<KIND>(a, r.h);
 #pragma unroll
         for (int g = 0; g < N / 4; ++g)
           *reinterpret_cast<uint2*>(r.o + h * a.p.os.head + g * 64 + c0) =
@@ -1073,11 +1128,11 @@ __device__ __forceinline__ void join_warps(const DecodeArgs& a, char* smem, int 
   if (tid == 0) reinterpret_cast<int4*>(a.p.workspace)[blockIdx.x] = make_int4(carried, carried_row, 0, 0);
 }
 
-template <int D, bool E4M3, int NB>
-__global__ void __launch_bounds__(Cfg<D, E4M3, NB>::kThreads, 1)
+template <int D, int KIND, int NB>
+__global__ void __launch_bounds__(Cfg<D, KIND, NB>::kThreads, 1)
     decode_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap) {
-  using C = Cfg<D, E4M3, NB>;
+  using C = Cfg<D, KIND, NB>;
   extern __shared__ __align__(1024) char smem[];  // the swizzled tiles need the alignment
   const uint32_t base = smem_u32(smem);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
@@ -1107,7 +1162,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NB>::kThreads, 1)
   fence_barrier_init();
   wait_for_previous();
 
-  if (E4M3 && tid * 32 < a.p.c.H_kv) {  // the scales are wanted at the start and at the end of a row
+  if (KIND == kE4m3 && tid * 32 < a.p.c.H_kv) {  // the scales are wanted at the start and at the end of a row
     asm volatile("prefetch.global.L1 [%0];" ::"l"(a.p.c.k_scale + tid * 32));
     asm volatile("prefetch.global.L1 [%0];" ::"l"(a.p.c.v_scale + tid * 32));
   }
@@ -1203,6 +1258,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NB>::kThreads, 1)
   const uint32_t ring = base + pair * C::kStages * C::kStage;
   const uint32_t meta = base + C::kOffMeta + pair * C::kStages * 16;
   const uint32_t bars = base + C::kOffBars + pair * C::kStages * 16;
+  const uint32_t exps = base + C::kOffExps + pair * C::kStages * 4;
   int fetched = 0, rest = 0;
   if constexpr (C::kPairs == 8) {
     if (warp >= C::kPairs) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
@@ -1217,9 +1273,9 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NB>::kThreads, 1)
       w.plan = make_plan(a, w.u, place.len, place.tiles, lane);
       w.pos = at;
       w.end = until;
-      fetched = fetch<D, E4M3, NB>(a, &kmap, &vmap, w, ring, meta, bars, run, wait, lane, rest);
+      fetched = fetch<D, KIND, NB>(a, &kmap, &vmap, w, ring, meta, bars, exps, run, wait, lane, rest);
     } else {
-      compute<D, E4M3, NB>(a, smem, ring, meta, bars, pair, place.u * a.rows + place.m, wait, lane);
+      compute<D, KIND, NB>(a, smem, ring, meta, bars, exps, pair, place.u * a.rows + place.m, wait, lane);
     }
   }
   __syncthreads();
@@ -1230,12 +1286,12 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NB>::kThreads, 1)
     if (tid == 0) reinterpret_cast<int4*>(a.p.workspace)[blockIdx.x] = make_int4(0, 0, 0, 0);
     return;
   }
-  if (tid < 32 * C::kPairs) join_warps<D, E4M3, NB>(a, smem, tid);
+  if (tid < 32 * C::kPairs) join_warps<D, KIND, NB>(a, smem, tid);
 }
 
 // Joins the parts of a row that several CTAs hold: CTA x's header says how many there are, its own
 // second part first, then the first parts of the CTAs behind it.  One block a head, one thread a channel.
-template <int D, bool E4M3, int NB>
+template <int D, int KIND, int NB>
 __global__ void __launch_bounds__(D) join_kernel(const __grid_constant__ DecodeArgs a) {
   constexpr int kHeads = 8 * NB;
   wait_for_previous();
@@ -1245,7 +1301,7 @@ __global__ void __launch_bounds__(D) join_kernel(const __grid_constant__ DecodeA
   if (n < 2) return;
   const RowAt r = row_at<NB>(a, head.y);
   if (h >= r.heads) return;
-  const float v_scale = value_scale<E4M3>(a, r.h);
+  const float v_scale = value_scale<KIND>(a, r.h);
   float pm[kAtOnce], pl[kAtOnce], po[kAtOnce];
   auto load = [&](int i, int at, bool in) {
     const Part x = part_at<D>(a.p.workspace, kHeads, blockIdx.x + at, at == 0);
@@ -1280,14 +1336,14 @@ __global__ void __launch_bounds__(D) join_kernel(const __grid_constant__ DecodeA
 bool make_pool_map(CUtensorMap* map, const void* base, const KvView& c, int64_t page_bytes) {
   EncodeTiledFn enc = encode_tiled_fn();
   if (!enc) return false;
-  const int item = c.e4m3 ? 1 : 2, P = 1 << c.log2_page, row = c.d * item;
+  const int item = c.kind == kBf16 ? 2 : 1, P = 1 << c.log2_page, row = c.d * item;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(c.d), static_cast<cuuint64_t>(c.H_kv) * P,
                               static_cast<cuuint64_t>(c.num_pages)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(row), static_cast<cuuint64_t>(page_bytes)};
   const cuuint32_t box[3] = {static_cast<cuuint32_t>((row < 128 ? row : 128) / item),
                              static_cast<cuuint32_t>(P < kTileKeys ? P : kTileKeys), 1};
   const cuuint32_t steps[3] = {1, 1, 1};
-  return enc(map, c.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+  return enc(map, item == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
              const_cast<void*>(base), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
              row < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -1305,24 +1361,31 @@ int sm_count(int dev) {
   return n < kMaxCtas ? n : kMaxCtas;
 }
 
-template <int D, bool E4M3, int NB>
+template <int D, int KIND, int NB>
 int launch(DecodeArgs& a, int dev, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream) {
-  using C = Cfg<D, E4M3, NB>;
+  using C = Cfg<D, KIND, NB>;
   // Where no row can have more than 4 tiles a warp pair, rows stay whole: the second kernel, 2 to 3 us on
   // the GPU and a launch, costs more than the few tiles by which runs then differ.
   a.whole_rows = a.most_tiles <= 4 * C::kPairs;
   static std::atomic<bool> allowed[kMaxDevices];  // the shared memory it needs
   if (dev >= kMaxDevices || !allowed[dev].load(std::memory_order_relaxed)) {
-    if (cudaFuncSetAttribute(decode_kernel<D, E4M3, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(decode_kernel<D, KIND, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              C::kSmem) != cudaSuccess)
       return -1;
     if (dev < kMaxDevices) allowed[dev].store(true, std::memory_order_relaxed);
   }
-  return launch_after(decode_kernel<D, E4M3, NB>, dim3(a.ctas), C::kThreads, C::kSmem, stream, a, k, v) &&
-                 (a.whole_rows || launch_after(join_kernel<D, E4M3, NB>, dim3(a.ctas, a.group < C::kHeads ? a.group : C::kHeads), D,
+  return launch_after(decode_kernel<D, KIND, NB>, dim3(a.ctas), C::kThreads, C::kSmem, stream, a, k, v) &&
+                 (a.whole_rows || launch_after(join_kernel<D, KIND, NB>, dim3(a.ctas, a.group < C::kHeads ? a.group : C::kHeads), D,
                               0, stream, a))
              ? 0
              : -1;
+}
+
+template <int KIND>
+int launch_kind(DecodeArgs& a, int dev, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream) {
+  if (a.heads == 8)
+    return a.p.c.d == 128 ? launch<128, KIND, 1>(a, dev, k, v, stream) : launch<64, KIND, 1>(a, dev, k, v, stream);
+  return a.p.c.d == 128 ? launch<128, KIND, 2>(a, dev, k, v, stream) : launch<64, KIND, 2>(a, dev, k, v, stream);
 }
 
 // Heads of a row: 8 where a group has no more, else 16 (a larger group takes several rows, whose
@@ -1374,12 +1437,13 @@ int launch_attn_decode(const DecodeParams& p, uint64_t wait_ns, cudaStream_t str
   CUtensorMap k, v;
   if (!make_pool_map(&k, p.c.k, p.c, p.c.k_page_bytes) || !make_pool_map(&v, p.c.v, p.c, p.c.v_page_bytes))
     return -1;
-  if (heads == 8) {
-    if (p.c.d == 128) return p.c.e4m3 ? launch<128, true, 1>(a, dev, k, v, stream) : launch<128, false, 1>(a, dev, k, v, stream);
-    return p.c.e4m3 ? launch<64, true, 1>(a, dev, k, v, stream) : launch<64, false, 1>(a, dev, k, v, stream);
+  switch (p.c.kind) {
+    case kBf16: return launch_kind<kBf16>(a, dev, k, v, stream);
+    case kE4m3: return launch_kind<kE4m3>(a, dev, k, v, stream);
+    case kE4m3Block: return launch_kind<kE4m3Block>(a, dev, k, v, stream);
+    case kInt8Block: return launch_kind<kInt8Block>(a, dev, k, v, stream);
   }
-  if (p.c.d == 128) return p.c.e4m3 ? launch<128, true, 2>(a, dev, k, v, stream) : launch<128, false, 2>(a, dev, k, v, stream);
-  return p.c.e4m3 ? launch<64, true, 2>(a, dev, k, v, stream) : launch<64, false, 2>(a, dev, k, v, stream);
+  return -1;
 }
 
 }  // namespace cm

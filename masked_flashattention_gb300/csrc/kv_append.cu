@@ -159,11 +159,11 @@ __device__ __forceinline__ void rotate_pieces(uint4& w0, uint4& w1, const float2
   w1 = pack8(hi);
 }
 
-// Sequence and page (of those that it adds to) of page number `item` of all that the call touches; false where
-// there are fewer.  SCAN: items are dealt out without gaps, by a scan over the sequences, 256 at a time, in which
+// Sequence and page (of those that it adds to; or, with 2^log2_unit the tokens of a block, block) number `item` of all
+// that the call touches; false where there are fewer.  SCAN: items are dealt out without gaps, by a scan over the sequences, 256 at a time, in which
 // the whole block takes part; else a sequence has `segs` of them, and those it does not need end at once.
 template <bool SCAN>
-__device__ __forceinline__ bool find_page(const AppendParams& p, int item, int segs, int& b, int& seg) {
+__device__ __forceinline__ bool find_page(const AppendParams& p, int item, int segs, int log2_unit, int& b, int& seg) {
   if constexpr (!SCAN) {
     b = item / segs;
     seg = item - b * segs;
@@ -175,7 +175,7 @@ __device__ __forceinline__ bool find_page(const AppendParams& p, int item, int s
   for (int b0 = 0, before = 0; b0 < p.c.B && before <= item; b0 += kThreads) {
     int start, count, base, pages = 0;
     if (b0 + tid < p.c.B && new_tokens(p, b0 + tid, start, count, base) && count > 0)
-      pages = ((start + count - 1) >> p.c.log2_page) - (start >> p.c.log2_page) + 1;
+      pages = ((start + count - 1) >> log2_unit) - (start >> log2_unit) + 1;
     int sum = pages;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -202,6 +202,49 @@ __device__ __forceinline__ bool find_page(const AppendParams& p, int item, int s
   return b >= 0;
 }
 
+// A page's summary from each lane's largest and smallest of its 16 channels, as stored (fp16 or bf16 pairs, times scale).
+template <int D, bool F16>
+__device__ __forceinline__ void write_summary(const AppendParams& p, int64_t at, uint32_t (&high)[8], uint32_t (&low)[8],
+                                              float scale, int c0, int c1, int j, int sub) {
+  constexpr int kPer = D / 16;
+  float a = 0.f, most[16], least[16];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+#pragma unroll
+    for (int d = kPer; d < 32; d <<= 1) {
+      high[i] = max2<F16>(high[i], __shfl_xor_sync(0xFFFFFFFFu, high[i], d));
+      low[i] = min2<F16>(low[i], __shfl_xor_sync(0xFFFFFFFFu, low[i], d));
+    }
+    const float2 m = value2<F16>(high[i], scale), l = value2<F16>(low[i], scale);
+    most[2 * i] = m.x;
+    most[2 * i + 1] = m.y;
+    least[2 * i] = l.x;
+    least[2 * i + 1] = l.y;
+    a = fmaxf(a, fmaxf(fmaxf(fabsf(m.x), fabsf(m.y)), fmaxf(fabsf(l.x), fabsf(l.y))));
+  }
+#pragma unroll
+  for (int d = 1; d < kPer; d <<= 1) a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, d));
+  const int e = scale_exponent(a);
+  const float inv = pow2_bits(-e);
+  if (sub) return;
+  int8_t* to = p.c.summary + at * 2 * D;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    uint32_t up[2] = {0, 0}, down[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int u = static_cast<int>(fminf(fmaxf(ceilf(most[8 * half + i] * inv), -127.f), 127.f));
+      const int l = static_cast<int>(fminf(fmaxf(floorf(least[8 * half + i] * inv), -127.f), 127.f));
+      up[i >> 2] |= static_cast<uint32_t>(u & 0xFF) << (8 * (i & 3));
+      down[i >> 2] |= static_cast<uint32_t>(l & 0xFF) << (8 * (i & 3));
+    }
+    const int c = half ? c1 : c0;
+    *reinterpret_cast<uint2*>(to + c) = make_uint2(up[0], up[1]);
+    *reinterpret_cast<uint2*>(to + D + c) = make_uint2(down[0], down[1]);
+  }
+  if (j == 0) p.c.summary_scale[at] = pow2_bits(e);
+}
+
 // A block's share of the second role.
 template <int D, bool E4M3, bool INTER, bool SCAN>
 __device__ __forceinline__ void store_keys_by_page(const AppendParams& p, int segs, uint4* ring) {
@@ -213,7 +256,7 @@ __device__ __forceinline__ void store_keys_by_page(const AppendParams& p, int se
   const int item = blockIdx.x / head_blocks;
   const int h = (blockIdx.x - item * head_blocks) * (kThreads / 32) + tid / 32;
   int b, seg, start, count, base;
-  if (!find_page<SCAN>(p, item, segs, b, seg)) return;
+  if (!find_page<SCAN>(p, item, segs, p.c.log2_page, b, seg)) return;
   if (!new_tokens(p, b, start, count, base) || h >= p.c.H_kv) return;
   const int place = (start >> p.c.log2_page) + seg, first = place << p.c.log2_page;
   const int lo = max(start, first) - first, hi = min(start + count, first + P) - first;  // new rows of the page
@@ -306,62 +349,221 @@ __device__ __forceinline__ void store_keys_by_page(const AppendParams& p, int se
       low[i] = min2<E4M3>(low[i], x[i]);
     }
   }
-  if (!paged) return;
-  float a = 0.f, most[16], least[16];
+  if (paged) write_summary<D, E4M3>(p, static_cast<int64_t>(page) * p.c.H_kv + h, high, low, scale, c0, c1, j, sub);
+}
+
+// ---- blocks with a scale each ---------------------------------------------------------------------
+// e of the smallest power of two with a <= 127 * 2^e (int8) or a <= 448 * 2^e = 1.75 * 2^(e + 8) (e4m3), held to +-32
+template <bool INT8>
+__device__ __forceinline__ int needed_exponent(float a) {
+  const uint32_t u = __float_as_uint(a), m = u & 0x7FFFFFu;
+  const int x = static_cast<int>(u >> 23) - 127, e = INT8 ? x - 6 + (m > 0x7E0000u) : x - 8 + (m > 0x600000u);
+  return min(max(e, -kMaxBlockExp), kMaxBlockExp);
+}
+// 8 fp32 values times a power of two as the cache holds them
+template <bool INT8>
+__device__ __forceinline__ uint2 pack8_block(const float (&x)[8], float times) {
+  uint32_t w[2];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 2; ++i) {
+    if constexpr (INT8) {
+      uint32_t q[4];
 #pragma unroll
-    for (int d = kPer; d < 32; d <<= 1) {
-      high[i] = max2<E4M3>(high[i], __shfl_xor_sync(0xFFFFFFFFu, high[i], d));
-      low[i] = min2<E4M3>(low[i], __shfl_xor_sync(0xFFFFFFFFu, low[i], d));
+      for (int c = 0; c < 4; ++c)  // NaN becomes 0
+        q[c] = static_cast<uint32_t>(min(max(__float2int_rn(x[4 * i + c] * times), -127), 127));
+      w[i] = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
+    } else {
+      uint32_t q[2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        q[c] = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i + 2 * c] * times, x[4 * i + 2 * c + 1] * times),
+                                        __NV_SATFINITE, __NV_E4M3);
+      w[i] = q[0] | (q[1] << 16);
     }
-    const float2 m = value2<E4M3>(high[i], scale), l = value2<E4M3>(low[i], scale);
-    most[2 * i] = m.x;
-    most[2 * i + 1] = m.y;
-    least[2 * i] = l.x;
-    least[2 * i + 1] = l.y;
-    a = fmaxf(a, fmaxf(fmaxf(fabsf(m.x), fabsf(m.y)), fmaxf(fabsf(l.x), fabsf(l.y))));
   }
+  return make_uint2(w[0], w[1]);
+}
+template <bool INT8>
+__device__ __forceinline__ void unpack8_block(uint2 w, float (&x)[8]) {
+  const uint32_t u[2] = {w.x, w.y};
 #pragma unroll
-  for (int d = 1; d < kPer; d <<= 1) a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, d));
-  const int e = scale_exponent(a);
-  const float inv = pow2_bits(-e);
-  if (sub) return;
-  const int64_t at = static_cast<int64_t>(page) * p.c.H_kv + h;
-  int8_t* to = p.c.summary + at * 2 * D;
+  for (int i = 0; i < 2; ++i) {
+    if constexpr (INT8) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) x[4 * i + c] = static_cast<float>(static_cast<int8_t>(u[i] >> (8 * c)));
+    } else {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const uint32_t h = widen2(u[i] >> (16 * c));
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        x[4 * i + 2 * c] = f.x;
+        x[4 * i + 2 * c + 1] = f.y;
+      }
+    }
+  }
+}
+// a lane's 16 channels of a token, as stored times the block's scale, into the page's largest and smallest: a stored
+// number has at most 8 bits, so bf16 holds it exactly
+template <bool INT8>
+__device__ __forceinline__ void take_in(uint2 a, uint2 b, float scale, uint32_t (&high)[8], uint32_t (&low)[8]) {
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
-    uint32_t up[2] = {0, 0}, down[2] = {0, 0};
+    float x[8];
+    unpack8_block<INT8>(half ? b : a, x);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int u = static_cast<int>(fminf(fmaxf(ceilf(most[8 * half + i] * inv), -127.f), 127.f));
-      const int l = static_cast<int>(fminf(fmaxf(floorf(least[8 * half + i] * inv), -127.f), 127.f));
-      up[i >> 2] |= static_cast<uint32_t>(u & 0xFF) << (8 * (i & 3));
-      down[i >> 2] |= static_cast<uint32_t>(l & 0xFF) << (8 * (i & 3));
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t y = pack_bf16x2(x[2 * i] * scale, x[2 * i + 1] * scale);
+      high[4 * half + i] = max2<false>(high[4 * half + i], y);
+      low[4 * half + i] = min2<false>(low[4 * half + i], y);
     }
-    const int c = half ? c1 : c0;
-    *reinterpret_cast<uint2*>(to + c) = make_uint2(up[0], up[1]);
-    *reinterpret_cast<uint2*>(to + D + c) = make_uint2(down[0], down[1]);
   }
-  if (j == 0) p.c.summary_scale[at] = pow2_bits(e);
+}
+
+// The second role where blocks have scales: one warp a head's keys or values of a block, or with summaries of all the
+// blocks of a page that the call touches.  A block's new rows are in the warp's registers at once (16 rows, 16
+// channels of one of 4 or 8 of them a lane and step), so they are read once: rotated, their largest magnitude taken,
+// the scale settled, then stored.  Earlier rows are read only where the scale grows (or for the summary).
+template <int D, bool INT8, bool INTER, bool SCAN>
+__device__ __forceinline__ void store_blocks(const AppendParams& p, int segs) {
+  constexpr int kPer = D / 16, kRows = 32 / kPer, kSteps = kBlockTokens / kRows;
+  const int tid = threadIdx.x, lane = tid & 31, P = 1 << p.c.log2_page;
+  const bool whole_pages = p.c.summary != nullptr;
+  const int log2_unit = whole_pages ? p.c.log2_page : 4;
+  const int head_blocks = (2 * p.c.H_kv + kThreads / 32 - 1) / (kThreads / 32);
+  const int item = blockIdx.x / head_blocks;
+  const int hh = (blockIdx.x - item * head_blocks) * (kThreads / 32) + tid / 32;
+  int b, seg, start, count, base;
+  if (!find_page<SCAN>(p, item, segs, log2_unit, b, seg)) return;
+  if (!new_tokens(p, b, start, count, base) || hh >= 2 * p.c.H_kv) return;
+  const bool is_v = hh >= p.c.H_kv;
+  const int h = is_v ? hh - p.c.H_kv : hh;
+  const int first = ((start >> log2_unit) + seg) << log2_unit;  // positions from here on
+  const int lo = max(start, first), hi = min(start + count, first + (1 << log2_unit));
+  if (lo >= hi) return;
+  const int page = p.c.table[static_cast<int64_t>(b) * p.c.max_pages + (first >> p.c.log2_page)];
+  const bool paged = static_cast<unsigned>(page) < static_cast<unsigned>(p.c.num_pages);
+  if (!paged && hh == 0 && lane == 0) set_status(p.c.status, kDevBadMeta, b);
+  const int j = lane % kPer, sub = lane / kPer, pairs = is_v ? 0 : p.rot_dim >> 4;
+  const bool turns = j < pairs;
+  const int c0 = 8 * (turns ? j : 2 * j), c1 = 8 * (turns ? j + pairs : 2 * j + 1);
+  const Strides& st = is_v ? p.vs : p.ks;
+  const __nv_bfloat16* src = (is_v ? p.v : p.k) + h * st.head + (p.cu_new ? base * st.token : b * st.seq);
+  const int64_t at = static_cast<int64_t>(paged ? page : 0) * p.c.H_kv + h;
+  char* pool = (is_v ? p.c.v + (paged ? page : 0) * p.c.v_page_bytes : p.c.k + (paged ? page : 0) * p.c.k_page_bytes) +
+               (static_cast<int64_t>(h) << p.c.log2_page) * D;
+  float* scales = const_cast<float*>(is_v ? p.c.v_scale : p.c.k_scale) + (at << (p.c.log2_page - 4));
+  const bool sums = whole_pages && !is_v && paged;
+  uint32_t high[8], low[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    high[i] = 0xFF80FF80u;  // -inf
+    low[i] = 0x7F807F80u;
+  }
+#pragma unroll 1
+  for (int f = sums ? first : lo & ~15; f < hi; f += kBlockTokens) {
+    const int row = f & (P - 1);
+    char* to = pool + row * D;
+    const bool carried = lo > f;  // holds earlier tokens
+    const int e_old = carried && paged ? block_exponent(__float_as_uint(scales[row >> 4])) : -kMaxBlockExp;
+    uint4 w[kSteps][2];
+    uint32_t top = 0;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      const int r = s * kRows + sub, pos = f + r;
+      w[s][0] = w[s][1] = make_uint4(0, 0, 0, 0);
+      if (pos >= lo && pos < hi) {
+        const __nv_bfloat16* x = src + static_cast<int64_t>(pos - start) * st.token;
+        w[s][0] = __ldg(reinterpret_cast<const uint4*>(x + c0));
+        w[s][1] = __ldg(reinterpret_cast<const uint4*>(x + c1));
+      } else if (pos < lo && sums) {
+        const uint2 a = *reinterpret_cast<const uint2*>(to + r * D + c0), c = *reinterpret_cast<const uint2*>(to + r * D + c1);
+        w[s][0].x = a.x, w[s][0].y = a.y, w[s][1].x = c.x, w[s][1].y = c.y;
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      const int pos = f + s * kRows + sub;
+      if (pos < lo || pos >= hi) continue;
+      if (turns) {
+        float2 cs[8];
+        load_turn<INTER>(p.rope, static_cast<int64_t>(pos) * p.rot_dim, j, pairs, cs);
+        rotate_pieces<INTER>(w[s][0], w[s][1], cs);
+      }
+      if (p.k_out && !is_v) {
+        __nv_bfloat16* out = p.k_out + h * p.kos.head + (p.cu_new ? base * p.kos.token : b * p.kos.seq) +
+                             static_cast<int64_t>(pos - start) * p.kos.token;
+        *reinterpret_cast<uint4*>(out + c0) = w[s][0];
+        *reinterpret_cast<uint4*>(out + c1) = w[s][1];
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        top = max2<false>(top, w[s][i].x & 0x7FFF7FFFu);
+        top = max2<false>(top, w[s][i].y & 0x7FFF7FFFu);
+        top = max2<false>(top, w[s][i].z & 0x7FFF7FFFu);
+        top = max2<false>(top, w[s][i].w & 0x7FFF7FFFu);
+      }
+    }
+    if (!paged) continue;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) top = max2<false>(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+    const float2 tops = bf16x2_to_float2(top);
+    const int e = f + kBlockTokens <= lo ? e_old : max(e_old, needed_exponent<INT8>(fmaxf(tops.x, tops.y)));
+    const float scale = pow2_bits(e), inv = pow2_bits(-e);
+    const bool again = carried && e > e_old;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      const int r = s * kRows + sub, pos = f + r;
+      const bool fresh = pos >= lo;
+      if (pos >= hi || !(fresh || again || sums)) continue;
+      uint2* to0 = reinterpret_cast<uint2*>(to + r * D + c0);
+      uint2* to1 = reinterpret_cast<uint2*>(to + r * D + c1);
+      uint2 a, c;
+      float x[8];
+      if (fresh) {
+        unpack8(w[s][0], x);
+        a = pack8_block<INT8>(x, inv);
+        unpack8(w[s][1], x);
+        c = pack8_block<INT8>(x, inv);
+      } else {
+        a = sums ? make_uint2(w[s][0].x, w[s][0].y) : *to0;
+        c = sums ? make_uint2(w[s][1].x, w[s][1].y) : *to1;
+        if (again) {
+          const float fade = pow2_bits(e_old - e);
+          unpack8_block<INT8>(a, x);
+          a = pack8_block<INT8>(x, fade);
+          unpack8_block<INT8>(c, x);
+          c = pack8_block<INT8>(x, fade);
+        }
+      }
+      if (fresh || again) {
+        *to0 = a;
+        *to1 = c;
+      }
+      if (sums) take_in<INT8>(a, c, scale, high, low);
+    }
+    if (lane == 0 && f + kBlockTokens > lo) scales[row >> 4] = scale;
+  }
+  if (sums) write_summary<D, false>(p, at, high, low, 1.f, c0, c1, j, sub);
 }
 
 // Blocks 0 .. page_blocks-1 have the second role.
-template <int D, bool E4M3, bool INTER, bool SCAN>
-__global__ void __launch_bounds__(kThreads, 4)
+template <int D, int KIND, bool INTER, bool SCAN>
+__global__ void __launch_bounds__(kThreads, KIND >= kE4m3Block ? 2 : 4)
     append_kernel(const AppendParams p, int log2_tokens, int page_blocks, int segs) {
+  constexpr bool E4M3 = KIND == kE4m3, BLOCKS = KIND >= kE4m3Block;
   constexpr int kPer = D / 16;  // threads of a token's head
-  constexpr int kItem = E4M3 ? 1 : 2;
+  constexpr int kItem = KIND == kBf16 ? 2 : 1;
   __shared__ Token tokens[8];
   extern __shared__ __align__(16) uint4 ring[];  // [kSlots][2][kThreads]: a thread's own 16-byte pieces
   let_next_start();
   wait_for_previous();
   if (static_cast<int>(blockIdx.x) < page_blocks) {
-    store_keys_by_page<D, E4M3, INTER, SCAN>(p, segs, ring);
+    if constexpr (BLOCKS) store_blocks<D, KIND == kInt8Block, INTER, SCAN>(p, segs);
+    else store_keys_by_page<D, E4M3, INTER, SCAN>(p, segs, ring);
     return;
   }
   const int block = blockIdx.x - page_blocks;
-  // heads in the order queries, keys (unless they go by page), values
+  // heads in the order queries, keys (unless they go by page), values (unless blocks have scales)
   const int H_k = page_blocks ? 0 : p.c.H_kv, values = p.H_q + H_k;
   const int tid = threadIdx.x, P = 1 << p.c.log2_page, n = 1 << log2_tokens;
   const int j = tid % kPer, tt = (tid / kPer) & (n - 1), h0 = (tid / kPer) >> log2_tokens;
@@ -369,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 4)
   const bool packed = p.cu_new != nullptr;
   const int total = packed ? p.n_tokens : p.c.B * p.max_new;
   const int i0 = block << log2_tokens, i = i0 + tt;
-  const int heads = values + p.c.H_kv;
+  const int heads = BLOCKS ? p.H_q : values + p.c.H_kv;
 
   // channels of the thread: pieces of 8
   const int pairs = p.rot_dim >> 4;  // threads that rotate
@@ -461,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 4)
       *reinterpret_cast<uint4*>(to + c0) = out0;
       *reinterpret_cast<uint4*>(to + c1) = out1;
     }
-    if (is_q || t.page < 0) continue;
+    if (BLOCKS || is_q || t.page < 0) continue;
     char* row = (is_v ? p.c.v + t.page * p.c.v_page_bytes : p.c.k + t.page * p.c.k_page_bytes) +
                 ((static_cast<int64_t>(hh) << p.c.log2_page) + (t.pos & (P - 1))) * (D * kItem);
     if constexpr (E4M3) {
@@ -478,9 +680,18 @@ __global__ void __launch_bounds__(kThreads, 4)
   }
 }
 
-// The most pages a run of max_new tokens can touch.
+// Whether blocks of the grid go by page (for the summaries) or by block of tokens, and how many tokens that is.
+bool has_scaled_blocks(const AppendParams& p) { return p.c.kind >= kE4m3Block; }
+bool goes_by_page(const AppendParams& p) { return p.max_new > 0 && (p.c.summary || has_scaled_blocks(p)); }
+int log2_unit(const AppendParams& p) { return p.c.summary ? p.c.log2_page : 4; }
+int head_blocks(const AppendParams& p) {
+  const int heads = has_scaled_blocks(p) ? 2 * p.c.H_kv : p.c.H_kv;
+  return (heads + kThreads / 32 - 1) / (kThreads / 32);
+}
+
+// The most pages (or blocks) a run of max_new tokens can touch.
 int append_segments(const AppendParams& p) {
-  const int P = 1 << p.c.log2_page;
+  const int P = 1 << log2_unit(p);
   return (p.max_new + P - 2) / P + 1;
 }
 // Pages that blocks are launched for, and whether they are dealt out by a scan.  Packed tokens: every page but a
@@ -491,13 +702,12 @@ int append_segments(const AppendParams& p) {
 // blocks on.
 int64_t append_pages(const AppendParams& p, bool& scan) {
   const int64_t all = static_cast<int64_t>(append_segments(p)) * p.c.B;
-  const int64_t most = (p.n_tokens >> p.c.log2_page) + 2 * static_cast<int64_t>(p.c.B);
-  const int head_blocks = (p.c.H_kv + kThreads / 32 - 1) / (kThreads / 32);
-  scan = p.cu_new != nullptr && (all - most) * head_blocks > 4 * 608;
-  return (scan ? most : all) * head_blocks;
+  const int64_t most = (p.n_tokens >> log2_unit(p)) + 2 * static_cast<int64_t>(p.c.B);
+  scan = p.cu_new != nullptr && (all - most) * head_blocks(p) > 4 * 608;
+  return (scan ? most : all) * head_blocks(p);
 }
 
-template <int D, bool E4M3>
+template <int D, int KIND>
 bool launch(const AppendParams& p, cudaStream_t stream) {
   const int total = p.cu_new ? p.n_tokens : p.c.B * p.max_new;
   // tokens of a CTA: one while there are few (16 CTAs an SM at most), up to 8 that share the lookups
@@ -506,9 +716,9 @@ bool launch(const AppendParams& p, cudaStream_t stream) {
   const int blocks = total > 0 ? (total + (1 << log2_tokens) - 1) >> log2_tokens : 1;  // new_lens needs one
   bool scan = false;
   const int segs = append_segments(p);
-  const int pages = p.c.summary && p.max_new > 0 ? static_cast<int>(append_pages(p, scan)) : 0;
-  auto* kernel = p.interleaved ? (scan ? append_kernel<D, E4M3, true, true> : append_kernel<D, E4M3, true, false>)
-                               : (scan ? append_kernel<D, E4M3, false, true> : append_kernel<D, E4M3, false, false>);
+  const int pages = goes_by_page(p) ? static_cast<int>(append_pages(p, scan)) : 0;
+  auto* kernel = p.interleaved ? (scan ? append_kernel<D, KIND, true, true> : append_kernel<D, KIND, true, false>)
+                               : (scan ? append_kernel<D, KIND, false, true> : append_kernel<D, KIND, false, false>);
   return launch_after(kernel, dim3(pages + blocks), kThreads, kSlots * 2 * kThreads * 16, stream, p, log2_tokens, pages,
                       segs);
 }
@@ -517,12 +727,17 @@ bool launch(const AppendParams& p, cudaStream_t stream) {
 
 int64_t append_page_blocks(const AppendParams& p) {
   bool scan;
-  return p.c.summary && p.max_new > 0 ? append_pages(p, scan) : 0;
+  return goes_by_page(p) ? append_pages(p, scan) : 0;
 }
 
 int launch_kv_append(const AppendParams& p, cudaStream_t stream) {
-  const bool ok = p.c.d == 128 ? (p.c.e4m3 ? launch<128, true>(p, stream) : launch<128, false>(p, stream))
-                               : (p.c.e4m3 ? launch<64, true>(p, stream) : launch<64, false>(p, stream));
+  bool ok = false;
+  switch (p.c.kind) {
+    case kBf16: ok = p.c.d == 128 ? launch<128, kBf16>(p, stream) : launch<64, kBf16>(p, stream); break;
+    case kE4m3: ok = p.c.d == 128 ? launch<128, kE4m3>(p, stream) : launch<64, kE4m3>(p, stream); break;
+    case kE4m3Block: ok = p.c.d == 128 ? launch<128, kE4m3Block>(p, stream) : launch<64, kE4m3Block>(p, stream); break;
+    case kInt8Block: ok = p.c.d == 128 ? launch<128, kInt8Block>(p, stream) : launch<64, kInt8Block>(p, stream); break;
+  }
   return ok ? 0 : -1;
 }
 

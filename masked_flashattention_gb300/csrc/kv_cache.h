@@ -10,19 +10,26 @@ namespace cm {
 // Limit of each bounded wait inside the kernels (cm_set_wait_limit_ns; kept in api.cu).
 uint64_t wait_limit_ns();
 
+// How the cache holds keys and values (CM_KV_*): bf16; e4m3 with a scale for each head; e4m3 or int8 with a scale for
+// each block of 16 tokens and head.
+enum : int { kBf16 = 0, kE4m3 = 1, kE4m3Block = 2, kInt8Block = 3 };
+constexpr int kBlockTokens = 16;
+// Exponents of block scales are held to +-32: weights times values then stay within fp32 in any mixture of blocks.
+constexpr int kMaxBlockExp = 32;
+
 // The cache and the sequences of a call (cm_kv_cache and cm_kv_seqs, checked).
 struct KvView {
   char* k;
   char* v;
   int64_t k_page_bytes, v_page_bytes;  // distance of two pages
-  const float* k_scale;                // [H_kv], e4m3 only
+  const float* k_scale;                // [H_kv], or of blocks [num_pages][H_kv][page size / 16]; none for bf16
   const float* v_scale;
   int8_t* summary;                     // [num_pages][H_kv][2][d]
   float* summary_scale;                // [num_pages][H_kv]
   int32_t* status;
   const int32_t* table;                // [B][max_pages]
   const int32_t* lens;                 // [B]
-  int num_pages, log2_page, H_kv, d, e4m3;
+  int num_pages, log2_page, H_kv, d, kind;
   int B, max_pages;
 };
 
@@ -118,6 +125,11 @@ __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ---- device helpers shared by the kernels ---------------------------------------------------
+
+// Exponent of a block's scale as every kernel reads it: a power of two, held to 2^+-32.
+__device__ __forceinline__ int block_exponent(uint32_t bits) {
+  return min(max(static_cast<int>((bits >> 23) & 0xFFu) - 127, -kMaxBlockExp), kMaxBlockExp);
+}
 
 // Power of two 2^e, e within the normal range, by its bits.
 __device__ __forceinline__ float pow2_bits(int e) { return __int_as_float((e + 127) << 23); }

@@ -87,3 +87,67 @@ def pick(score, n, keep_first, keep_last):
     forced = [i < keep_first or i >= total - keep_last for i in range(total)]
     order = sorted(range(total), key=lambda i: (not forced[i], -score[i] if not forced[i] else 0, i))
     return sorted(order[:n])
+
+
+# ---- caches with a scale for each block of 16 tokens and head ----------------------------------
+BLOCK = 16
+
+
+def block_exponent(a: float, kind: str) -> int:
+    """e of the smallest 2^e with a <= top * 2^e, held to [-32, 32]; top = 127 (int8) or 448 (e4m3)."""
+    top = 127.0 if kind == "int8" else 448.0
+    if math.isinf(a):
+        return 32
+    e = -32
+    while e < 32 and a > top * 2.0 ** e:
+        e += 1
+    return e
+
+
+def stored(x, kind: str):
+    """Values [...] in units of the scale, in 64 bits, as the cache holds them (64-bit numbers)."""
+    if kind == "int8":
+        return torch.round(torch.nan_to_num(x.to(F64), 0.0)).clamp(-127, 127)
+    y = torch.where(x.isnan(), x, x.clamp(-448, 448))
+    return y.float().to(torch.float8_e4m3fn).to(F64)  # the products are exact in fp32
+
+
+class BlockRow:
+    """One head's keys or values of one sequence, in a cache with block scales: codes and exponents as lists of tokens
+    and blocks, changed call by call."""
+
+    def __init__(self, kind: str):
+        self.kind, self.codes, self.exps = kind, [], []
+
+    def append(self, x):
+        """x [n, d]: the new tokens of one call."""
+        lo, hi = len(self.codes), len(self.codes) + x.shape[0]
+        self.codes += [None] * x.shape[0]
+        for f in range(lo // BLOCK * BLOCK, hi, BLOCK):
+            first, last = max(f, lo), min(f + BLOCK, hi)
+            new = x[first - lo:last - lo].to(F64)
+            a = new.abs()
+            e = block_exponent(a[~a.isnan()].max().item() if (~a.isnan()).any() else 0.0, self.kind)
+            n = f // BLOCK
+            if first > f:
+                if e > self.exps[n]:
+                    for i in range(f, first):
+                        self.codes[i] = stored(self.codes[i] * 2.0 ** (self.exps[n] - e), self.kind)
+                    self.exps[n] = e
+                e = self.exps[n]
+            else:
+                self.exps.append(e)
+            for i in range(first, last):
+                self.codes[i] = stored(new[i - first] * 2.0 ** -e, self.kind)
+
+    def values(self):
+        """[tokens, d] in 64 bits."""
+        return torch.stack([c * 2.0 ** self.exps[i // BLOCK] for i, c in enumerate(self.codes)])
+
+
+def block_rows(pool, scales, table, h, positions):
+    """Values [n, d] in 64 bits of one head's tokens at the given positions of a sequence."""
+    P = pool.shape[2]
+    at, row = table[positions // P].long(), positions % P
+    x = pool.view(torch.uint8)[at, h, row].view(pool.dtype).to(F64)
+    return x * scales[at, h, row // BLOCK].to(F64)[:, None]
