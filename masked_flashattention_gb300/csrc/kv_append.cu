@@ -171,6 +171,28 @@ __device__ __forceinline__ bool find_page(const AppendParams& p, int item, int s
   }
   __shared__ int sums[kThreads / 32], found[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
+  if (p.c.B <= 64) {  // two steps of a warp at most: every warp for itself, without the block's barriers
+    for (int b0 = 0, before = 0; b0 < p.c.B; b0 += 32) {
+      int start, count, base, pages = 0;
+      if (b0 + lane < p.c.B && new_tokens(p, b0 + lane, start, count, base) && count > 0)
+        pages = ((start + count - 1) >> log2_unit) - (start >> log2_unit) + 1;
+      int sum = pages;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int x = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+        if (lane >= d) sum += x;
+      }
+      sum += before;
+      const uint32_t hit = __ballot_sync(0xFFFFFFFFu, item >= sum - pages && item < sum);
+      if (hit) {
+        b = b0 + __ffs(hit) - 1;
+        seg = item - __shfl_sync(0xFFFFFFFFu, sum - pages, __ffs(hit) - 1);
+        return true;
+      }
+      before = __shfl_sync(0xFFFFFFFFu, sum, 31);
+    }
+    return false;
+  }
   if (tid == 0) found[0] = -1;
   for (int b0 = 0, before = 0; b0 < p.c.B && before <= item; b0 += kThreads) {
     int start, count, base, pages = 0;
@@ -360,8 +382,9 @@ __device__ __forceinline__ int needed_exponent(float a) {
   const int x = static_cast<int>(u >> 23) - 127, e = INT8 ? x - 6 + (m > 0x7E0000u) : x - 8 + (m > 0x600000u);
   return min(max(e, -kMaxBlockExp), kMaxBlockExp);
 }
-// 8 fp32 values times a power of two as the cache holds them
-template <bool INT8>
+// 8 fp32 values times a power of two as the cache holds them.  PLAIN: int8, and none is NaN or beyond 127 then: added to
+// 1.5 * 2^23, a value is rounded to a whole number, halves to even, whose 8 bits are the sum's last.
+template <bool INT8, bool PLAIN>
 __device__ __forceinline__ uint2 pack8_block(const float (&x)[8], float times) {
   uint32_t w[2];
 #pragma unroll
@@ -370,7 +393,8 @@ __device__ __forceinline__ uint2 pack8_block(const float (&x)[8], float times) {
       uint32_t q[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c)  // NaN becomes 0
-        q[c] = static_cast<uint32_t>(min(max(__float2int_rn(x[4 * i + c] * times), -127), 127));
+        q[c] = PLAIN ? __float_as_uint(fmaf(x[4 * i + c], times, 12582912.f))
+                     : static_cast<uint32_t>(min(max(__float2int_rn(x[4 * i + c] * times), -127), 127));
       w[i] = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
     } else {
       uint32_t q[2];
@@ -419,16 +443,23 @@ __device__ __forceinline__ void take_in(uint2 a, uint2 b, float scale, uint32_t 
   }
 }
 
-// The second role where blocks have scales: one warp a head's keys or values of a block, or with summaries of all the
-// blocks of a page that the call touches.  A block's new rows are in the warp's registers at once (16 rows, 16
-// channels of one of 4 or 8 of them a lane and step), so they are read once: rotated, their largest magnitude taken,
-// the scale settled, then stored.  Earlier rows are read only where the scale grows (or for the summary).
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t c;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
+  return c;
+}
+
+// The second role where blocks have scales: one warp a head's keys or values of one to four blocks, or with summaries of
+// all the blocks of a page that the call touches.  A lane's pieces of a block's new rows (16 channels of one of 4 or 8 rows a
+// step) come into shared memory that no other thread reads.  They are gone through twice: rotated, with
+// their largest magnitude, and once that has settled the scale, stored.  Earlier rows are read only where the scale
+// grows (or for the summary).
 template <int D, bool INT8, bool INTER, bool SCAN>
-__device__ __forceinline__ void store_blocks(const AppendParams& p, int segs) {
+__device__ __forceinline__ void store_blocks(const AppendParams& p, int segs, int log2_unit, uint4* ring) {
   constexpr int kPer = D / 16, kRows = 32 / kPer, kSteps = kBlockTokens / kRows;
+  static_assert(kSteps <= kSlots, "a block's pieces fit the ring");
   const int tid = threadIdx.x, lane = tid & 31, P = 1 << p.c.log2_page;
   const bool whole_pages = p.c.summary != nullptr;
-  const int log2_unit = whole_pages ? p.c.log2_page : 4;
   const int head_blocks = (2 * p.c.H_kv + kThreads / 32 - 1) / (kThreads / 32);
   const int item = blockIdx.x / head_blocks;
   const int hh = (blockIdx.x - item * head_blocks) * (kThreads / 32) + tid / 32;
@@ -440,14 +471,24 @@ __device__ __forceinline__ void store_blocks(const AppendParams& p, int segs) {
   const int first = ((start >> log2_unit) + seg) << log2_unit;  // positions from here on
   const int lo = max(start, first), hi = min(start + count, first + (1 << log2_unit));
   if (lo >= hi) return;
-  const int page = p.c.table[static_cast<int64_t>(b) * p.c.max_pages + (first >> p.c.log2_page)];
-  const bool paged = static_cast<unsigned>(page) < static_cast<unsigned>(p.c.num_pages);
-  if (!paged && hh == 0 && lane == 0) set_status(p.c.status, kDevBadMeta, b);
   const int j = lane % kPer, sub = lane / kPer, pairs = is_v ? 0 : p.rot_dim >> 4;
   const bool turns = j < pairs;
   const int c0 = 8 * (turns ? j : 2 * j), c1 = 8 * (turns ? j + pairs : 2 * j + 1);
   const Strides& st = is_v ? p.vs : p.ks;
   const __nv_bfloat16* src = (is_v ? p.v : p.k) + h * st.head + (p.cu_new ? base * st.token : b * st.seq);
+  const uint32_t slots = smem_u32(ring) + tid * 16;
+  auto load_new = [&](int pos, int s) {
+    if (pos >= lo && pos < hi) {
+      const __nv_bfloat16* x = src + static_cast<int64_t>(pos - start) * st.token;
+      copy_async<16>(slots + (2 * s) * kThreads * 16, x + c0);
+      copy_async<16>(slots + (2 * s + 1) * kThreads * 16, x + c1);
+    }
+  };
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) load_new((lo & ~15) + s * kRows + sub, s);  // while their page is looked up
+  const int page = p.c.table[static_cast<int64_t>(b) * p.c.max_pages + (first >> p.c.log2_page)];
+  const bool paged = static_cast<unsigned>(page) < static_cast<unsigned>(p.c.num_pages);
+  if (!paged && hh == 0 && lane == 0) set_status(p.c.status, kDevBadMeta, b);
   const int64_t at = static_cast<int64_t>(paged ? page : 0) * p.c.H_kv + h;
   char* pool = (is_v ? p.c.v + (paged ? page : 0) * p.c.v_page_bytes : p.c.k + (paged ? page : 0) * p.c.k_page_bytes) +
                (static_cast<int64_t>(h) << p.c.log2_page) * D;
@@ -459,97 +500,121 @@ __device__ __forceinline__ void store_blocks(const AppendParams& p, int segs) {
     high[i] = 0xFF80FF80u;  // -inf
     low[i] = 0x7F807F80u;
   }
+  if (sums)  // blocks that the call leaves as they are count in the summary
 #pragma unroll 1
-  for (int f = sums ? first : lo & ~15; f < hi; f += kBlockTokens) {
+    for (int pos = first + sub; pos < (lo & ~15); pos += kRows) {
+      const int row = pos & (P - 1);
+      const char* from = pool + row * D;
+      take_in<INT8>(*reinterpret_cast<const uint2*>(from + c0), *reinterpret_cast<const uint2*>(from + c1),
+                    pow2_bits(block_exponent(__float_as_uint(scales[row >> 4]))), high, low);
+    }
+#pragma unroll 1
+  for (int f = lo & ~15; f < hi; f += kBlockTokens) {
     const int row = f & (P - 1);
     char* to = pool + row * D;
     const bool carried = lo > f;  // holds earlier tokens
     const int e_old = carried && paged ? block_exponent(__float_as_uint(scales[row >> 4])) : -kMaxBlockExp;
-    uint4 w[kSteps][2];
-    uint32_t top = 0;
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      const int r = s * kRows + sub, pos = f + r;
-      w[s][0] = w[s][1] = make_uint4(0, 0, 0, 0);
-      if (pos >= lo && pos < hi) {
-        const __nv_bfloat16* x = src + static_cast<int64_t>(pos - start) * st.token;
-        w[s][0] = __ldg(reinterpret_cast<const uint4*>(x + c0));
-        w[s][1] = __ldg(reinterpret_cast<const uint4*>(x + c1));
-      } else if (pos < lo && sums) {
-        const uint2 a = *reinterpret_cast<const uint2*>(to + r * D + c0), c = *reinterpret_cast<const uint2*>(to + r * D + c1);
-        w[s][0].x = a.x, w[s][0].y = a.y, w[s][1].x = c.x, w[s][1].y = c.y;
-      }
-    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    uint32_t top = 0;  // as whole numbers: NaN above all others
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       const int pos = f + s * kRows + sub;
       if (pos < lo || pos >= hi) continue;
+      uint4 w0 = ring[(2 * s) * kThreads + tid], w1 = ring[(2 * s + 1) * kThreads + tid];
       if (turns) {
         float2 cs[8];
         load_turn<INTER>(p.rope, static_cast<int64_t>(pos) * p.rot_dim, j, pairs, cs);
-        rotate_pieces<INTER>(w[s][0], w[s][1], cs);
+        rotate_pieces<INTER>(w0, w1, cs);
+        ring[(2 * s) * kThreads + tid] = w0;
+        ring[(2 * s + 1) * kThreads + tid] = w1;
       }
       if (p.k_out && !is_v) {
         __nv_bfloat16* out = p.k_out + h * p.kos.head + (p.cu_new ? base * p.kos.token : b * p.kos.seq) +
                              static_cast<int64_t>(pos - start) * p.kos.token;
-        *reinterpret_cast<uint4*>(out + c0) = w[s][0];
-        *reinterpret_cast<uint4*>(out + c1) = w[s][1];
+        *reinterpret_cast<uint4*>(out + c0) = w0;
+        *reinterpret_cast<uint4*>(out + c1) = w1;
       }
+      const uint32_t u[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        top = max2<false>(top, w[s][i].x & 0x7FFF7FFFu);
-        top = max2<false>(top, w[s][i].y & 0x7FFF7FFFu);
-        top = max2<false>(top, w[s][i].z & 0x7FFF7FFFu);
-        top = max2<false>(top, w[s][i].w & 0x7FFF7FFFu);
-      }
+      for (int i = 0; i < 8; ++i) top = max_u16x2(top, u[i] & 0x7FFF7FFFu);
     }
-    if (!paged) continue;
+    if (!paged) {
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) top = max2<false>(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-    const float2 tops = bf16x2_to_float2(top);
-    const int e = f + kBlockTokens <= lo ? e_old : max(e_old, needed_exponent<INT8>(fmaxf(tops.x, tops.y)));
-    const float scale = pow2_bits(e), inv = pow2_bits(-e);
+      for (int s = 0; s < kSteps; ++s) load_new(f + kBlockTokens + s * kRows + sub, s);
+      continue;
+    }
+    top = max_u16x2(top, top >> 16);
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) top = max_u16x2(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+    float a = __uint_as_float(top << 16);
+    const bool plain = a <= (INT8 ? 127.f : 448.f) * 4294967296.f;
+    if (!(a <= INFINITY)) {  // some are NaN: passed over
+      top = 0;
+#pragma unroll 1
+      for (int s = 0; s < kSteps; ++s) {
+        const int pos = f + s * kRows + sub;
+        if (pos < lo || pos >= hi) continue;
+        const uint4 w0 = ring[(2 * s) * kThreads + tid], w1 = ring[(2 * s + 1) * kThreads + tid];
+        const uint32_t u[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = max2<false>(top, u[i] & 0x7FFF7FFFu);
+      }
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) top = max2<false>(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+      const float2 tops = bf16x2_to_float2(top);
+      a = fmaxf(tops.x, tops.y);
+    }
+    const int e = max(e_old, needed_exponent<INT8>(a));
+    const float scale = pow2_bits(e), inv = pow2_bits(-e), fade = pow2_bits(e_old - e);
     const bool again = carried && e > e_old;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       const int r = s * kRows + sub, pos = f + r;
       const bool fresh = pos >= lo;
-      if (pos >= hi || !(fresh || again || sums)) continue;
+      if (pos >= hi || !(fresh || again || sums)) {
+        load_new(pos + kBlockTokens, s);
+        continue;
+      }
       uint2* to0 = reinterpret_cast<uint2*>(to + r * D + c0);
       uint2* to1 = reinterpret_cast<uint2*>(to + r * D + c1);
-      uint2 a, c;
+      uint2 u0, u1;
       float x[8];
       if (fresh) {
-        unpack8(w[s][0], x);
-        a = pack8_block<INT8>(x, inv);
-        unpack8(w[s][1], x);
-        c = pack8_block<INT8>(x, inv);
+        unpack8(ring[(2 * s) * kThreads + tid], x);
+        u0 = plain ? pack8_block<INT8, true>(x, inv) : pack8_block<INT8, false>(x, inv);
+        unpack8(ring[(2 * s + 1) * kThreads + tid], x);
+        u1 = plain ? pack8_block<INT8, true>(x, inv) : pack8_block<INT8, false>(x, inv);
+        load_new(pos + kBlockTokens, s);  // the next block's, now that these pieces are in registers
       } else {
-        a = sums ? make_uint2(w[s][0].x, w[s][0].y) : *to0;
-        c = sums ? make_uint2(w[s][1].x, w[s][1].y) : *to1;
+        load_new(pos + kBlockTokens, s);
+        u0 = *to0;
+        u1 = *to1;
         if (again) {
-          const float fade = pow2_bits(e_old - e);
-          unpack8_block<INT8>(a, x);
-          a = pack8_block<INT8>(x, fade);
-          unpack8_block<INT8>(c, x);
-          c = pack8_block<INT8>(x, fade);
+          unpack8_block<INT8>(u0, x);
+          u0 = pack8_block<INT8, true>(x, fade);
+          unpack8_block<INT8>(u1, x);
+          u1 = pack8_block<INT8, true>(x, fade);
         }
       }
       if (fresh || again) {
-        *to0 = a;
-        *to1 = c;
+        if (turns) {
+          *to0 = u0;
+          *to1 = u1;
+        } else {  // neighbours
+          *reinterpret_cast<uint4*>(to0) = make_uint4(u0.x, u0.y, u1.x, u1.y);
+        }
       }
-      if (sums) take_in<INT8>(a, c, scale, high, low);
+      if (sums) take_in<INT8>(u0, u1, scale, high, low);
     }
-    if (lane == 0 && f + kBlockTokens > lo) scales[row >> 4] = scale;
+    if (lane == 0) scales[row >> 4] = scale;
   }
   if (sums) write_summary<D, false>(p, at, high, low, 1.f, c0, c1, j, sub);
 }
 
 // Blocks 0 .. page_blocks-1 have the second role.
 template <int D, int KIND, bool INTER, bool SCAN>
-__global__ void __launch_bounds__(kThreads, KIND >= kE4m3Block ? 2 : 4)
-    append_kernel(const AppendParams p, int log2_tokens, int page_blocks, int segs) {
+__global__ void __launch_bounds__(kThreads, 4)
+    append_kernel(const AppendParams p, int log2_tokens, int page_blocks, int segs, int log2_unit) {
   constexpr bool E4M3 = KIND == kE4m3, BLOCKS = KIND >= kE4m3Block;
   constexpr int kPer = D / 16;  // threads of a token's head
   constexpr int kItem = KIND == kBf16 ? 2 : 1;
@@ -558,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, KIND >= kE4m3Block ? 2 : 4)
   let_next_start();
   wait_for_previous();
   if (static_cast<int>(blockIdx.x) < page_blocks) {
-    if constexpr (BLOCKS) store_blocks<D, KIND == kInt8Block, INTER, SCAN>(p, segs);
+    if constexpr (BLOCKS) store_blocks<D, KIND == kInt8Block, INTER, SCAN>(p, segs, log2_unit, ring);
     else store_keys_by_page<D, E4M3, INTER, SCAN>(p, segs, ring);
     return;
   }
@@ -629,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, KIND >= kE4m3Block ? 2 : 4)
         t.pos = start + place;
       }
     }
-    if (t.seq >= 0) {
+    if (!BLOCKS && t.seq >= 0) {
       t.page = p.c.table[static_cast<int64_t>(t.seq) * p.c.max_pages + (t.pos >> p.c.log2_page)];
       if (static_cast<unsigned>(t.page) >= static_cast<unsigned>(p.c.num_pages)) {
         set_status(p.c.status, kDevBadMeta, t.seq);
@@ -683,7 +748,13 @@ __global__ void __launch_bounds__(kThreads, KIND >= kE4m3Block ? 2 : 4)
 // Whether blocks of the grid go by page (for the summaries) or by block of tokens, and how many tokens that is.
 bool has_scaled_blocks(const AppendParams& p) { return p.c.kind >= kE4m3Block; }
 bool goes_by_page(const AppendParams& p) { return p.max_new > 0 && (p.c.summary || has_scaled_blocks(p)); }
-int log2_unit(const AppendParams& p) { return p.c.summary ? p.c.log2_page : 4; }
+// Blocks with scales: four a warp, within a page, where every warp of the GPU then still has some (the next block's
+// pieces are on their way while one is stored; 186 us for 42,000 tokens, 197 with one a warp).
+int log2_unit(const AppendParams& p) {
+  if (p.c.summary) return p.c.log2_page;
+  const int64_t tokens = p.cu_new ? p.n_tokens : static_cast<int64_t>(p.c.B) * p.max_new;
+  return tokens * 2 * p.c.H_kv < 152 * 32 * 64 ? 4 : p.c.log2_page < 6 ? p.c.log2_page : 6;
+}
 int head_blocks(const AppendParams& p) {
   const int heads = has_scaled_blocks(p) ? 2 * p.c.H_kv : p.c.H_kv;
   return (heads + kThreads / 32 - 1) / (kThreads / 32);
@@ -720,7 +791,7 @@ bool launch(const AppendParams& p, cudaStream_t stream) {
   auto* kernel = p.interleaved ? (scan ? append_kernel<D, KIND, true, true> : append_kernel<D, KIND, true, false>)
                                : (scan ? append_kernel<D, KIND, false, true> : append_kernel<D, KIND, false, false>);
   return launch_after(kernel, dim3(pages + blocks), kThreads, kSlots * 2 * kThreads * 16, stream, p, log2_tokens, pages,
-                      segs);
+                      segs, log2_unit(p));
 }
 
 }  // namespace
