@@ -17,10 +17,11 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libcm.so")
 
 SOURCES = ["compiler.cpp", "codegen.cpp", "preprocess.cu", "attn_fwd.cu", "attn_bwd.cu", "attn_dq.cu", "api.cu",
-           "attn_bwd_noalloc.cu", "kv_append.cu", "attn_decode.cu", "select_pages.cu",
+           "attn_bwd_noalloc.cu", "kv_append.cu", "attn_decode.cu", "attn_decode_bf16.cu",
+           "attn_decode_e4m3.cu", "attn_decode_e4m3_block.cu", "attn_decode_int8_block.cu", "select_pages.cu",
            "kv_pages.cu", "api_decode.cu"]
 HEADERS = ["program.h", "kernels.h", "ptx.cuh", "tma_host.h", "descriptor_core.cuh", "mask.cuh",
-           "kv_cache.h"]
+           "kv_cache.h", "attn_decode.h", "attn_decode.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
