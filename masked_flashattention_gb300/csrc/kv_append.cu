@@ -21,6 +21,7 @@
 // for an e4m3 cache one more after the division by the scale (the cache holds what k_out says).
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
+#include <type_traits>
 
 #include "kv_cache.h"
 #include "ptx.cuh"
@@ -450,9 +451,10 @@ __device__ __forceinline__ void take_in(uint2 a, uint2 b, float scale, uint32_t 
   }
 }
 
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+// Larger magnitudes of two pairs; NaN where one is NaN.
+__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
   uint32_t c;
-  asm("max.u16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
+  asm("{\n\t.reg .b32 x;\n\tabs.bf16x2 x, %2;\n\tmax.NaN.bf16x2 %0, %1, x;\n\t}" : "=r"(c) : "r"(a), "r"(b));
   return c;
 }
 
@@ -493,6 +495,18 @@ __device__ __forceinline__ void store_blocks(const AppendParams& p, int segs, in
   };
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) load_new((lo & ~15) + s * kRows + sub, s);  // while their page is looked up
+  // a block's rows of the rotation's table, into the cache that the heads' warps share
+  const int log2_lines = p.rot_dim > 64 ? 2 : p.rot_dim > 32 ? 1 : 0;  // of 128 bytes, of a row
+  auto warm = [&](int f) {
+#pragma unroll
+    for (int x = lane; x < 64; x += 32) {
+      const int pos = f + (x >> log2_lines), c = (x & ((1 << log2_lines) - 1)) * 32;
+      if (!is_v && x >> log2_lines < kBlockTokens && pos >= lo && pos < hi && c < p.rot_dim)
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(p.rope + static_cast<int64_t>(pos) * p.rot_dim + c));
+    }
+  };
+  const bool many = hi - lo >= kBlockTokens;
+  if (many) warm(lo & ~15);
   const int page = p.c.table[static_cast<int64_t>(b) * p.c.max_pages + (first >> p.c.log2_page)];
   const bool paged = static_cast<unsigned>(page) < static_cast<unsigned>(p.c.num_pages);
   if (!paged && hh == 0 && lane == 0) set_status(p.c.status, kDevBadMeta, b);
@@ -508,7 +522,7 @@ __device__ __forceinline__ void store_blocks(const AppendParams& p, int segs, in
     low[i] = 0x7F807F80u;
   }
   if (sums)  // blocks that the call leaves as they are count in the summary
-#pragma unroll 1
+#pragma unroll 4
     for (int pos = first + sub; pos < (lo & ~15); pos += kRows) {
       const int row = pos & (P - 1);
       const char* from = pool + row * D;
@@ -521,8 +535,9 @@ __device__ __forceinline__ void store_blocks(const AppendParams& p, int segs, in
     char* to = pool + row * D;
     const bool carried = lo > f;  // holds earlier tokens
     const int e_old = carried && paged ? block_exponent(__float_as_uint(scales[row >> 4])) : -kMaxBlockExp;
+    if (many) warm(f + kBlockTokens);
     asm volatile("cp.async.wait_all;" ::: "memory");
-    uint32_t top = 0;  // as whole numbers: NaN above all others
+    uint32_t top = 0;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       const int pos = f + s * kRows + sub;
@@ -543,16 +558,16 @@ __device__ __forceinline__ void store_blocks(const AppendParams& p, int segs, in
       }
       const uint32_t u[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) top = max_u16x2(top, u[i] & 0x7FFF7FFFu);
+      for (int i = 0; i < 8; ++i) top = max_abs_bf16x2(top, u[i]);
     }
     if (!paged) {
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) load_new(f + kBlockTokens + s * kRows + sub, s);
       continue;
     }
-    top = max_u16x2(top, top >> 16);
+    top = max_abs_bf16x2(top, top >> 16);
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) top = max_u16x2(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+    for (int d = 1; d < 32; d <<= 1) top = max_abs_bf16x2(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
     float a = __uint_as_float(top << 16);
     const bool plain = a <= (INT8 ? 127.f : 448.f) * 4294967296.f;
     if (!(a <= INFINITY)) {  // some are NaN: passed over
@@ -573,41 +588,54 @@ __device__ __forceinline__ void store_blocks(const AppendParams& p, int segs, in
     }
     const int e = max(e_old, needed_exponent<INT8>(a));
     const float scale = pow2_bits(e), inv = pow2_bits(-e), fade = pow2_bits(e_old - e);
-    const bool again = carried && e > e_old;
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      const int r = s * kRows + sub, pos = f + r;
-      const bool fresh = pos >= lo;
-      if (pos >= hi || !(fresh || again || sums)) {
-        load_new(pos + kBlockTokens, s);
-        continue;
-      }
-      uint2* to0 = reinterpret_cast<uint2*>(to + r * D + c0);
-      uint2* to1 = reinterpret_cast<uint2*>(to + r * D + c1);
-      uint2 u0, u1;
-      float x[8];
-      if (fresh) {
+    // new rows; the next block's pieces are asked for once these are in registers
+    auto store_new = [&](int s, auto is_plain, auto in_sums) {
+      const int pos = f + s * kRows + sub;
+      if (pos >= lo && pos < hi) {
+        uint2* out = reinterpret_cast<uint2*>(to + (s * kRows + sub) * D);
+        float x[8];
         unpack8(ring[(2 * s) * kThreads + tid], x);
-        u0 = plain ? pack8_block<INT8, true>(x, inv) : pack8_block<INT8, false>(x, inv);
+        const uint2 u0 = pack8_block<INT8, is_plain.value>(x, inv);
         unpack8(ring[(2 * s + 1) * kThreads + tid], x);
-        u1 = plain ? pack8_block<INT8, true>(x, inv) : pack8_block<INT8, false>(x, inv);
-        load_new(pos + kBlockTokens, s);  // the next block's, now that these pieces are in registers
-      } else {
-        load_new(pos + kBlockTokens, s);
-        u0 = *to0;
-        u1 = *to1;
-        if (again) {
-          unpack8_block<INT8>(u0, x);
-          u0 = pack8_block<INT8, true>(x, fade);
-          unpack8_block<INT8>(u1, x);
-          u1 = pack8_block<INT8, true>(x, fade);
+        const uint2 u1 = pack8_block<INT8, is_plain.value>(x, inv);
+        out[c0 >> 3] = u0;
+        out[c1 >> 3] = u1;
+        if constexpr (in_sums.value) take_in<INT8>(u0, u1, scale, high, low);
+      }
+      load_new(pos + kBlockTokens, s);
+    };
+    if (plain && !sums) {
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) store_new(s, std::true_type(), std::false_type());
+    } else if (plain) {
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) store_new(s, std::true_type(), std::true_type());
+    } else {
+#pragma unroll 1
+      for (int s = 0; s < kSteps; ++s) store_new(s, std::false_type(), std::true_type());
+    }
+    if (carried && (e > e_old || sums)) {  // earlier rows
+      uint2 u[kSteps][2];
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        const uint2* from = reinterpret_cast<const uint2*>(to + (s * kRows + sub) * D);
+        const bool in = f + s * kRows + sub < lo;
+        u[s][0] = in ? from[c0 >> 3] : make_uint2(0, 0);
+        u[s][1] = in ? from[c1 >> 3] : make_uint2(0, 0);
+      }
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        if (f + s * kRows + sub >= lo) continue;
+        uint2* out = reinterpret_cast<uint2*>(to + (s * kRows + sub) * D);
+        if (e > e_old) {
+          float x[8];
+          unpack8_block<INT8>(u[s][0], x);
+          out[c0 >> 3] = u[s][0] = pack8_block<INT8, true>(x, fade);
+          unpack8_block<INT8>(u[s][1], x);
+          out[c1 >> 3] = u[s][1] = pack8_block<INT8, true>(x, fade);
         }
+        if (sums) take_in<INT8>(u[s][0], u[s][1], scale, high, low);
       }
-      if (fresh || again) {
-        *to0 = u0;
-        *to1 = u1;
-      }
-      if (sums) take_in<INT8>(u0, u1, scale, high, low);
     }
     if (lane == 0) scales[row >> 4] = scale;
   }
@@ -783,7 +811,8 @@ int64_t append_pages(const AppendParams& p, bool& scan) {
 
 template <int D, int KIND>
 bool launch(const AppendParams& p, cudaStream_t stream) {
-  const int total = p.cu_new ? p.n_tokens : p.c.B * p.max_new;
+  const bool none = KIND >= kE4m3Block && p.H_q == 0;  // nothing goes by token
+  const int total = none ? 0 : p.cu_new ? p.n_tokens : p.c.B * p.max_new;
   // tokens of a CTA: one while there are few (16 CTAs an SM at most), up to 8 that share the lookups
   int log2_tokens = 0;
   while (log2_tokens < 3 && total >> log2_tokens > 152 * 16) ++log2_tokens;
