@@ -303,7 +303,9 @@ CM_API int cm_attn_bwd_noalloc(const cm_descriptor* desc, const void* q, const v
  *     infinity), and a NaN makes it NaN; the other channels do not change.  Weights are held in fp32: one
  *     below 2^-110 of a row's largest may count as 0, and 0 times an infinity is NaN.  Weights of at
  *     most 1 times values are summed before the division: beside a bf16 cache, where a row's keys times
- *     the largest |v| pass 2^127, an output may overflow. */
+ *     the largest |v| pass 2^127, an output may overflow.
+ *   - Beside 8-bit caches weights are rounded to fp16: to 11 bits each, and below 2^-21 of the row's largest to 2^-32 of
+ *     that.  With block scales this holds for the products of weights and their values' scales. */
 
 #define CM_KV_BF16 0
 #define CM_KV_E4M3 1
@@ -412,7 +414,8 @@ CM_API int cm_attn_decode_workspace_size(int B, int H_q, int H_kv, int d, size_t
  * o[b][h] = softmax_j(scale * q[b][h] . k[j]) v[j] over the visible j < lens[b], of key-value head
  * h / (H_q / H_kv).  q, o: bf16 [B][H_q][d] with strides in elements for {sequence, head}, multiples
  * of 8; lse: fp32 [B][H_q] in natural log, or NULL.  H_q is a multiple of H_kv.  (Beside an e4m3 cache,
- * channels of q below 2^-31 of their head's largest lose bits.)  o may be q with the same strides; otherwise
+ * channels of q below 2^-31 of their head's largest lose bits; beside block types all do, where the head's largest times
+ * scale passes 2^80.)  o may be q with the same strides; otherwise
  * outputs overlap nothing else, nor themselves (o_stride at least d).
  *   desc  NULL: every token is visible.  Else a descriptor of B samples with S >= lens[b] in the
  *         CM_FORM_VISIBLE form: the token sees what row lens[b] - 1 of the forward half says, cut
@@ -483,7 +486,8 @@ CM_API int cm_kv_status(const cm_kv_cache* cache, void* stream);
  *   status         device int32: 0, or the first device error (cm_kv_pages_status)
  * State, device int32 [B + 1][2], 8-byte aligned: for sequence b the pages {lo, hi} that it owns, which are the entries
  * [0, f) and [max(lo, f), hi) of its row below hi, with f = ceil(sinks / page_size); in row B {free pages, 0}.  Both
- * calls read `state` and write all of `new_state` (other memory); the next call goes on from there.  A new pool starts
+ * calls read `state` and write all of `new_state` (other memory); the next call goes on from there, so the calls on one pool
+ * run one after another (one stream, or ordered by events).  A new pool starts
  * with all pages in free_pages, {0, 0} for every sequence and {num_pages, 0}. */
 typedef struct cm_kv_pages {
   int32_t num_pages, page_size, B, max_pages, window, sinks;
@@ -513,7 +517,8 @@ CM_API int cm_kv_reserve(const cm_kv_pages* pages, const int32_t* state, int32_t
  * before the position lens[b] - window but not among the first f.  The rows keep their entries, which
  * are no longer the sequence's: a call that reads them reads what the page's new owner put there (attention under the same window does not).
  * After its end a row of the table is ready for another sequence with lens[b] = 0.
- * A sequence whose state is out of range keeps it and gives nothing back; a number that names no page goes into the list as it is
+ * Lengths must not fall behind a release by more than what the window still covers.  A sequence whose state is out of
+ * range, or under a window its length (beyond hi * page_size), keeps its state and gives nothing back; a number that names no page goes into the list as it is
  * (cm_kv_reserve will not hand it out), and pages beyond num_pages in the list are dropped; these record
  * CM_ERR_DEVICE_CHECK. */
 CM_API int cm_kv_release(const cm_kv_pages* pages, const int32_t* state, int32_t* new_state,

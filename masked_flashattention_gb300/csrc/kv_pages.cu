@@ -80,6 +80,7 @@ __device__ __forceinline__ bool give_back(const PagesParams& p, int b, Return& r
     r.to = own.y;
     r.left = make_int2(0, 0);
   } else if (p.window) {
+    if (held < 0 || held > static_cast<int64_t>(own.y) << p.log2_page) return false;
     r.to = min(own.y, max(held - p.window, 0) >> p.log2_page);
     if (r.to > r.at) r.left.x = r.to;
   }
@@ -118,7 +119,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) pages_kernel(const 
       Request r;
       good = request(p, b, r);
       n = r.need - r.hi;
-      if (p.cu_new && r.count < 0) atomicMin(&fall, b);
+      if (p.cu_new && p.cu_new[b + 1] < r.base) atomicMin(&fall, b);
     }
     if (!good && blockIdx.x == 0) set_status(p.status, kDevBadMeta, b);
     places[b] = good ? n : kBad;

@@ -64,6 +64,9 @@ def release(table, free, state, lens, done, window, sinks, P, num_pages):
         if not 0 <= lo <= hi <= len(table[b]):
             bad = True
             continue
+        if window and not done[b] and not 0 <= lens[b] <= hi * P:
+            bad = True
+            continue
         at = max(lo, first)
         if done[b]:
             places = list(range(min(first, hi))) + list(range(at, hi))

@@ -177,6 +177,27 @@ def test_what_is_out_of_range(B):
         y.check(bad=True)
 
 
+def test_lengths_out_of_range_under_a_window(B):
+    """A length that the pages do not cover gives nothing back, whatever a window would make of it; an ended one needs none."""
+    x = Both(B, 40, 5, 16, 16, window=5, sinks=1)
+    x.reserve([0] * 5, [100] * 5)
+    x.release([100, -2**31, 113, 2**31 - 1, -1], [0, 0, 0, 1, 0], bad=True)
+    assert x.state[:5] == [[5, 7], [0, 7], [0, 7], [0, 0], [0, 7]]
+    x.whole()
+
+
+def test_bounds_that_fall_past_32_bits(B):
+    """cu_new falls by more than 2^31: nothing behind is granted."""
+    x = Both(B, 40, 3, 8, 16)
+    cu = [0, 5, -2**31, 3]
+    slots = torch.full((5,), -7, dtype=torch.int64, device="cuda")
+    granted = torch.empty(3, dtype=torch.int32, device="cuda")
+    B.cm_kv_reserve(x.gpu, x.gpu.state, x.gpu.spare, _ints([0] * 3), 5, cu_new=_ints(cu), granted=granted, slots=slots)
+    assert granted.tolist() == [5, 0, 0] and B.cm_kv_pages_status(x.gpu) == B.CM_ERR_DEVICE_CHECK
+    assert slots.tolist() == [x.free[39] * 16 + i for i in range(5)]
+    assert x.gpu.spare.tolist() == [[0, 1], [0, 0], [0, 0], [39, 0]]
+
+
 def test_numbers_that_name_no_page(B):
     x = Both(B, 8, 2, 8, 16)
     x.free[6], x.free[3] = 99, -4
