@@ -233,46 +233,62 @@ __device__ __forceinline__ bool find_page(const AppendParams& p, int item, int s
 }
 
 // A page's summary from each lane's largest and smallest of its 16 channels, as stored (fp16 or bf16 pairs, times scale).
+// Lanes that hold the same channels halve them among themselves at every step, so that in the end each has 4 (or 2) of
+// the row's channels to itself, and the rest of the work is spread over the warp.
 template <int D, bool F16>
 __device__ __forceinline__ void write_summary(const AppendParams& p, int64_t at, uint32_t (&high)[8], uint32_t (&low)[8],
-                                              float scale, int c0, int c1, int j, int sub) {
+                                              float scale, int c0, int c1, int lane) {
   constexpr int kPer = D / 16;
-  float a = 0.f, most[16], least[16];
+  int first = 0;  // of the pairs that are the lane's
+  int n = 8;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int d = 16; d >= kPer; d >>= 1) {
+    n >>= 1;
+    const bool upper = lane & d;
+    first += upper ? n : 0;
 #pragma unroll
-    for (int d = kPer; d < 32; d <<= 1) {
-      high[i] = max2<F16>(high[i], __shfl_xor_sync(0xFFFFFFFFu, high[i], d));
-      low[i] = min2<F16>(low[i], __shfl_xor_sync(0xFFFFFFFFu, low[i], d));
+    for (int i = 0; i < 4; ++i) {
+      if (i >= n) break;
+      const uint32_t h = __shfl_xor_sync(0xFFFFFFFFu, upper ? high[i] : high[i + n], d);
+      const uint32_t l = __shfl_xor_sync(0xFFFFFFFFu, upper ? low[i] : low[i + n], d);
+      high[i] = max2<F16>(upper ? high[i + n] : high[i], h);
+      low[i] = min2<F16>(upper ? low[i + n] : low[i], l);
     }
-    const float2 m = value2<F16>(high[i], scale), l = value2<F16>(low[i], scale);
-    most[2 * i] = m.x;
-    most[2 * i + 1] = m.y;
-    least[2 * i] = l.x;
-    least[2 * i + 1] = l.y;
-    a = fmaxf(a, fmaxf(fmaxf(fabsf(m.x), fabsf(m.y)), fmaxf(fabsf(l.x), fabsf(l.y))));
+  }
+  constexpr int kPairs = kPer / 4;  // 2 of d = 128, 1 of 64
+  float a = 0.f;
+  float2 most[kPairs], least[kPairs];
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i) {
+    most[i] = value2<F16>(high[i], scale);
+    least[i] = value2<F16>(low[i], scale);
+    a = fmaxf(a, fmaxf(fmaxf(fabsf(most[i].x), fabsf(most[i].y)), fmaxf(fabsf(least[i].x), fabsf(least[i].y))));
   }
 #pragma unroll
-  for (int d = 1; d < kPer; d <<= 1) a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, d));
+  for (int d = 1; d < 32; d <<= 1) a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, d));
   const int e = scale_exponent(a);
   const float inv = pow2_bits(-e);
-  if (sub) return;
-  int8_t* to = p.c.summary + at * 2 * D;
+  uint32_t up = 0, down = 0;
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    uint32_t up[2] = {0, 0}, down[2] = {0, 0};
+  for (int i = 0; i < kPairs; ++i) {
+    const float m[2] = {most[i].x, most[i].y}, l[2] = {least[i].x, least[i].y};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int u = static_cast<int>(fminf(fmaxf(ceilf(most[8 * half + i] * inv), -127.f), 127.f));
-      const int l = static_cast<int>(fminf(fmaxf(floorf(least[8 * half + i] * inv), -127.f), 127.f));
-      up[i >> 2] |= static_cast<uint32_t>(u & 0xFF) << (8 * (i & 3));
-      down[i >> 2] |= static_cast<uint32_t>(l & 0xFF) << (8 * (i & 3));
+    for (int x = 0; x < 2; ++x) {
+      const int u = static_cast<int>(fminf(fmaxf(ceilf(m[x] * inv), -127.f), 127.f));
+      const int v = static_cast<int>(fminf(fmaxf(floorf(l[x] * inv), -127.f), 127.f));
+      up |= static_cast<uint32_t>(u & 0xFF) << (8 * (2 * i + x));
+      down |= static_cast<uint32_t>(v & 0xFF) << (8 * (2 * i + x));
     }
-    const int c = half ? c1 : c0;
-    *reinterpret_cast<uint2*>(to + c) = make_uint2(up[0], up[1]);
-    *reinterpret_cast<uint2*>(to + D + c) = make_uint2(down[0], down[1]);
   }
-  if (j == 0) p.c.summary_scale[at] = pow2_bits(e);
+  int8_t* to = p.c.summary + at * 2 * D + (first < 4 ? c0 : c1) + 2 * (first & 3);
+  if constexpr (kPairs == 2) {
+    *reinterpret_cast<uint32_t*>(to) = up;
+    *reinterpret_cast<uint32_t*>(to + D) = down;
+  } else {
+    *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(up);
+    *reinterpret_cast<uint16_t*>(to + D) = static_cast<uint16_t>(down);
+  }
+  if (lane == 0) p.c.summary_scale[at] = pow2_bits(e);
 }
 
 // A block's share of the second role.
@@ -379,7 +395,7 @@ __device__ __forceinline__ void store_keys_by_page(const AppendParams& p, int se
       low[i] = min2<E4M3>(low[i], x[i]);
     }
   }
-  if (paged) write_summary<D, E4M3>(p, static_cast<int64_t>(page) * p.c.H_kv + h, high, low, scale, c0, c1, j, sub);
+  if (paged) write_summary<D, E4M3>(p, static_cast<int64_t>(page) * p.c.H_kv + h, high, low, scale, c0, c1, lane);
 }
 
 // ---- blocks with a scale each ---------------------------------------------------------------------
@@ -604,10 +620,10 @@ __device__ __forceinline__ void store_blocks(const AppendParams& p, int segs, in
       }
       load_new(pos + kBlockTokens, s);
     };
-    if (plain && !sums) {
+    if ((plain || !INT8) && !sums) {
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) store_new(s, std::true_type(), std::false_type());
-    } else if (plain) {
+    } else if (plain || !INT8) {
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) store_new(s, std::true_type(), std::true_type());
     } else {
@@ -639,7 +655,7 @@ __device__ __forceinline__ void store_blocks(const AppendParams& p, int segs, in
     }
     if (lane == 0) scales[row >> 4] = scale;
   }
-  if (sums) write_summary<D, false>(p, at, high, low, 1.f, c0, c1, j, sub);
+  if (sums) write_summary<D, false>(p, at, high, low, 1.f, c0, c1, lane);
 }
 
 // Blocks 0 .. page_blocks-1 have the second role.
@@ -813,13 +829,13 @@ template <int D, int KIND>
 bool launch(const AppendParams& p, cudaStream_t stream) {
   const bool none = KIND >= kE4m3Block && p.H_q == 0;  // nothing goes by token
   const int total = none ? 0 : p.cu_new ? p.n_tokens : p.c.B * p.max_new;
+  bool scan = false;
+  const int segs = append_segments(p);
+  const int pages = goes_by_page(p) ? static_cast<int>(append_pages(p, scan)) : 0;
   // tokens of a CTA: one while there are few (16 CTAs an SM at most), up to 8 that share the lookups
   int log2_tokens = 0;
   while (log2_tokens < 3 && total >> log2_tokens > 152 * 16) ++log2_tokens;
   const int blocks = total > 0 ? (total + (1 << log2_tokens) - 1) >> log2_tokens : 1;  // new_lens needs one
-  bool scan = false;
-  const int segs = append_segments(p);
-  const int pages = goes_by_page(p) ? static_cast<int>(append_pages(p, scan)) : 0;
   auto* kernel = p.interleaved ? (scan ? append_kernel<D, KIND, true, true> : append_kernel<D, KIND, true, false>)
                                : (scan ? append_kernel<D, KIND, false, true> : append_kernel<D, KIND, false, false>);
   return launch_after(kernel, dim3(pages + blocks), kThreads, kSlots * 2 * kThreads * 16, stream, p, log2_tokens, pages,
