@@ -824,6 +824,7 @@ class KVPages:
             _kv_tensor(state, "state", _I32, (self.B + 1, 2), self.index)
             self.state, self.spare = state, torch.empty_like(state)
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self._rows, self._state_shape = torch.Size((self.B,)), torch.Size((self.B + 1, 2))
         self.c = cm_kv_pages(self.num_pages, page_size, self.B, self.max_pages, window, sinks,
                              page_table.data_ptr(), free_pages.data_ptr(), self.status.data_ptr())
         self._address = ctypes.addressof(self.c)
@@ -839,11 +840,16 @@ class KVPages:
 
 
 def _pages_state(pages: KVPages, state, new_state, lens):
-    _on_current_device(pages)
-    dev, shape = pages.index, (pages.B + 1, 2)
+    dev, shape, rows = pages.index, pages._state_shape, pages._rows
+    if (state.dtype is _I32 and new_state.dtype is _I32 and lens.dtype is _I32 and state.shape == shape
+            and new_state.shape == shape and lens.shape == rows
+            and dev == torch._C._cuda_getDevice() == state.get_device() == new_state.get_device() == lens.get_device()
+            and state.is_contiguous() and new_state.is_contiguous() and lens.is_contiguous()):
+        return
+    _on_current_device(pages)  # one of these says what is wrong
     _kv_tensor(state, "state", _I32, shape, dev)
     _kv_tensor(new_state, "new_state", _I32, shape, dev)
-    _kv_tensor(lens, "lens", _I32, (pages.B,), dev)
+    _kv_tensor(lens, "lens", _I32, rows, dev)
 
 
 def cm_kv_reserve(pages: KVPages, state, new_state, lens, n_tokens: int, max_new: int | None = None,
@@ -859,9 +865,9 @@ def cm_kv_reserve(pages: KVPages, state, new_state, lens, n_tokens: int, max_new
     if cu_new is not None:
         _kv_tensor(cu_new, "cu_new", _I32, (B + 1,), dev)
     if n_new is not None:
-        _kv_tensor(n_new, "n_new", _I32, (B,), dev)
+        _kv_tensor(n_new, "n_new", _I32, pages._rows, dev)
     if granted is not None:
-        _kv_tensor(granted, "granted", _I32, (B,), dev)
+        _kv_tensor(granted, "granted", _I32, pages._rows, dev)
     if slots is not None:
         _kv_tensor(slots, "slots", torch.int64, (B, n_tokens) if cu_new is None else (n_tokens,), dev)
     if not (0 <= n_tokens < 1 << 31 and (max_new is None or 0 <= max_new < 1 << 31)):
@@ -878,7 +884,7 @@ def cm_kv_release(pages: KVPages, state, new_state, lens, done=None, stream=None
     lie behind the pool's window.  state and new_state: int32 [B + 1, 2]."""
     _pages_state(pages, state, new_state, lens)
     if done is not None:
-        _kv_tensor(done, "done", _I32, (pages.B,), pages.index)
+        _kv_tensor(done, "done", _I32, pages._rows, pages.index)
     rc = _serving()[5](pages._address, state.data_ptr(), new_state.data_ptr(), lens.data_ptr(), _ptr(done),
                        _kv_stream(pages, stream))
     if rc != CM_OK:

@@ -23,14 +23,23 @@
 // renewed only when a score passes it, and then put 2^8 above that maximum (all in log2 units), which
 // bounds p by 1 and spares the cross-lane maximum on most tiles; beside an e4m3 cache p is fp16 and taken
 // 2^15 larger (kLift).  P is rounded to the values' 16-bit type for the second product; sums, maxima and O are fp32.
-// An e4m3 cache is widened to fp16 (exactly) between shared memory and the product; queries become
+// An 8-bit cache is widened to fp16 (exactly) between shared memory and the product; queries become
 // fp16 scaled by a power of two per head so that none overflows (scale_q).
+// With a scale for each block of 16 keys, half a tile, the fetching warp hands the four exponents of a tile's blocks
+// along with it.  The keys' is a factor of the scores.  The values' is added to the scores in log2 units, so that a weight is
+// that of the stored numbers and the running maximum bounds it however far scales lie apart; the sum of the weights
+// takes it off again.  Neither is an instruction more a score than one scale a head takes.
+// Under a sliding window a row's tiles are those of the first keys and of the last (WINDOW, kernels of their own: as a
+// further case of the mask's intervals they took 46.9 us instead of 45.6 in the case below, and the calls without one slowed by 1 to 3 %).
 //
 // Measured (8 key-value heads of 128, 4 query heads each, bf16): 64 sequences of up to 16384 keys, 331 us =
 // 7.0 TB/s, 103 % of the copy bandwidth; one of 131071, 84 us = 6.4 TB/s; 200 of up to 333, 17.3 us.  What
 // stands above the bytes is the start, 4 us from the launch to the first tile on its way (length, place, page
 // number: one load behind another) and up to 4 more until the memory's address translations are warm, and the end,
 // 4 to 5 us where rows are split (join, launch, join).  One CTA a head took 52 ms for the one of 131071.
+// With block scales: the 64 sequences, int8, 178 us = 6.5 TB/s, 95 %; the one of 131071, e4m3, 49.5 us; 40 of up to 32768
+// with 16 heads a group, int8, 70 us (67 with one scale a head, e4m3: the widening of the bytes holds both).  Windows: 256 sequences
+// under 1024 keys and 16 sinks, int8, 45 us = 4.2 TB/s (start, row ends and join); one of 100,003 under 4096, bf16, 9.0 us.
 #pragma once
 #include <cuda_fp16.h>
 #include <atomic>
