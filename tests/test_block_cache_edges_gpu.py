@@ -182,3 +182,46 @@ def test_append_in_place_and_without_queries(B, kind, d, rot, inter):
             assert torch.equal(getattr(c, x).view(torch.uint8), getattr(caches[0], x).view(torch.uint8))
             a, b = (getattr(y, x + "_scale").nan_to_num(-1.0) for y in (c, caches[0]))
             assert torch.equal(a, b)
+
+
+def test_the_second_loop_of_the_readme(B):
+    """The README's loop without end as it stands there: prompts of different lengths, then tokens; one sequence ends."""
+    import os
+    import re
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    blocks = re.findall(r"```python\n(.*?)```", open(os.path.join(root, "README.md")).read(), re.S)
+    code, = (x for x in blocks if "KVPages.alloc" in x)
+    gen = torch.Generator().manual_seed(88)
+    Bn, H, Hq, d, num_pages = 2, 2, 4, 64, 9
+    counts, over = [[130, 70], [1, 1], [1, 2], [3, 1]], [[0, 0], [0, 1], [0, 0], [0, 0]]
+
+    def ints(x):
+        return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+    def draw(h, t):
+        return torch.randn(Bn, h, t, d, generator=gen).to(torch.bfloat16).cuda()
+
+    steps = [(draw(H, max(c)), draw(H, max(c)), draw(Hq, max(c)), ints(c), ints(x)) for c, x in zip(counts, over)]
+    keep = [(k.clone(), v.clone(), q.clone()) for k, v, q, _, _ in steps]
+    rope = _rope(512, d, gen)
+    names = {"torch": torch, "cm": B, "num_pages": num_pages, "max_pages": 8, "H_kv": H, "d": d, "B": Bn, "rope": rope.cuda(),
+             "steps": steps, "lens": ints([0, 0]), "after": ints([0, 0])}
+    exec(code, names)
+    cache, pages = names["cache"], names["pages"]
+    assert names["lens"].tolist() == [135, 3] and B.cm_kv_status(cache) == B.CM_OK and B.cm_kv_pages_status(pages) == B.CM_OK
+    assert pages.state.tolist() == [[0, 3], [0, 1], [num_pages - 4, 0]]
+    # the values as the oracle's blocks hold them (the second sequence since its end), and the last step's attention
+    values = [[K.BlockRow("int8") for _ in range(H)] for _ in range(Bn)]
+    for (_, v, _), c, x in zip(keep, counts, over):
+        for b in range(Bn):
+            for h in range(H):
+                values[b][h].append(v[b, h, :c[b]].cpu())
+                if x[b]:
+                    values[b][h] = K.BlockRow("int8")
+    table = pages.page_table.cpu()
+    for b, n in ((0, 135), (1, 3)):
+        for h in range(H):
+            assert torch.equal(K.block_rows(cache.v.cpu(), cache.v_scale.cpu(), table[b], h, torch.arange(n)), values[b][h].values())
+    q = torch.stack([K.rotate(keep[-1][2][b, :, counts[-1][b] - 1].cpu(), rope[n - 1, :, 0], rope[n - 1, :, 1], False)[0]
+                     for b, n in ((0, 135), (1, 3))]).to(torch.bfloat16)
+    _check(cache, pages.page_table, q, names["o"], names["lse"], 1 / math.sqrt(d), lambda b, g: torch.arange([135, 3][b]))
