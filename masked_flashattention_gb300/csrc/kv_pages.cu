@@ -8,8 +8,9 @@
 // for one another, and then takes its share of the page numbers and slots, a warp a piece of a sequence.  Input and
 // output state are separate memory, so no block's reading meets another's writing.  Prefix sums make
 // the result the same as that of a loop over the sequences; there are no atomics but the status word's and the block's own.
-// Measured: a step of 256 sequences 3.1 us (either call), of which a launch is 2.2; 500 prompts, 483,000 slots, 9.1 us; 2000
-// sequences that end with 1.28 million pages 6.7 us.  With blocks of 512 threads, 64-bit sums and one slot a lane: 3.5, 12.4 and 10.1 us.
+// Measured: a step of 256 sequences 2.8 us (reserve) and 3.2 (release), of which a launch is 2.2; 500 prompts, 483,000 slots, 9.3 us (9.7 and 14.3 with
+// pieces of 512 and 2048 slots); 2000
+// sequences that end with 1.28 million pages 6.7 us.  With blocks of 512 threads and 64-bit sums: 3.5, 3.4, 12.4 and 10.1 us.
 #include <cstdint>
 
 #include "kv_cache.h"
@@ -19,7 +20,7 @@ namespace cm {
 namespace {
 
 constexpr int kSms = 152;           // blocks of 1024 threads, or as many threads in smaller ones
-constexpr int kTokens = 512;        // slots of a warp's piece: two a lane and step, all steps' page numbers on their way at once
+constexpr int kTokens = 1024;       // slots of a warp's piece, one a lane and step, page numbers of eight steps on their way at once
 constexpr int kEntries = 256;       // page numbers of a warp's piece (at most 64 pieces a sequence), the same
 constexpr int kShort = -1, kBad = -2;  // instead of a place in the list: too few pages, out of range
 
@@ -225,49 +226,40 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) pages_kernel(const 
         const int page = p.free_pages[free - 1 - place - k];
         return static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages) ? page : -1;
       };
-      if (place >= 0) {
+      if (p.slots == nullptr) {
+        if (place >= 0) {
 #pragma unroll 4
-        for (int k = piece * 32 + lane; k < r.need - r.hi; k += pieces * 32) {
-          const int page = fresh(k);
-          if (page < 0) set_status(p.status, kDevBadMeta, b);
-          row[r.hi + k] = page;
+          for (int k = piece * 32 + lane; k < r.need - r.hi; k += pieces * 32) {
+            const int page = fresh(k);
+            if (page < 0) set_status(p.status, kDevBadMeta, b);
+            row[r.hi + k] = page;
+          }
         }
+        continue;
       }
-      if (p.slots == nullptr || r.count == 0) continue;
+      if (r.count == 0) continue;
+      // with slots, a new page's first token is one of these: its lane writes the table's entry too
       int64_t* slots = p.slots + (p.cu_new ? r.base : static_cast<int64_t>(b) * p.n_tokens);
-      // pairs of slots that lie on 16 bytes; the piece's bounds lie on pairs, but the sequence's ends may not
-      const int odd = static_cast<int>(reinterpret_cast<uintptr_t>(slots) >> 3) & 1;
-      constexpr int kSteps = kTokens / 64;
-      const int first = piece * kTokens + 2 * lane - odd;
-      auto page_at = [&](int i) {  // of token i
-        const int k = (r.held + i) >> p.log2_page;
-        return k < r.hi ? row[k] : fresh(k - r.hi);
-      };
-      int page[kSteps];
+      constexpr int kSteps = 8;
+      const int end = min(r.count, (piece + 1) * kTokens);
+#pragma unroll 1
+      for (int first = piece * kTokens + lane; first < end; first += kSteps * 32) {
+        int page[kSteps];
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        const int i = first + s * 64;
-        page[s] = place >= 0 && i + 1 >= 0 && i < r.count ? page_at(max(i, 0)) : -1;
-      }
+        for (int s = 0; s < kSteps; ++s) {
+          const int i = first + s * 32, k = (r.held + i) >> p.log2_page;
+          page[s] = place >= 0 && i < end ? (k < r.hi ? row[k] : fresh(k - r.hi)) : -1;
+        }
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        const int i = first + s * 64;
-        if (i + 1 < 0 || i >= r.count) continue;
-        auto slot = [&](int x, int of) -> int64_t {
-          return static_cast<unsigned>(of) < static_cast<unsigned>(p.num_pages)
-                     ? (static_cast<int64_t>(of) << p.log2_page) + ((r.held + x) & (P - 1))
-                     : -1;
-        };
-        int second = page[s];
-        if (place >= 0 && i >= 0 && i + 1 < r.count && ((r.held + i + 1) & (P - 1)) == 0) second = page_at(i + 1);
-        const int64_t a = slot(i, page[s]), c = slot(i + 1, second);
-        const bool has0 = i >= 0, has1 = i + 1 < r.count;
-        if (place >= 0 && ((has0 && a < 0) || (has1 && c < 0))) set_status(p.status, kDevBadMeta, b);
-        if (has0 && has1) {
-          *reinterpret_cast<longlong2*>(slots + i) = make_longlong2(a, c);
-        } else {
-          if (has0) slots[i] = a;
-          if (has1) slots[i + 1] = c;
+        for (int s = 0; s < kSteps; ++s) {
+          const int i = first + s * 32, pos = r.held + i, k = pos >> p.log2_page;
+          if (i >= end) break;
+          const bool good = static_cast<unsigned>(page[s]) < static_cast<unsigned>(p.num_pages);
+          if (place >= 0) {
+            if (k >= r.hi && (pos & (P - 1)) == 0) row[k] = page[s];
+            if (!good) set_status(p.status, kDevBadMeta, b);
+          }
+          slots[i] = good ? (static_cast<int64_t>(page[s]) << p.log2_page) + (pos & (P - 1)) : -1;
         }
       }
     }
@@ -302,7 +294,7 @@ int launch(const PagesParams& p, int pieces, cudaStream_t stream) {
 }  // namespace
 
 int launch_kv_reserve(const PagesParams& p, cudaStream_t stream) {
-  return launch<false>(p, (p.max_new + 1 + kTokens - 1) / kTokens, stream);  // a row may begin in the middle of a pair
+  return launch<false>(p, p.max_new > kTokens ? (p.max_new + kTokens - 1) / kTokens : 1, stream);
 }
 
 int launch_kv_release(const PagesParams& p, cudaStream_t stream) {
