@@ -1343,7 +1343,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND, NB>::kThreads, 1)
 // Joins the parts of a row that several CTAs hold: CTA x's header says how many there are, its own
 // second part first, then the first parts of the CTAs behind it.  One block a head, one thread a channel.
 template <int D, int KIND, int NB>
-__global__ void __launch_bounds__(D) join_kernel(const __grid_constant__ DecodeArgs a) {
+__global__ void __launch_bounds__(D, NB == 1 ? 1 : 1024 / D) join_kernel(const __grid_constant__ DecodeArgs a) {
   constexpr int kHeads = 8 * NB;
   constexpr int kAtOnce = 16;  // parts whose loads are in flight
   const int h = blockIdx.y;
