@@ -37,9 +37,9 @@
 // stands above the bytes is the start, 4 us from the launch to the first tile on its way (length, place, page
 // number: one load behind another) and up to 4 more until the memory's address translations are warm, and the end,
 // 4 to 5 us where rows are split (join, launch, join).  One CTA a head took 52 ms for the one of 131071.
-// With block scales: the 64 sequences, int8, 178 us = 6.5 TB/s, 95 %; the one of 131071, e4m3, 49.5 us; 40 of up to 32768
+// With block scales: the 64 sequences, int8, 177 us = 6.5 TB/s, 96 %; the one of 131071, e4m3, 49.5 us; 40 of up to 32768
 // with 16 heads a group, int8, 70 us (67 with one scale a head, e4m3: the widening of the bytes holds both).  Windows: 256 sequences
-// under 1024 keys and 16 sinks, int8, 45 us = 4.2 TB/s (start, row ends and join); one of 100,003 under 4096, bf16, 9.0 us.
+// under 1024 keys and 16 sinks, int8, 43.8 us = 4.4 TB/s (start, row ends and join); one of 100,003 under 4096, bf16, 8.9 us.
 #pragma once
 #include <cuda_fp16.h>
 #include <atomic>
@@ -1343,7 +1343,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND, NB>::kThreads, 1)
 // Joins the parts of a row that several CTAs hold: CTA x's header says how many there are, its own
 // second part first, then the first parts of the CTAs behind it.  One block a head, one thread a channel.
 template <int D, int KIND, int NB>
-__global__ void __launch_bounds__(D, NB == 1 ? 1 : 1024 / D) join_kernel(const __grid_constant__ DecodeArgs a) {
+__global__ void __launch_bounds__(D, (NB == 1 ? 512 : 1024) / D) join_kernel(const __grid_constant__ DecodeArgs a) {
   constexpr int kHeads = 8 * NB;
   constexpr int kAtOnce = 16;  // parts whose loads are in flight
   const int h = blockIdx.y;
