@@ -131,7 +131,7 @@ __device__ __forceinline__ void rotate16(float (&lo)[8], float (&hi)[8], const f
 
 // Channels of a lane's two pieces of 8: partners of a rotation for the first `pairs` lanes of a row, then as far apart as the
 // lanes are many, so that what the lanes read or write at once lies side by side (neighbouring pieces instead took 200 us for
-// 42,000 tokens without rotation, 171 as it is).
+// 42,000 tokens without rotation, int8, 158 as it is).
 __device__ __forceinline__ int first_piece(int j, int pairs) { return 8 * (j < pairs ? j : j + pairs); }
 template <int PER>
 __device__ __forceinline__ int second_piece(int j, int pairs) { return 8 * (j < pairs ? j + pairs : j + PER); }
@@ -801,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, 4)
 bool has_scaled_blocks(const AppendParams& p) { return p.c.kind >= kE4m3Block; }
 bool goes_by_page(const AppendParams& p) { return p.max_new > 0 && (p.c.summary || has_scaled_blocks(p)); }
 // Blocks with scales: four a warp, within a page, where every warp of the GPU then still has some (the next block's
-// pieces are on their way while one is stored; 186 us for 42,000 tokens, 197 with one a warp).
+// pieces are on their way while one is stored; 42,000 tokens took 197 us with one a warp, 186 with four).
 int log2_unit(const AppendParams& p) {
   if (p.c.summary) return p.c.log2_page;
   const int64_t tokens = p.cu_new ? p.n_tokens : static_cast<int64_t>(p.c.B) * p.max_new;

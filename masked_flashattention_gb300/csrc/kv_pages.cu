@@ -8,9 +8,9 @@
 // for one another, and then takes its share of the page numbers and slots, a warp a piece of a sequence.  Input and
 // output state are separate memory, so no block's reading meets another's writing.  Prefix sums make
 // the result the same as that of a loop over the sequences; there are no atomics but the status word's and the block's own.
-// Measured: a step of 256 sequences 2.8 us (reserve) and 3.2 (release), of which a launch is 2.2; 500 prompts, 483,000 slots, 9.3 us (9.7 and 14.3 with
-// pieces of 512 and 2048 slots); 2000
-// sequences that end with 1.28 million pages 6.7 us.  With blocks of 512 threads and 64-bit sums: 3.5, 3.4, 12.4 and 10.1 us.
+// Measured: a step of 256 sequences 2.8 us (reserve) and 3.2 (release), of which a launch is 2.2; 500 prompts, 483,000
+// slots, 9.3 us (9.7 and 14.3 with pieces of 512 and 2048 slots); 2000 sequences that end with 1.28 million pages
+// 6.7 us.  With blocks of 512 threads and 64-bit sums: 3.5, 3.4, 12.4 and 10.1 us.
 #include <cstdint>
 
 #include "kv_cache.h"
@@ -20,7 +20,7 @@ namespace cm {
 namespace {
 
 constexpr int kSms = 152;           // blocks of 1024 threads, or as many threads in smaller ones
-constexpr int kTokens = 1024;       // slots of a warp's piece, one a lane and step, page numbers of eight steps on their way at once
+constexpr int kTokens = 1024;       // slots of a warp's piece, one a lane and step; eight steps' page numbers are on their way at once
 constexpr int kEntries = 256;       // page numbers of a warp's piece (at most 64 pieces a sequence), the same
 constexpr int kShort = -1, kBad = -2;  // instead of a place in the list: too few pages, out of range
 
