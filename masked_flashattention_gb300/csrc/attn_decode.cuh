@@ -490,6 +490,31 @@ __device__ __forceinline__ bool warp_wait(const WaitCtl& w, uint32_t bar, uint32
   return __all_sync(0xFFFFFFFFu, got);
 }
 
+// Two fp32 operations an instruction, each rounded as by itself.
+struct F2 {
+  float x, y;
+};
+__device__ __forceinline__ uint64_t as_pair(F2 a) {
+  uint64_t p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(a.x), "f"(a.y));
+  return p;
+}
+__device__ __forceinline__ F2 from_pair(uint64_t p) {
+  F2 a;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a.x), "=f"(a.y) : "l"(p));
+  return a;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  uint64_t c;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(c) : "l"(as_pair(a)), "l"(as_pair(b)));
+  return from_pair(c);
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(as_pair(a)), "l"(as_pair(b)), "l"(as_pair(c)));
+  return from_pair(d);
+}
+
 // Exponents of a tile's block scales (keys' two, then values' two), a byte each.
 __device__ __forceinline__ uint32_t pack_exponents(uint32_t k0, uint32_t k1, uint32_t v0, uint32_t v1) {
   const uint32_t a = __byte_perm(block_exponent(k0), block_exponent(k1), 0x0040);
@@ -811,9 +836,13 @@ __device__ __forceinline__ void compute_tile(State<D, KIND, NB>& t, uint32_t k_a
 #pragma unroll
       for (int n = 0; n < NB; ++n)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          s2[i][n][x] += s[i][n][x];
-          s[i][n][x] = fmaf(s2[i][n][x], t.scale[n][x & 1] * ks, lv - t.m[n][x & 1]);
+        for (int x = 0; x < 4; x += 2) {
+          const F2 sum = add2({s[i][n][x], s[i][n][x + 1]}, {s2[i][n][x], s2[i][n][x + 1]});
+          s2[i][n][x] = sum.x;
+          s2[i][n][x + 1] = sum.y;
+          const F2 over = fma2(sum, {t.scale[n][0] * ks, t.scale[n][1] * ks}, {lv - t.m[n][0], lv - t.m[n][1]});
+          s[i][n][x] = over.x;
+          s[i][n][x + 1] = over.y;
         }
     }
     if (!whole) hide();
@@ -871,8 +900,16 @@ __device__ __forceinline__ void compute_tile(State<D, KIND, NB>& t, uint32_t k_a
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         e[x] = ex2_approx(kBlocks ? s[i][n][x] : s[i][n][x] - (x & 1 ? m1 : m0));
-        if constexpr (kBlocks) t.l[n][x & 1] = fmaf(e[x], pow2_bits(-exponent_at(exps, 2 + i)), t.l[n][x & 1]);
-        else t.l[n][x & 1] += e[x];
+        if constexpr (!kBlocks) t.l[n][x & 1] += e[x];
+      }
+      if constexpr (kBlocks) {
+        const float iv = pow2_bits(-exponent_at(exps, 2 + i));
+#pragma unroll
+        for (int x = 0; x < 4; x += 2) {
+          const F2 l = fma2({e[x], e[x + 1]}, {iv, iv}, {t.l[n][0], t.l[n][1]});
+          t.l[n][0] = l.x;
+          t.l[n][1] = l.y;
+        }
       }
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
