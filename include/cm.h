@@ -371,7 +371,10 @@ typedef struct cm_kv_seqs {
  *           rot_dim channels (a multiple of 16, at most d; 0: no rotation, rope NULL) are rotated
  *           in pairs (i, i + rot_dim / 2), or (2i, 2i + 1) if interleaved:
  *           (x, y) -> (x cos - y sin, y cos + x sin), every product and sum rounded to fp32 once.
- *   new_lens device int32 [B] (may be NULL, not lens): receives lens[b] + the tokens appended. */
+ *   new_lens device int32 [B] (may be NULL, not lens, not granted): receives lens[b] + the tokens appended.
+ *   granted packed tokens only: device int32 [B] (may be NULL: all), the tokens that each sequence may append, as
+ *           cm_kv_reserve gives them.  Sequence b appends the first granted[b] of its own, which must be 0 to all of them;
+ *           the others count as tokens of no sequence.  (Padded tokens say the same by n_new.) */
 typedef struct cm_kv_new {
   const void* k;
   const void* v;
@@ -385,6 +388,7 @@ typedef struct cm_kv_new {
   int32_t rot_dim, interleaved, rope_len;
   const float* rope;
   int32_t* new_lens;
+  const int32_t* granted;
 } cm_kv_new;
 
 /* Append: token i of sequence b gets position p = lens[b] + i; its key and query are rotated to p
@@ -399,7 +403,7 @@ typedef struct cm_kv_new {
  * a block holds depends on how many calls its tokens came in, by these roundings alone.  No calibration goes before, and an outlier
  * costs 16 tokens of one head their precision.
  * A sequence whose length or token count is out of range (lens[b] < 0, more than max_new tokens,
- * tokens outside n_tokens, positions past the table or rope_len) appends nothing (new_lens[b] =
+ * tokens outside n_tokens, granted[b] below 0 or above its tokens, positions past the table or rope_len) appends nothing (new_lens[b] =
  * lens[b]), and tokens of a page outside the pool are left out (their q_out and k_out are written);
  * both record CM_ERR_DEVICE_CHECK.  Tokens of no sequence, and their outputs, are left alone.
  * Sequences must not append to a page they share. */
@@ -476,8 +480,8 @@ CM_API int cm_kv_status(const cm_kv_cache* cache, void* stream);
 
 /* The pages of a pool and the page tables that are made of them, on the device: cm_kv_reserve takes pages
  * for the tokens to come out of a list of free ones, cm_kv_release puts them back.  A step of a serving
- * loop is reserve, append (cm_kv_append with n_new = granted), attention, release; nothing of it is read on the
- * host, so it can be captured into one graph.
+ * loop is reserve, append (cm_kv_append with n_new = granted, or packed tokens with granted beside cu_new), attention, release;
+ * nothing of it is read on the host, so it can be captured into one graph.
  *   num_pages, page_size, B, max_pages  as in cm_kv_cache and cm_kv_seqs (same limits)
  *   window, sinks  window 0: sequences keep all their pages until they end.  Else pages that hold no token
  *                  which a token to come sees under cm_attn_decode_window(window, sinks) are given back.
@@ -500,7 +504,8 @@ typedef struct cm_kv_pages {
  * (cu_new, n_new, n_tokens, max_new): its row gets the pages it lacks, from the end of the list, in
  * the order of the sequences.  From the first sequence on for which too few are left, sequences that need a page get none.
  *   granted  device int32 [B] (may be NULL; not lens, not n_new): the tokens that may be appended, all of a
- *            sequence's or 0.
+ *            sequence's or 0.  A row that was granted nothing keeps its entries, which may name pages that are another
+ *            sequence's by now, so an append that does not heed `granted` would write there.
  *   slots    device int64, [n_tokens] for packed tokens, [B][n_tokens] for padded ones (may be NULL): each new token's
  *            place in the pool, page * page_size + row; -1 where none was granted.  Places of no token are left alone.
  * A sequence whose length, token count or state is out of range (as in cm_kv_append; lo * page_size <= lens[b] <= hi *

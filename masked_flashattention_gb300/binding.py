@@ -82,7 +82,7 @@ class cm_kv_new(ctypes.Structure):
                 ("n_tokens", ctypes.c_int32), ("max_new", ctypes.c_int32),
                 ("H_q", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
                 ("interleaved", ctypes.c_int32), ("rope_len", ctypes.c_int32),
-                ("rope", ctypes.c_void_p), ("new_lens", ctypes.c_void_p)]
+                ("rope", ctypes.c_void_p), ("new_lens", ctypes.c_void_p), ("granted", ctypes.c_void_p)]
 
 
 _lib = None
@@ -566,7 +566,7 @@ def _kv_tensor(t, name, dtype, shape, device: int):
 # objects of their own that take them as bytes.
 _I32 = torch.int32
 _SEQS = struct.Struct("2i2P")      # cm_kv_seqs, field by field
-_NEW = struct.Struct("5P15q2P6i2P")  # cm_kv_new
+_NEW = struct.Struct("5P15q2P6i3P")  # cm_kv_new
 _TWO = struct.Struct("2q")
 assert _SEQS.size == ctypes.sizeof(cm_kv_seqs) and _NEW.size == ctypes.sizeof(cm_kv_new)
 _calls = None
@@ -643,14 +643,15 @@ def _addr(t):
 
 def cm_kv_append(cache: KVCache, page_table, lens, k, v, q=None, q_out=None, k_out=None, rope=None,
                  interleaved: bool = False, cu_new=None, n_new=None, max_new: int | None = None,
-                 new_lens=None, stream=None) -> None:
+                 new_lens=None, stream=None, granted=None) -> None:
     """Store the new tokens' keys and values behind the lens[b] tokens that each sequence holds,
     rotating keys (and queries, into q_out) to their positions.  With cu_new (int32 [B + 1]) the
     tokens are packed, k, v [n, H_kv, d] and q [n, H_q, d]; without it they are padded, [B, H, T, d],
     and n_new (int32 [B]) says how many of T each sequence has (all of them where it is not given).
     max_new: the most tokens of any sequence (default: as many as the tensors hold).  rope: fp32
     [positions, rot_dim / 2, 2] of cosines and sines.  new_lens (int32 [B]) receives the new
-    lengths."""
+    lengths.  granted (int32 [B], packed tokens): of each sequence's tokens only the first so many, as reserve_pages
+    says; padded tokens take it as n_new."""
     B, seqs = _kv_seqs(cache, page_table, lens)
     dev, packed = cache.index, cu_new is not None
     shape, ks = _tokens(k, "k", cache, packed)
@@ -678,6 +679,10 @@ def cm_kv_append(cache: KVCache, page_table, lens, k, v, q=None, q_out=None, k_o
         _kv_tensor(cu_new, "cu_new", torch.int32, (B + 1,), dev)
     elif n_new is not None:
         _kv_tensor(n_new, "n_new", torch.int32, (B,), dev)
+    if granted is not None:
+        if not packed:
+            raise ValueError("granted is for packed tokens; padded ones take it as n_new")
+        _kv_tensor(granted, "granted", torch.int32, (B,), dev)
     if rope is not None:
         rope_len, half, two = rope.shape
         if two != 2:
@@ -689,7 +694,7 @@ def cm_kv_append(cache: KVCache, page_table, lens, k, v, q=None, q_out=None, k_o
     tok = _NEW.pack(
         k.data_ptr(), v.data_ptr(), _addr(q), _addr(q_out), _addr(k_out), *ks, *vs, *qs, *qos, *kos,
         _addr(cu_new), _addr(n_new), n, n if max_new is None else max_new, H_q, rot_dim,
-        interleaved, rope_len, _addr(rope), _addr(new_lens))
+        interleaved, rope_len, _addr(rope), _addr(new_lens), _addr(granted))
     rc = _serving()[0](cache._address, seqs, tok, _kv_stream(cache, stream))
     if rc != CM_OK:
         raise CMError(rc, "cm_kv_append")
@@ -857,7 +862,8 @@ def cm_kv_reserve(pages: KVPages, state, new_state, lens, n_tokens: int, max_new
     """Pages out of the pool for the tokens that each sequence is about to append behind its lens[b]: packed ones
     (cu_new int32 [B + 1]; n_tokens of all sequences) or padded ones (n_new int32 [B] of n_tokens each, all of
     them where it is not given).  max_new: the most tokens of any sequence (default n_tokens).  granted
-    (int32 [B]): the tokens that may be appended, all of a sequence's or 0.  slots (int64 [n_tokens], padded [B,
+    (int32 [B]): the tokens that may be appended, all of a sequence's or 0; cm_kv_append takes it as granted beside cu_new,
+    or as n_new for padded tokens.  slots (int64 [n_tokens], padded [B,
     n_tokens]): page * page_size + row of every token, -1 where none was granted.  state and new_state: int32
     [B + 1, 2]."""
     _pages_state(pages, state, new_state, lens)

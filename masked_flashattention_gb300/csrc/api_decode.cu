@@ -220,6 +220,7 @@ CM_API int cm_kv_append(const cm_kv_cache* cache, const cm_kv_seqs* seqs, const 
   if (t->cu_new ? (t->n_new || !good_ints(t->cu_new)) : (t->n_new && !good_ints(t->n_new)))
     return CM_ERR_INVALID_ARG;
   if (!t->cu_new && !t->n_new && t->max_new != t->n_tokens) return CM_ERR_INVALID_ARG;
+  if (t->granted && (!t->cu_new || !good_ints(t->granted) || t->granted == t->new_lens)) return CM_ERR_INVALID_ARG;
   if (t->rot_dim < 0 || t->rot_dim > cache->d || t->rot_dim % 16 != 0) return CM_ERR_INVALID_ARG;
   if (t->rot_dim ? (!good_ptr(t->rope) || t->rope_len < 1) : t->rope != nullptr)
     return CM_ERR_INVALID_ARG;
@@ -241,6 +242,7 @@ CM_API int cm_kv_append(const cm_kv_cache* cache, const cm_kv_seqs* seqs, const 
   p.kos = strides3(t->k_out_stride);
   p.cu_new = t->cu_new;
   p.n_new = t->n_new;
+  p.granted = t->granted;
   p.n_tokens = t->n_tokens;
   p.max_new = t->max_new;
   p.H_q = t->q ? t->H_q : 0;

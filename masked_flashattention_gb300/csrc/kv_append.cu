@@ -109,10 +109,15 @@ __device__ __forceinline__ bool new_tokens(const AppendParams& p, int b, int& st
   } else {
     count = p.n_new ? p.n_new[b] : p.n_tokens;
   }
+  bool good = start >= 0 && base >= 0 && count >= 0 && count <= p.max_new &&
+              static_cast<int64_t>(base) + count <= p.n_tokens;
+  if (p.granted) {  // of its tokens, the first so many
+    const int given = p.granted[b];
+    good = good && given >= 0 && given <= count;
+    count = given;
+  }
   const int64_t end = static_cast<int64_t>(start) + count;
-  return start >= 0 && base >= 0 && count >= 0 && count <= p.max_new &&
-         static_cast<int64_t>(base) + count <= p.n_tokens &&
-         end <= (static_cast<int64_t>(p.c.max_pages) << p.c.log2_page) &&
+  return good && end <= (static_cast<int64_t>(p.c.max_pages) << p.c.log2_page) &&
          (p.rot_dim == 0 || count == 0 || end <= p.rope_len);
 }
 

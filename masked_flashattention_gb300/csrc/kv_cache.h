@@ -42,7 +42,7 @@ struct AppendParams {
   const __nv_bfloat16 *k, *v, *q;
   __nv_bfloat16 *q_out, *k_out;
   Strides ks, vs, qs, qos, kos;
-  const int32_t *cu_new, *n_new;
+  const int32_t *cu_new, *n_new, *granted;
   int n_tokens, max_new, H_q;
   int rot_dim, interleaved, rope_len;
   const float* rope;
