@@ -162,21 +162,20 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 // Two of the four 8-bit numbers of x as fp16x2, exact: bytes 0 and 1, or 2 and 3; ODD: bytes 0 and 2, or 1 and 3.
-// A whole number n is the fp16 1024 + (n + 128), whose bits are 0x6400 + (n + 128), less 1152; RAISED leaves both steps out and gives
-// the bits n + 128, which as fp16 are (n + 128) * 2^-24.
-template <int KIND, bool ODD = false, bool RAISED = false>
+// A whole number n is the fp16 1024 + (n + 128), whose bits are 0x6400 + (n + 128), less 1152.  (Keys as the bits n + 128 alone,
+// which as fp16 are (n + 128) * 2^-24, with the sum's excess taken off in fp32, were 0.4 to 1.2 % faster; but a score was then off
+// by the rounding of 128 * sum |q|, whatever the keys were.)
+template <int KIND, bool ODD = false>
 __device__ __forceinline__ void widen(uint32_t x, uint32_t& lo, uint32_t& hi) {
   if constexpr (KIND == kInt8Block) {
     x ^= 0x80808080u;
-    const uint32_t top = RAISED ? 0u : 0x64646464u;
+    const uint32_t top = 0x64646464u;
     lo = __byte_perm(x, top, ODD ? 0x4240 : 0x4140);
     hi = __byte_perm(x, top, ODD ? 0x4341 : 0x4342);
-    if constexpr (!RAISED) {
-      const __half2 less = __half2half2(__ushort_as_half(0x6480));
-      const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&lo), less), z = __hsub2(*reinterpret_cast<const __half2*>(&hi), less);
-      lo = *reinterpret_cast<const uint32_t*>(&y);
-      hi = *reinterpret_cast<const uint32_t*>(&z);
-    }
+    const __half2 less = __half2half2(__ushort_as_half(0x6480));
+    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&lo), less), z = __hsub2(*reinterpret_cast<const __half2*>(&hi), less);
+    lo = *reinterpret_cast<const uint32_t*>(&y);
+    hi = *reinterpret_cast<const uint32_t*>(&z);
   } else {
     if constexpr (ODD) x = __byte_perm(x, 0, 0x3120);
     asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
@@ -665,7 +664,7 @@ __device__ __forceinline__ void read_q(const DecodeArgs& a, int row, int n, int 
 // whose largest value is below 2^-112 stays below 2^14.)
 template <int D, int KIND, int NB>
 __device__ __forceinline__ void scale_q(const DecodeArgs& a, int row, int lane, uint32_t (&q)[NB][D / 16][2],
-                                        float (&scale)[NB][2], float (&raise)[NB][2]) {
+                                        float (&scale)[NB][2]) {
   const float base = a.p.scale * 1.4426950408889634f * (KIND == kE4m3 ? a.p.c.k_scale[row_index(a, row).h] : 1.f);
 #pragma unroll
   for (int n = 0; n < NB; ++n) {
@@ -693,22 +692,6 @@ __device__ __forceinline__ void scale_q(const DecodeArgs& a, int row, int lane, 
           q[n][s][x] = *reinterpret_cast<const uint32_t*>(&f);
         }
       float mine = base * pow2_bits(e);
-      if constexpr (KIND == kInt8Block) {  // the keys are raised by 128 and 2^-24 of themselves
-        float sum = 0.f;
-#pragma unroll
-        for (int s = 0; s < D / 16; ++s)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&q[n][s][x]));
-            sum += f.x + f.y;
-          }
-        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
-        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
-        sum *= -128.f / 16777216.f;
-        raise[n][0] = __shfl_sync(0xFFFFFFFFu, sum, (lane & 3) * 8);
-        raise[n][1] = __shfl_sync(0xFFFFFFFFu, sum, (lane & 3) * 8 + 4);
-        mine *= 16777216.f;
-      }
       // times a block's scale of at most 2^32 it stays finite, so that a key of zeros scores 0 beside any query
       if constexpr (KIND >= kE4m3Block) mine = fminf(fmaxf(mine, -0x1p95f), 0x1p95f);
       scale[n][0] = __shfl_sync(0xFFFFFFFFu, mine, (lane & 3) * 8);  // heads of the lane's columns
@@ -731,7 +714,6 @@ template <int D, int KIND, int NB>
 struct State {
   uint32_t q[NB][D / 16][2];
   float scale[NB][2];
-  float raise[NB][2];  // int8: what the sum of a score starts from
   float m[NB][2], l[NB][2];
   float o[NB][D / 16][4];
 };
@@ -753,10 +735,7 @@ __device__ __forceinline__ void compute_tile(State<D, KIND, NB>& t, uint32_t k_a
 #pragma unroll
     for (int n = 0; n < NB; ++n)
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        s[i][n][x] = KIND == kInt8Block ? t.raise[n][x & 1] : 0.f;
-        s2[i][n][x] = 0.f;
-      }
+      for (int x = 0; x < 4; ++x) s[i][n][x] = s2[i][n][x] = 0.f;
   // S^T = K Q^T: matrices of ldmatrix are (keys 0-7, 8-15) x (pieces 2j, 2j+1)
   constexpr int kSteps = D * (k8 ? 1 : 2) / 32, kGroup = kSteps < 4 ? kSteps : 4;
   const int row = lane & 15, col = lane >> 4;
@@ -779,8 +758,8 @@ __device__ __forceinline__ void compute_tile(State<D, KIND, NB>& t, uint32_t k_a
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             uint32_t f[4];
-            widen<KIND, false, true>(w[j][i][2 * x], f[0], f[2]);
-            widen<KIND, false, true>(w[j][i][2 * x + 1], f[1], f[3]);
+            widen<KIND>(w[j][i][2 * x], f[0], f[2]);
+            widen<KIND>(w[j][i][2 * x + 1], f[1], f[3]);
 #pragma unroll
             for (int n = 0; n < NB; ++n)
               mma16816<true>(x ? s2[i][n] : s[i][n], f, t.q[n][2 * (j0 + j) + x][0], t.q[n][2 * (j0 + j) + x][1]);
@@ -1044,7 +1023,7 @@ __device__ __forceinline__ void compute(const DecodeArgs& a, char* smem, uint32_
 #pragma unroll
         for (int n = 0; n < NB; ++n) read_q<D, KIND>(a, row, n, lane, t.q[n]);
       }
-      scale_q<D, KIND, NB>(a, row, lane, t.q, t.scale, t.raise);
+      scale_q<D, KIND, NB>(a, row, lane, t.q, t.scale);
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
         t.m[n][0] = t.m[n][1] = -INFINITY;

@@ -1,0 +1,75 @@
+"""Scores beside caches with block scales where their sums are hardest: queries of one sign beside small stored numbers and
+zeros."""
+import math
+
+import pytest
+import torch
+
+from oracle import kv_cache as K
+from tests.test_block_cache_gpu import _check, _filled
+from tests.test_kv_cache_gpu import BF16_HALF, F32_HALF, F64
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def B():
+    from masked_flashattention_gb300 import binding
+    binding.lib()
+    return binding
+
+
+def _stored(pool, x):
+    """x [d or 1] into every row of the pool, as whole numbers."""
+    pool.view(torch.uint8).copy_(x.to(pool.dtype).view(torch.uint8).expand(pool.shape))
+
+
+def _one_sign(shape, gen):
+    """Sizes spread over 2^-12 .. 2^6, so that sums of them do not come out even."""
+    return (2.0 ** (18 * torch.rand(shape, generator=gen) - 12)).to(torch.bfloat16).cuda()
+
+
+@pytest.mark.parametrize("kind,d,P,group", [("int8", 128, 32, 4), ("int8", 64, 16, 12), ("e4m3", 128, 16, 3)])
+def test_keys_of_zeros_score_zero(B, kind, d, P, group):
+    """Every product is 0, so every score is, beside queries of one sign and any size: with the bound of the other tests,
+    which for a sum of zeros leaves the weights' rounding alone."""
+    gen = torch.Generator().manual_seed(91)
+    lens, H = [90, 33, 700], 2
+    cache, table, n = _filled(B, lens, H, P, d, kind, gen)
+    _stored(cache.k, torch.zeros(1, device="cuda"))
+    cache.k_scale.copy_(torch.where(cache.k_scale.isnan(), cache.k_scale, 4.0))
+    q = _one_sign((3, H * group, d), gen)
+    for sign in (1, -1):
+        o, lse = B.decode_attention(cache, table, n, sign * q)
+        _check(cache, table, sign * q, o, lse, 1 / math.sqrt(d), lambda b, g: torch.arange(lens[b]))
+
+
+@pytest.mark.parametrize("kind,d,P,group", [("int8", 128, 64, 4), ("int8", 64, 16, 16), ("e4m3", 64, 32, 2)])
+def test_small_numbers_beside_queries_of_one_sign(B, kind, d, P, group):
+    """Stored keys of 0 and now and then -1 or 1, as in a block whose scale an outlier set: a score is off by its own sum's rounding, which
+    goes by the magnitudes of its products."""
+    gen = torch.Generator().manual_seed(92)
+    lens, H = [300, 1, 77], 2
+    cache, table, n = _filled(B, lens, H, P, d, kind, gen)
+    small = (torch.randint(-8, 9, cache.k.shape, generator=gen) / 8).trunc().cuda()
+    cache.k.view(torch.uint8).copy_(small.to(cache.k.dtype).view(torch.uint8))
+    cache.k_scale.copy_(torch.where(cache.k_scale.isnan(), cache.k_scale, 4.0))
+    q = _one_sign((3, H * group, d), gen)
+    o, lse = (x.double().cpu() for x in B.decode_attention(cache, table, n, q))
+    k, v, ks, vs, host = (x.cpu() for x in (cache.k, cache.v, cache.k_scale, cache.v_scale, table))
+    for b in range(3):
+        for g in range(H):
+            pos, hs = torch.arange(lens[b]), slice(group * g, group * (g + 1))
+            kk, vv = K.block_rows(k, ks, host[b], g, pos), K.block_rows(v, vs, host[b], g, pos)
+            want, wl, size, mag = K.decode(q[b, hs].cpu(), kk, vv, d ** -0.5)
+            ds = (d + 8) * 2 * F32_HALF * size + 128 * F32_HALF
+            sums = lens[b] / 8 * 2 * F32_HALF + 2.0 ** -18
+            assert ((lse[b, hs] - wl).abs() <= ds + sums + 2.0 ** -20 * (1 + wl.abs())).all(), (b, g)
+            # Scores span 2^100 and more here.  Beside 2^-11 of itself a weight (with its value's scale) is off by half of fp16's
+            # smallest number, 2^-25; the row's largest is 2^7 at least, so by 2^-32 of that, times a stored number of at most 127
+            # or 448, for each of n keys.
+            p = torch.exp(d ** -0.5 * q[b, hs].cpu().to(F64) @ kk.T - wl[:, None])
+            scale = vs[host[b, pos // P].long(), g, pos % P // 16].to(F64)
+            lost = 2.0 ** -32 * (p * scale).amax(1, keepdim=True) * (127 if kind == "int8" else 448) * lens[b]
+            bound = BF16_HALF * want.abs() + (2.0 ** -11 + 2 * ds + sums) * mag + lost
+            assert ((o[b, hs] - want).abs() <= bound).all(), (b, g, ((o[b, hs] - want).abs() / bound).max())
