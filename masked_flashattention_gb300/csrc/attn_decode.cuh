@@ -58,6 +58,10 @@ constexpr float kRenew = 8.f;       // log2 units a score may pass the maximum b
 // largest: with 2^8, a million keys of 2^-25 each beside one large one lost 3 % of the sum.
 template <int KIND>
 constexpr float kLift = KIND != kBf16 ? 7.f : -kRenew;
+// What the reference starts from.  With block scales a score is taken over it in the same step that scales it, so it is a
+// number: a score of -inf over a reference of -inf would be NaN, and not the 0 that its weight is.
+template <int KIND>
+constexpr float kLowest = KIND >= kE4m3Block ? -3.402823466e38f : -INFINITY;
 constexpr size_t kSmemMax = 232448;
 
 // flags of a tile
@@ -806,8 +810,8 @@ __device__ __forceinline__ void compute_tile(State<D, KIND, NB>& t, uint32_t k_a
   };
   if constexpr (kBlocks) {
     // A key's score gets the log of its value's scale: weights are then those of the stored numbers, and none is
-    // beyond what the reference allows.  s becomes the score over the reference at once (+inf over a
-    // reference of -inf, so that it is renewed).
+    // beyond what the reference allows.  s becomes the score over the reference at once (any number is far over the
+    // one that a row starts from, so that it is renewed).
     float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -847,7 +851,7 @@ __device__ __forceinline__ void compute_tile(State<D, KIND, NB>& t, uint32_t k_a
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) s[i][n][x] -= t.m[n][x & 1] == -INFINITY ? 0.f : t.m[n][x & 1];
+          for (int x = 0; x < 4; ++x) s[i][n][x] -= t.m[n][x & 1];
     }
   } else {
 #pragma unroll
@@ -1026,7 +1030,7 @@ __device__ __forceinline__ void compute(const DecodeArgs& a, char* smem, uint32_
       scale_q<D, KIND, NB>(a, row, lane, t.q, t.scale);
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
-        t.m[n][0] = t.m[n][1] = -INFINITY;
+        t.m[n][0] = t.m[n][1] = kLowest<KIND>;
         t.l[n][0] = t.l[n][1] = 0.f;
 #pragma unroll
         for (int j = 0; j < D / 16; ++j)

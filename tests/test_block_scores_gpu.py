@@ -1,5 +1,5 @@
 """Scores beside caches with block scales where their sums are hardest: queries of one sign beside small stored numbers and
-zeros."""
+zeros, and scores of minus infinity."""
 import math
 
 import pytest
@@ -8,6 +8,7 @@ import torch
 from oracle import kv_cache as K
 from tests.test_block_cache_gpu import _check, _filled
 from tests.test_kv_cache_gpu import BF16_HALF, F32_HALF, F64
+from tests.test_window_gpu import _visible
 
 pytestmark = pytest.mark.gpu
 
@@ -73,3 +74,27 @@ def test_small_numbers_beside_queries_of_one_sign(B, kind, d, P, group):
             lost = 2.0 ** -32 * (p * scale).amax(1, keepdim=True) * (127 if kind == "int8" else 448) * lens[b]
             bound = BF16_HALF * want.abs() + (2.0 ** -11 + 2 * ds + sums) * mag + lost
             assert ((o[b, hs] - want).abs() <= bound).all(), (b, g, ((o[b, hs] - want).abs() / bound).max())
+
+
+@pytest.mark.parametrize("kind,d,P,group", [("e4m3", 64, 16, 3), ("e4m3", 128, 64, 8), ("e4m3", 64, 32, 16), ("int8", 64, 16, 3), ("int8", 128, 128, 8)])
+def test_rows_whose_keys_all_score_minus_infinity(B, kind, d, P, group):
+    """An infinite query beside keys that are negative in its channel: the row gets o = 0 and lse = -inf, alone in its group
+    and with all of it, in one tile and in many; the other heads are what they were."""
+    gen = torch.Generator().manual_seed(93)
+    lens, H, at = [20, 700, 65], 2, 9
+    cache, table, n = _filled(B, lens, H, P, d, kind, gen)
+    below = torch.randint(1, 100, cache.k.shape[:-1], generator=gen).neg().float().cuda()
+    cache.k.view(torch.uint8)[..., at] = below.to(cache.k.dtype).view(torch.uint8)
+    q = torch.randn(3, H * group, d, generator=gen).to(torch.bfloat16).cuda()
+    hit = torch.zeros(3, H * group, dtype=torch.bool)
+    hit[0, 0] = hit[1, 1] = hit[1, group + 2] = hit[2, group:] = True
+    bad = q.clone()
+    bad[hit.cuda(), at] = math.inf
+    for more in ({}, {"window": 50, "sinks": 3}):
+        want = B.decode_attention(cache, table, n, q, **more)
+        o, lse = B.decode_attention(cache, table, n, bad, **more)
+        assert not o[hit.cuda()].any() and (lse[hit.cuda()] == -math.inf).all()
+        # a warp's heads renew their references together, so the other heads keep their bounds, not their bits
+        o[hit.cuda()], lse[hit.cuda()] = want[0][hit.cuda()], want[1][hit.cuda()]
+        _check(cache, table, q, o, lse, 1 / math.sqrt(d),
+               lambda b, g: _visible(lens[b], 50, 3) if more else torch.arange(lens[b]))
