@@ -160,6 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) pages_kernel(const 
       places[b] = static_cast<int>(min(at, static_cast<Sum>(p.num_pages)));
       at += n;
       most = static_cast<int>(min(at, static_cast<Sum>(p.num_pages)));
+      if (blockIdx.x == 0 && at > p.num_pages - free) set_status(p.status, kDevBadMeta, 0xFFFF);  // more pages than there are
     } else {  // sums only grow, so from the first that does not fit on none does
       const bool fits = n == 0 || at + n <= free;
       places[b] = n == 0 ? 0 : fits ? static_cast<int>(at) : kShort;
@@ -183,10 +184,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) pages_kernel(const 
       if (p.granted) p.granted[b] = good ? r.count : 0;
     }
   }
-  if (blockIdx.x == 0 && tid == 0) {
-    if (RELEASE && used > p.num_pages - free) set_status(p.status, kDevBadMeta, 0xFFFF);  // more pages than there are
-    p.new_state[p.B] = make_int2(RELEASE ? min(free + used, p.num_pages) : free - used, 0);
-  }
+  if (blockIdx.x == 0 && tid == 0)
+    p.new_state[p.B] = make_int2(!RELEASE ? free - used : used > p.num_pages - free ? p.num_pages : free + used, 0);
 
   // pieces of sequences, one a warp, in turn
   const int step = gridDim.x * kWarps, step_b = step / pieces, step_piece = step - step_b * pieces;

@@ -134,3 +134,14 @@ def test_granted_out_of_range(B):
     for bad in ({"granted": lens}, {"cu_new": _ints([0, 2, 4, 6, 8]), "granted": lens[:3]}):
         with pytest.raises(ValueError):
             B.cm_kv_append(cache, table, lens, *((k, k) if "cu_new" in bad else (pad, pad)), **bad)
+def test_more_pages_come_back_than_there_are(B):
+    """Sequences whose states claim more pages than the pool has, from a list that is empty, partly full and full: what has
+    no room is dropped and reported, and the list never names more than there are."""
+    for left in (0, 2, 5):
+        x = Both(B, 5, 3, 8, 16)
+        x.table = [[0, 1, 2, 3, 4, 0, 1, 2], [3, 4, 0, 1, 2, 3, 4, 0], [1, 2, 3, 4, 0, 1, 2, 3]]
+        x.state = [[0, 8], [0, 8], [0, 8], [left, 0]]
+        x.gpu.page_table.copy_(_ints(x.table))
+        x.gpu.state.copy_(_ints(x.state))
+        x.release([0, 0, 0], [1, 0, 1], bad=True)
+        assert x.state[3] == [5, 0]
