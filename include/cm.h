@@ -490,7 +490,7 @@ CM_API int cm_kv_status(const cm_kv_cache* cache, void* stream);
  *   status         device int32: 0, or the first device error (cm_kv_pages_status)
  * State, device int32 [B + 1][2], 8-byte aligned: for sequence b the pages {lo, hi} that it owns, which are the entries
  * [0, f) and [max(lo, f), hi) of its row below hi, with f = ceil(sinks / page_size); in row B {free pages, 0}.  Both
- * calls read `state` and write all of `new_state` (other memory); the next call goes on from there, so the calls on one pool
+ * calls read `state` and write all of `new_state` (memory that is no part of what the call reads, as `granted`); the next call goes on from there, so the calls on one pool
  * run one after another (one stream, or ordered by events).  A new pool starts
  * with all pages in free_pages, {0, 0} for every sequence and {num_pages, 0}. */
 typedef struct cm_kv_pages {
@@ -503,7 +503,7 @@ typedef struct cm_kv_pages {
 /* Pages for the tokens that each sequence is about to append behind its lens[b], counted as in cm_kv_new
  * (cu_new, n_new, n_tokens, max_new): its row gets the pages it lacks, from the end of the list, in
  * the order of the sequences.  From the first sequence on for which too few are left, sequences that need a page get none.
- *   granted  device int32 [B] (may be NULL; not lens, not n_new): the tokens that may be appended, all of a
+ *   granted  device int32 [B] (may be NULL): the tokens that may be appended, all of a
  *            sequence's or 0.  A row that was granted nothing keeps its entries, which may name pages that are another
  *            sequence's by now, so an append that does not heed `granted` would write there.
  *   slots    device int64, [n_tokens] for packed tokens, [B][n_tokens] for padded ones (may be NULL): each new token's

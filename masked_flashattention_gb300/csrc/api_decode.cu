@@ -16,6 +16,12 @@ bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 bool good_ptr(const void* p) { return p && aligned(p, 16); }
 bool good_ints(const void* p) { return p && aligned(p, 4); }
 
+// Whether two ranges of memory share a byte.
+bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && (x < y ? y - x < static_cast<uintptr_t>(a_bytes) : x - y < static_cast<uintptr_t>(b_bytes));
+}
+
 int check_cache(const cm_kv_cache* c) {
   if (!c || c->num_pages < 1 || c->H_kv < 1) return CM_ERR_INVALID_ARG;
   if (c->dtype < CM_KV_BF16 || c->dtype > CM_KV_INT8_BLOCK) return CM_ERR_INVALID_ARG;
@@ -113,7 +119,9 @@ int check_pages(const cm_kv_pages* g, const int32_t* state, const int32_t* new_s
     return CM_ERR_UNSUPPORTED;
   if (!good_ints(g->page_table) || !good_ints(g->free_pages) || !good_ints(g->status) || !good_ints(lens))
     return CM_ERR_INVALID_ARG;
-  if (!state || !new_state || state == new_state || !aligned(state, 8) || !aligned(new_state, 8))
+  const int64_t rows = 4 * int64_t{g->B}, states = 8 * (int64_t{g->B} + 1);
+  if (!state || !new_state || !aligned(state, 8) || !aligned(new_state, 8) ||
+      overlap(new_state, states, state, states) || overlap(new_state, states, lens, rows))
     return CM_ERR_INVALID_ARG;
   p = {};
   p.page_table = g->page_table;
@@ -358,7 +366,12 @@ CM_API int cm_kv_reserve(const cm_kv_pages* pages, const int32_t* state, int32_t
   if (cu_new ? (n_new || !good_ints(cu_new)) : (n_new && !good_ints(n_new))) return CM_ERR_INVALID_ARG;
   if (!cu_new && !n_new && max_new != n_tokens) return CM_ERR_INVALID_ARG;
   if ((granted && !good_ints(granted)) || (slots && !aligned(slots, 8))) return CM_ERR_INVALID_ARG;
-  if (granted == lens || (granted && granted == n_new)) return CM_ERR_INVALID_ARG;
+  // every block reads what the sequences ask for, so no block's results may lie there
+  const int64_t rows = 4 * int64_t{p.B}, states = 8 * (int64_t{p.B} + 1);
+  if (overlap(granted, rows, lens, rows) || overlap(granted, rows, n_new, rows) || overlap(granted, rows, cu_new, rows + 4) ||
+      overlap(granted, rows, state, states) || overlap(granted, rows, new_state, states) ||
+      overlap(new_state, states, n_new, rows) || overlap(new_state, states, cu_new, rows + 4))
+    return CM_ERR_INVALID_ARG;
   if ((cu_new ? n_tokens : static_cast<int64_t>(p.B) * max_new) > (1LL << 30)) return CM_ERR_UNSUPPORTED;
   p.cu_new = cu_new;
   p.n_new = n_new;
@@ -374,7 +387,8 @@ CM_API int cm_kv_release(const cm_kv_pages* pages, const int32_t* state, int32_t
   cm::PagesParams p;
   const int rc = check_pages(pages, state, new_state, lens, p);
   if (rc != CM_OK) return rc;
-  if (done && !good_ints(done)) return CM_ERR_INVALID_ARG;
+  if ((done && !good_ints(done)) || overlap(new_state, 8 * (int64_t{p.B} + 1), done, 4 * int64_t{p.B}))
+    return CM_ERR_INVALID_ARG;
   p.done = done;
   return cm::launch_kv_release(p, static_cast<cudaStream_t>(stream)) == 0 ? CM_OK : CM_ERR_CUDA;
 }
