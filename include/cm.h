@@ -371,7 +371,8 @@ typedef struct cm_kv_seqs {
  *           rot_dim channels (a multiple of 16, at most d; 0: no rotation, rope NULL) are rotated
  *           in pairs (i, i + rot_dim / 2), or (2i, 2i + 1) if interleaved:
  *           (x, y) -> (x cos - y sin, y cos + x sin), every product and sum rounded to fp32 once.
- *   new_lens device int32 [B] (may be NULL, not lens, not granted): receives lens[b] + the tokens appended.
+ *   new_lens device int32 [B] (may be NULL; no part of lens, n_new, cu_new or granted): receives lens[b] + the tokens
+ *           appended.
  *   granted packed tokens only: device int32 [B] (may be NULL: all), the tokens that each sequence may append, as
  *           cm_kv_reserve gives them.  Sequence b appends the first granted[b] of its own, which must be 0 to all of them;
  *           the others count as tokens of no sequence.  (Padded tokens say the same by n_new.) */

@@ -228,11 +228,14 @@ CM_API int cm_kv_append(const cm_kv_cache* cache, const cm_kv_seqs* seqs, const 
   if (t->cu_new ? (t->n_new || !good_ints(t->cu_new)) : (t->n_new && !good_ints(t->n_new)))
     return CM_ERR_INVALID_ARG;
   if (!t->cu_new && !t->n_new && t->max_new != t->n_tokens) return CM_ERR_INVALID_ARG;
-  if (t->granted && (!t->cu_new || !good_ints(t->granted) || t->granted == t->new_lens)) return CM_ERR_INVALID_ARG;
+  if (t->granted && (!t->cu_new || !good_ints(t->granted))) return CM_ERR_INVALID_ARG;
   if (t->rot_dim < 0 || t->rot_dim > cache->d || t->rot_dim % 16 != 0) return CM_ERR_INVALID_ARG;
   if (t->rot_dim ? (!good_ptr(t->rope) || t->rope_len < 1) : t->rope != nullptr)
     return CM_ERR_INVALID_ARG;
-  if (t->new_lens && (!good_ints(t->new_lens) || t->new_lens == seqs->lens))
+  const int64_t rows = 4 * int64_t{seqs->B};  // one block writes the new lengths while others read these
+  if (t->new_lens && (!good_ints(t->new_lens) || overlap(t->new_lens, rows, seqs->lens, rows) ||
+                      overlap(t->new_lens, rows, t->n_new, rows) || overlap(t->new_lens, rows, t->cu_new, rows + 4) ||
+                      overlap(t->new_lens, rows, t->granted, rows)))
     return CM_ERR_INVALID_ARG;
   if ((t->cu_new ? t->n_tokens : static_cast<int64_t>(seqs->B) * t->max_new) > (1LL << 30))
     return CM_ERR_UNSUPPORTED;

@@ -42,3 +42,19 @@ def test_results_that_lie_in_what_is_read(B):
         assert reserve(**bad) == B.CM_ERR_INVALID_ARG, bad
     for a, b, done in ((state, state - 24, None), (state, lens - 24, None), (state, n_new + 8, n_new), (state, n_new - 24, n_new)):
         assert L.cm_kv_release(_pages(B), a, b, lens, done, None) == B.CM_ERR_INVALID_ARG, (a, b, done)
+
+
+def test_new_lengths_that_lie_in_what_an_append_reads(B):
+    """Two sequences: lens at A16 + 4 (8 bytes)."""
+    def append(**k):  # more tokens than a call takes: refused as unsupported where nothing else is wrong
+        n = 2**31 - 1 if "cu_new" in k else 1 << 30
+        return B.lib().cm_kv_append(_cache(B), _seqs(B), _new(B, n_tokens=n, max_new=n, **k), None)
+
+    far = 8 * A16
+    for good in ({}, {"new_lens": A16 + 12}, {"new_lens": A16 - 4}, {"new_lens": far, "n_new": far + 8},
+                 {"new_lens": far, "cu_new": far - 12}, {"new_lens": far, "cu_new": far + 8, "granted": far - 8}):
+        assert append(**good) == B.CM_ERR_UNSUPPORTED, good
+    for bad in ({"new_lens": A16 + 4}, {"new_lens": A16 + 8}, {"new_lens": A16}, {"new_lens": far, "n_new": far},
+                {"new_lens": far, "n_new": far + 4}, {"new_lens": far, "cu_new": far}, {"new_lens": far, "cu_new": far - 8},
+                {"new_lens": far, "cu_new": 9 * A16, "granted": far + 4}):
+        assert append(**bad) == B.CM_ERR_INVALID_ARG, bad
