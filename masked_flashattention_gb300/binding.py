@@ -751,8 +751,8 @@ def cm_attn_decode(cache: KVCache, page_table, lens, q, o, lse, workspace: torch
     if window is not None:
         if desc is not None or sel is not None:
             raise ValueError("a window comes without desc and without sel")
-        if window >= 1 << 31 or sinks >= 1 << 31:  # ctypes would take them modulo 2^32
-            raise ValueError("window and sinks must be below 2^31")
+        if not (-1 << 31 <= window < 1 << 31 and -1 << 31 <= sinks < 1 << 31):  # ctypes would take them modulo 2^32
+            raise ValueError("window and sinks must be at least 0 and below 2^31")
         rc = _serving()[3](cache._address, seqs, window, sinks, q.data_ptr(), qs, o.data_ptr(), os,
                            _ptr(lse), H, scale, workspace.data_ptr(), workspace.nbytes,
                            _kv_stream(cache, stream))
@@ -824,6 +824,8 @@ class KVPages:
         self.page_table, self.free_pages = page_table, free_pages
         self.page_size, self.window, self.sinks = page_size, window, sinks
         self.num_pages = free_pages.shape[0]
+        if not all(0 <= x < 1 << 31 for x in (self.num_pages, page_size, self.B, self.max_pages)):
+            raise ValueError("pages, page_size and sequences must be below 2^31")
         self.state = self.spare = None
         if state is not None:
             _kv_tensor(state, "state", _I32, (self.B + 1, 2), self.index)

@@ -1,0 +1,32 @@
+"""Windows where a call's numbers are at their ends."""
+import math
+
+import pytest
+import torch
+
+from tests.test_kv_cache_gpu import _check_decode, _filled
+from tests.test_window_gpu import _visible
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def B():
+    from masked_flashattention_gb300 import binding
+    binding.lib()
+    return binding
+
+
+def test_numbers_beyond_32_bits_are_refused(B):
+    """None is taken modulo 2^32: -(2^32) + 4 is no window of 4."""
+    gen = torch.Generator().manual_seed(56)
+    cache, table, n = _filled(B, [40], 1, 16, 64, "bf16", gen)
+    q = torch.zeros(1, 1, 64, dtype=torch.bfloat16, device="cuda")
+    for bad in ({"window": -2**32 + 4}, {"window": -2**31 - 1}, {"window": 2**31}, {"window": 4, "sinks": -2**32},
+                {"window": 4, "sinks": -2**32 + 3}, {"window": 4, "sinks": 2**32}):
+        with pytest.raises(ValueError):
+            B.decode_attention(cache, table, n, q, **bad)
+    t = torch.zeros(2, 4, dtype=torch.int32, device="cuda")
+    for bad in (2**32 + 16, -2**32 + 16):
+        with pytest.raises(ValueError):
+            B.KVPages(t, t[0], bad)
