@@ -806,7 +806,8 @@ def cm_kv_status(cache: KVCache, stream=None) -> int:
 
 class KVPages:
     """The pages of a pool and their tables (cm_kv_pages) over the caller's tensors: page_table int32
-    [B, max_pages], free_pages int32 [num_pages].  window (None or 0: none) and sinks as in cm_attn_decode.  state and
+    [B, max_pages], free_pages int32 [num_pages].  window (None or 0: none) and sinks as in cm_attn_decode; the attributes
+    are what that takes, None and 0 where the pool has no window.  state and
     spare, int32 [B + 1, 2], are what reserve_pages and release_pages go on from and write to; alloc makes
     them, the low-level calls take their own."""
 
@@ -822,7 +823,7 @@ class KVPages:
         if not (0 <= window < 1 << 31 and 0 <= sinks < 1 << 31):
             raise ValueError("window and sinks must be at least 0 and below 2^31")
         self.page_table, self.free_pages = page_table, free_pages
-        self.page_size, self.window, self.sinks = page_size, window, sinks
+        self.page_size, self.window, self.sinks = page_size, window or None, sinks if window else 0
         self.num_pages = free_pages.shape[0]
         if not all(0 <= x < 1 << 31 for x in (self.num_pages, page_size, self.B, self.max_pages)):
             raise ValueError("pages, page_size and sequences must be below 2^31")
