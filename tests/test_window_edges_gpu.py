@@ -42,3 +42,25 @@ def test_attention_takes_the_window_of_a_pool(B, window, sinks):
     q = torch.randn(3, 2, 64, generator=gen).to(torch.bfloat16).cuda()
     o, lse = B.decode_attention(cache, table, n, q, window=pages.window, sinks=pages.sinks)
     _check_decode(cache, table, n, q, o, lse, 1 / 8, lambda b, g: _visible(lens[b], window or 10**9, sinks))
+
+
+def test_the_work_of_a_call_goes_by_its_window(B):
+    """64 sequences of 8 heads with tables for 2^27 tokens each, 2^22 tiles, are more than a call takes; under a window it is
+    what the window can cover that counts, to the tile: 512 rows * (tiles + 1 + 2) below 2^31 - 320."""
+    gen = torch.Generator().manual_seed(58)
+    lens = [0] * 64
+    lens[0], lens[7], lens[63] = 300, 1, 129
+    P, H, d = 128, 8, 64
+    cache, narrow, n = _filled(B, lens, H, P, d, "bf16", gen)
+    table = torch.full((64, (1 << 27) // P), -7, dtype=torch.int32, device="cuda")
+    table[:, :narrow.shape[1]] = narrow
+    q = torch.randn(64, H, d, generator=gen).to(torch.bfloat16).cuda()
+    most = 32 * (2**22 - 4)
+    for more in ({}, {"window": most + 1}, {"window": most - 32, "sinks": 33}, {"window": 2**31 - 1}):
+        with pytest.raises(B.CMError) as e:
+            B.decode_attention(cache, table, n, q, **more)
+        assert e.value.code == B.CM_ERR_UNSUPPORTED
+    for more in ({"window": most}, {"window": most - 32, "sinks": 32}, {"window": 100, "sinks": 3}):
+        o, lse = B.decode_attention(cache, table, n, q, **more)
+        assert B.cm_kv_status(cache) == B.CM_OK
+        _check_decode(cache, table, n, q, o, lse, 1 / 8, lambda b, g: _visible(lens[b], more["window"], more.get("sinks", 0)))
