@@ -25,6 +25,30 @@ def _stored(pool, x):
     pool.view(torch.uint8).copy_(x.to(pool.dtype).view(torch.uint8).expand(pool.shape))
 
 
+def check_far(kind, cache, table, q, o, lse, scale, visible):
+    """_check where scores span 2^30 and more, so that most weights are far below the largest.  Beside 2^-11 of itself a weight
+    (with its value's scale) is off by half of fp16's smallest number, 2^-25; the row's largest is 2^7 at least, so by 2^-32 of
+    that, times a stored number of at most 127 or 448, for each of n keys."""
+    k, v, ks, vs, host, q = (x.cpu() for x in (cache.k, cache.v, cache.k_scale, cache.v_scale, table, q))
+    o, lse, d, P, group = o.double().cpu(), lse.double().cpu(), cache.d, cache.page_size, q.shape[1] // cache.H_kv
+    for b in range(q.shape[0]):
+        for g in range(cache.H_kv):
+            pos, hs = visible(b, g), slice(group * g, group * (g + 1))
+            if len(pos) == 0:
+                assert not o[b, hs].any() and (lse[b, hs] == -math.inf).all(), (b, g)
+                continue
+            kk, vv = K.block_rows(k, ks, host[b], g, pos), K.block_rows(v, vs, host[b], g, pos)
+            want, wl, size, mag = K.decode(q[b, hs], kk, vv, scale)
+            ds = (d + 8) * 2 * F32_HALF * size + 128 * F32_HALF
+            sums = len(pos) / 8 * 2 * F32_HALF + 2.0 ** -18
+            assert ((lse[b, hs] - wl).abs() <= ds + sums + 2.0 ** -20 * (1 + wl.abs())).all(), (b, g)
+            p = torch.exp(scale * q[b, hs].to(F64) @ kk.T - wl[:, None])
+            by = vs[host[b, pos // P].long(), g, pos % P // 16].to(F64)
+            lost = 2.0 ** -32 * (p * by).amax(1, keepdim=True) * (127 if kind == "int8" else 448) * len(pos)
+            bound = BF16_HALF * want.abs() + (2.0 ** -11 + 2 * ds + sums) * mag + lost
+            assert ((o[b, hs] - want).abs() <= bound).all(), (b, g, ((o[b, hs] - want).abs() / bound).max())
+
+
 def _one_sign(shape, gen):
     """Sizes spread over 2^-12 .. 2^6, so that sums of them do not come out even."""
     return (2.0 ** (18 * torch.rand(shape, generator=gen) - 12)).to(torch.bfloat16).cuda()
@@ -56,24 +80,8 @@ def test_small_numbers_beside_queries_of_one_sign(B, kind, d, P, group):
     cache.k.view(torch.uint8).copy_(small.to(cache.k.dtype).view(torch.uint8))
     cache.k_scale.copy_(torch.where(cache.k_scale.isnan(), cache.k_scale, 4.0))
     q = _one_sign((3, H * group, d), gen)
-    o, lse = (x.double().cpu() for x in B.decode_attention(cache, table, n, q))
-    k, v, ks, vs, host = (x.cpu() for x in (cache.k, cache.v, cache.k_scale, cache.v_scale, table))
-    for b in range(3):
-        for g in range(H):
-            pos, hs = torch.arange(lens[b]), slice(group * g, group * (g + 1))
-            kk, vv = K.block_rows(k, ks, host[b], g, pos), K.block_rows(v, vs, host[b], g, pos)
-            want, wl, size, mag = K.decode(q[b, hs].cpu(), kk, vv, d ** -0.5)
-            ds = (d + 8) * 2 * F32_HALF * size + 128 * F32_HALF
-            sums = lens[b] / 8 * 2 * F32_HALF + 2.0 ** -18
-            assert ((lse[b, hs] - wl).abs() <= ds + sums + 2.0 ** -20 * (1 + wl.abs())).all(), (b, g)
-            # Scores span 2^100 and more here.  Beside 2^-11 of itself a weight (with its value's scale) is off by half of fp16's
-            # smallest number, 2^-25; the row's largest is 2^7 at least, so by 2^-32 of that, times a stored number of at most 127
-            # or 448, for each of n keys.
-            p = torch.exp(d ** -0.5 * q[b, hs].cpu().to(F64) @ kk.T - wl[:, None])
-            scale = vs[host[b, pos // P].long(), g, pos % P // 16].to(F64)
-            lost = 2.0 ** -32 * (p * scale).amax(1, keepdim=True) * (127 if kind == "int8" else 448) * lens[b]
-            bound = BF16_HALF * want.abs() + (2.0 ** -11 + 2 * ds + sums) * mag + lost
-            assert ((o[b, hs] - want).abs() <= bound).all(), (b, g, ((o[b, hs] - want).abs() / bound).max())
+    o, lse = B.decode_attention(cache, table, n, q)
+    check_far(kind, cache, table, q, o, lse, 1 / math.sqrt(d), lambda b, g: torch.arange(lens[b]))
 
 
 @pytest.mark.parametrize("kind,d,P,group", [("e4m3", 64, 16, 3), ("e4m3", 128, 64, 8), ("e4m3", 64, 32, 16), ("int8", 64, 16, 3), ("int8", 128, 128, 8)])
