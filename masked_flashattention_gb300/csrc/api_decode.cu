@@ -311,7 +311,6 @@ CM_API int cm_attn_decode_window(const cm_kv_cache* cache, const cm_kv_seqs* seq
   if (window < 1 || sinks < 0) return CM_ERR_INVALID_ARG;
   p.window = window;
   p.sinks = sinks;
-  p.NI = 2;
   return launch_decode(p, stream);
 }
 

@@ -55,7 +55,7 @@ int launch_kv_append(const AppendParams& p, cudaStream_t stream);
 struct DecodeParams {
   KvView c;
   const int32_t* itab;  // forward Interval Table [B][NI][S][2], or nullptr
-  int NI, S;            // intervals of a row (2 under a window)
+  int NI, S;            // intervals of a row
   int window, sinks;    // the last `window` and the first `sinks` keys are visible; window 0: no window
   const int32_t* sel;   // [B][H_kv][sel_max] with nsel [B][H_kv], or nullptr
   const int32_t* nsel;
