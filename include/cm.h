@@ -418,9 +418,9 @@ CM_API int cm_attn_decode_workspace_size(int B, int H_q, int H_kv, int d, size_t
 /* Attention of one new token per sequence, the last of its lens[b] tokens:
  * o[b][h] = softmax_j(scale * q[b][h] . k[j]) v[j] over the visible j < lens[b], of key-value head
  * h / (H_q / H_kv).  q, o: bf16 [B][H_q][d] with strides in elements for {sequence, head}, multiples
- * of 8; lse: fp32 [B][H_q] in natural log, or NULL.  H_q is a multiple of H_kv.  (Beside an e4m3 cache,
+ * of 8; lse: fp32 [B][H_q] in natural log, or NULL.  H_q is a multiple of H_kv.  (Beside an 8-bit cache,
  * channels of q below 2^-31 of their head's largest lose bits; beside block types all do, where the head's largest times
- * scale passes 2^80.)  o may be q with the same strides; otherwise
+ * scale passes 2^108.)  o may be q with the same strides; otherwise
  * outputs overlap nothing else, nor themselves (o_stride at least d).
  *   desc  NULL: every token is visible.  Else a descriptor of B samples with S >= lens[b] in the
  *         CM_FORM_VISIBLE form: the token sees what row lens[b] - 1 of the forward half says, cut

@@ -30,16 +30,16 @@
 // that of the stored numbers and the running maximum bounds it however far scales lie apart; the sum of the weights
 // takes it off again.  Neither is an instruction more a score than one scale a head takes.
 // Under a sliding window a row's tiles are those of the first keys and of the last (WINDOW, kernels of their own: as a
-// further case of the mask's intervals they took 46.9 us instead of 45.6 in the case below, and the calls without one slowed by 1 to 3 %).
+// further case of the mask's intervals the case below took 46.9 us where it then took 45.6, and the calls without one slowed by 1 to 3 %).
 //
-// Measured (8 key-value heads of 128, 4 query heads each, bf16): 64 sequences of up to 16384 keys, 331 us =
-// 7.0 TB/s, 103 % of the copy bandwidth; one of 131071, 84 us = 6.4 TB/s; 200 of up to 333, 17.3 us.  What
+// Measured (8 key-value heads of 128, 4 query heads each, bf16): 64 sequences of up to 16384 keys, 332 us =
+// 6.9 TB/s, 102 % of the copy bandwidth; one of 131071, 85 us = 6.3 TB/s; 200 of up to 333, 17.6 us.  What
 // stands above the bytes is the start, 4 us from the launch to the first tile on its way (length, place, page
 // number: one load behind another) and up to 4 more until the memory's address translations are warm, and the end,
 // 4 to 5 us where rows are split (join, launch, join).  One CTA a head took 52 ms for the one of 131071.
-// With block scales: the 64 sequences, int8, 177 us = 6.5 TB/s, 96 %; the one of 131071, e4m3, 49.5 us; 40 of up to 32768
+// With block scales: the 64 sequences, int8, 180 us = 6.4 TB/s, 94 %; the one of 131071, e4m3, 50 us; 40 of up to 32768
 // with 16 heads a group, int8, 70 us (67 with one scale a head, e4m3: the widening of the bytes holds both).  Windows: 256 sequences
-// under 1024 keys and 16 sinks, int8, 43.8 us = 4.4 TB/s (start, row ends and join); one of 100,003 under 4096, bf16, 8.9 us.
+// under 1024 keys and 16 sinks, int8, 44.5 us = 4.3 TB/s (start, row ends and join); one of 100,003 under 4096, bf16, 9.1 us.
 #pragma once
 #include <cuda_fp16.h>
 #include <atomic>

@@ -16,8 +16,9 @@
 // Measured: 42,000 new tokens of 9 sequences, 32 query and 8 key-value heads of 128, with summaries, 156 us =
 // 6.7 TB/s, 99 % of the copy bandwidth (428 us with one unit a warp of 16 rows in registers, 265 with
 // the heads' loads in registers, which held a quarter of the warps, 183 with neighbouring pieces a lane); one token
-// of 256 sequences, e4m3, 9.3 us.  int8 with block scales, no summaries: 164 us = 5.9 TB/s (the rows of keys and values alone
-// 3.9 TB/s: they are gone through twice, and a rotation's row is read again by every head); 9.3 us.
+// of 256 sequences, e4m3, 9.2 us.  int8 with block scales, no summaries: 164 us = 5.9 TB/s (the rows of keys and values alone
+// 3.9 TB/s: they are gone through twice, and a rotation's row is read again by every head);
+// one token of 256 sequences, e4m3 with block scales and summaries, 9.5 us.
 //
 // Numerics: the rotation is fp32 with every product and sum rounded once (no fused
 // multiply-add), so that it equals the formula evaluated step by step; one rounding to bf16, and
@@ -806,7 +807,8 @@ __global__ void __launch_bounds__(kThreads, 4)
 bool has_scaled_blocks(const AppendParams& p) { return p.c.kind >= kE4m3Block; }
 bool goes_by_page(const AppendParams& p) { return p.max_new > 0 && (p.c.summary || has_scaled_blocks(p)); }
 // Blocks with scales: four a warp, within a page, where every warp of the GPU then still has some (the next block's
-// pieces are on their way while one is stored; 42,000 tokens took 197 us with one a warp, 186 with four).
+// pieces are on their way while one is stored; 42,000 tokens took 197 us with one a warp, 186 with four, before the
+// lanes' pieces lay as they do).
 int log2_unit(const AppendParams& p) {
   if (p.c.summary) return p.c.log2_page;
   const int64_t tokens = p.cu_new ? p.n_tokens : static_cast<int64_t>(p.c.B) * p.max_new;

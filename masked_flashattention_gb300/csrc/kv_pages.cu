@@ -9,8 +9,8 @@
 // output state are separate memory, so no block's reading meets another's writing.  Prefix sums make
 // the result the same as that of a loop over the sequences; there are no atomics but the status word's and the block's own.
 // Measured: a step of 256 sequences 2.8 us (reserve) and 3.2 (release), of which a launch is 2.2; 500 prompts, 483,000
-// slots, 9.3 us (9.7 and 14.3 with pieces of 512 and 2048 slots); 2000 sequences that end with 1.28 million pages
-// 6.7 us.  With blocks of 512 threads and 64-bit sums: 3.5, 3.4, 12.4 and 10.1 us.
+// slots, 9.2 us (9.7 and 14.3 with pieces of 512 and 2048 slots); 2000 sequences that end with 1.28 million pages
+// 6.8 us.  With blocks of 512 threads and 64-bit sums: 3.5, 3.4, 12.4 and 10.1 us.
 #include <cstdint>
 
 #include "kv_cache.h"
@@ -281,8 +281,9 @@ int launch(const PagesParams& p, int pieces, cudaStream_t stream) {
 }
 
 // Every block adds up all sequences, so blocks are as large as they can be where there is work for all SMs (2000 sequences
-// of 20000 tokens that end, pages of 16: 6.6 us, 12.7 with 256 threads); where a step has few pieces, barriers of
-// small blocks cost less (256 sequences, one token each: 3.1 us, 3.9 with 1024 threads).
+// of 20000 tokens that end, pages of 16: 6.8 us, 12.7 with 256 threads); where a step has few pieces, barriers of
+// small blocks cost less (256 sequences, one token each, before table and slots were written in one pass: 3.1 us, 3.9 with 1024
+// threads).
 template <bool RELEASE>
 int launch(const PagesParams& p, int pieces, cudaStream_t stream) {
   if (static_cast<int64_t>(p.B) * p.max_pages >= (1LL << 31)) return launch<RELEASE, int64_t, 1024>(p, pieces, stream);
